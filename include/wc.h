@@ -307,6 +307,119 @@ int wc_decode_u8_async(const wc_plan_t* plan, const void* blob_dev, uint8_t* out
 int wc_gemv_bf16_async(const uint16_t* W, uint32_t rows, uint32_t cols, const uint16_t* x, float* y,
                        void* stream);
 
+/*
+ * Limits of the operators below: rows of a 4-bit matrix or entries of a
+ * vocabulary, columns (always a positive multiple of 8), tokens of one call.
+ */
+#define WC_MAX_VOCAB  (1u << 22)
+#define WC_MAX_DIM    (1u << 16)
+#define WC_MAX_TOKENS (1u << 20)
+
+/*
+ * A matrix of 4-bit codes with group scales in device memory, the integer
+ * codes of a quantized model (the LazyWeights page's setting) as
+ * wc_decode_u8_async leaves an int4 plane:
+ *   w[r][c] = scales[r][c / group] * (code[r][c] - zeros[r][c / group]).
+ */
+typedef struct {
+    const uint8_t* codes;    /* rows x cols / 2 bytes, row-major: code c of a row in byte   */
+                             /* c / 2, even c in the low nibble; 16-byte aligned            */
+    const uint16_t* scales;  /* rows x ceil(cols / group) bf16, finite, 2-byte aligned      */
+    const uint8_t* zeros;    /* rows x ceil(cols / group) zero points, or NULL: 8 everywhere */
+    uint32_t rows;           /* at most WC_MAX_VOCAB                                        */
+    uint32_t cols;           /* a multiple of 8, at most WC_MAX_DIM                         */
+    uint32_t group;          /* columns per scale, a multiple of 32 (the last group of a    */
+                             /* row may be shorter; >= cols: one scale per row)             */
+} wc_q4_matrix;
+
+/* wc_q4_check -- WC_OK if sizes and alignment are as above, else
+ * WC_ERR_INVALID_ARG.  rows == 0 is valid (pointers are not looked at). */
+int wc_q4_check(const wc_q4_matrix* W);
+
+/*
+ * wc_gemv_q4_async -- y[t] = W x[t] for n_vecs vectors: one token, or the few
+ * that are verified at once (LazyWeights review: prompt lookup).  One launch.
+ *   x   device, n_vecs x cols bf16, 16-byte aligned;
+ *   y   device, n_vecs x rows float32 (written), 4-byte aligned.
+ * n_vecs is at most WC_GEMV_Q4_MAX_VECS.  Sums are held in fp32 or exact
+ * integers and taken in a fixed order: y is a deterministic function of the
+ * bits of W and x.  rows == 0 or n_vecs == 0 is a no-op.  WC_ERR_INVALID_ARG
+ * for bad sizes or alignment, WC_ERR_HIP if the launch fails.
+ */
+#define WC_GEMV_Q4_MAX_VECS 16u
+int wc_gemv_q4_async(const wc_q4_matrix* W, const uint16_t* x, uint32_t n_vecs, float* y, void* stream);
+
+/*
+ * wc_embed_async, wc_embed_q4_async -- out[t] = scale * table[id[t]], rounded
+ * once to bf16 (scale 1 on a bf16 table copies the words' bits).  One launch.
+ *   table     device, vocab x dim bf16, 16-byte aligned, dim a multiple of 8
+ *             (a tensor of wc_decode_async's output qualifies when its element
+ *             offset is a multiple of 8); or a 4-bit matrix of vocab rows;
+ *   ids       device, n token ids of id_bytes (4: int32, 8: int64) each;
+ *   out       device, n x dim bf16 (written), 16-byte aligned.
+ * An id outside [0, vocab) marks padding: its row of out is zero.  n == 0 is a
+ * no-op; n is at most WC_MAX_TOKENS.
+ */
+int wc_embed_async(const uint16_t* table, uint32_t vocab, uint32_t dim, const void* ids, uint32_t id_bytes,
+                   uint64_t n, float scale, uint16_t* out, void* stream);
+int wc_embed_q4_async(const wc_q4_matrix* W, const void* ids, uint32_t id_bytes, uint64_t n, float scale,
+                      uint16_t* out, void* stream);
+
+/*
+ * wc_embed_grad_async -- the table's gradient: dtable[v] = scale * (sum over
+ * the t with id[t] = v of dout[t]), summed in fp32 in token order, the same
+ * bits on every run.
+ *   dout      device, n x dim bf16, 16-byte aligned;
+ *   dtable    device, vocab x dim, 16-byte aligned: float32 (out_kind
+ *             WC_OUT_F32) or bf16 (WC_OUT_BF16);
+ *   accumulate  0: every row is written, zeros where no token has it; else the
+ *             sums are added to dtable (rounded once) and other rows are left
+ *             as they are: the gradient of a table that is also the output
+ *             matrix goes on top of wc_ce_grad_async's dW this way;
+ *   work_dev  device scratch of at least wc_embed_grad_work_bytes(n, dim)
+ *             bytes, 256-byte aligned, overwritten; calls that may overlap
+ *             need one each.
+ * Ids outside [0, vocab) give nothing.  At most four launches.
+ */
+#define WC_OUT_F32  0u
+#define WC_OUT_BF16 1u
+int wc_embed_grad_work_bytes(uint64_t n, uint32_t dim, uint64_t* work_bytes);
+int wc_embed_grad_async(const uint16_t* dout, const void* ids, uint32_t id_bytes, uint64_t n, float scale,
+                        void* dtable, uint32_t out_kind, uint32_t vocab, uint32_t dim, int accumulate,
+                        void* work_dev, uint64_t work_bytes, void* stream);
+
+/*
+ * Softmax cross entropy of the vocabulary product z[t][v] = h[t] . W[v],
+ * without keeping z (perplexity of decoded weights; a training step's loss):
+ *   lse[t]  = log sum_v exp(z[t][v]),   loss[t] = lse[t] - z[t][target[t]],
+ *   d[t][v] = (exp(z[t][v] - lse[t]) - [v = target[t]]) * dloss[t],
+ *   dh = d W,   dW = d^T h.
+ *   h        device, tokens x dim bf16;  W device, vocab x dim bf16; both
+ *            16-byte aligned, dim a multiple of 8;
+ *   targets  device, tokens ids of target_bytes (4: int32, 8: int64); one
+ *            outside [0, vocab) marks a token without a loss (loss 0, no
+ *            gradient whatever dloss holds there; its lse is still written);
+ *   loss, lse  device, tokens float32 (written);
+ *   dloss    device, tokens float32: the gradient of each token's loss;
+ *   dh, dW   device, bf16 as h and W (written), or NULL where not wanted
+ *            (not both);
+ *   work_dev device scratch, 256-byte aligned, of at least
+ *            wc_ce_work_bytes(tokens, vocab, dim, grad) bytes (grad 0: enough
+ *            for the loss; else for both calls), overwritten; calls that may
+ *            overlap need one each.
+ * z is accumulated in fp32; the gradient keeps a piece of the vocabulary's d
+ * at a time, in bf16.  Results are the same bits on every run.  tokens == 0
+ * is a no-op, but for dW, which is then zero.  The gradient takes the lse
+ * that the loss call wrote.
+ */
+int wc_ce_work_bytes(uint64_t tokens, uint32_t vocab, uint32_t dim, int grad, uint64_t* work_bytes);
+int wc_ce_loss_async(const uint16_t* h, const uint16_t* W, const void* targets, uint32_t target_bytes,
+                     uint64_t tokens, uint32_t vocab, uint32_t dim, float* loss, float* lse, void* work_dev,
+                     uint64_t work_bytes, void* stream);
+int wc_ce_grad_async(const uint16_t* h, const uint16_t* W, const void* targets, uint32_t target_bytes,
+                     uint64_t tokens, uint32_t vocab, uint32_t dim, const float* lse, const float* dloss,
+                     uint16_t* dh, uint16_t* dW, void* work_dev, uint64_t work_bytes, void* stream);
+
 /* ---- debug status ---------------------------------------------------------- */
 /*
  * wc_plan_debug_status -- a plan made with WC_DEBUG=1 in the environment

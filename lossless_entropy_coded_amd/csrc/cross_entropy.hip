@@ -1,0 +1,527 @@
+// cross_entropy.hip -- softmax cross entropy of the vocabulary product, and
+// its gradients, without keeping the logits.
+//
+// With h (tokens x dim) and W (vocab x dim) in bf16, z[t][v] = h[t] . W[v]:
+//   lse[t]  = log sum_v exp(z[t][v]),   loss[t] = lse[t] - z[t][target[t]],
+//   d[t][v] = (exp(z[t][v] - lse[t]) - [v = target[t]]) dloss[t],
+//   dh = d W,   dW = d^T h.
+// A target outside [0, vocab) marks a token without a loss: its loss, and its
+// rows of d, are zero.
+//
+// The loss takes one matrix product whose tiles never leave the chip: each
+// workgroup computes a tile of z in fp32 accumulators and leaves, per token,
+// the tile's maximum and its sum of exp(z - maximum); a second kernel joins a
+// token's tiles in tile order.  The gradient computes z again, a piece of the
+// vocabulary at a time, and keeps that piece's d in bf16 (the matrix cores'
+// input type: a relative rounding of at most 2^-8 per value, as dh and dW
+// themselves are rounded) for the two products that read it.  The rounding of
+// the target's own value, by far the largest of a row, is kept per token in
+// fp32 and its product with W[target] is added to dh.
+//
+// The three products run on one tile routine, out[n][m] = sum_k A(m, k) B(n, k),
+// m being the contiguous index of the output: a 32 x 32 accumulator block holds
+// 4 consecutive m of one n per lane, so the loss reduces over the vocabulary
+// (m) mostly inside a lane and every store is of 4 neighbours.  An operand is
+// stored with k contiguous, or with m (n) contiguous (then its fragments are
+// read with the transposing LDS load), so nothing is transposed in memory.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/wc.h"
+
+namespace wc {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr uint32_t kBk = 64;              // k per LDS stage
+constexpr uint32_t kNoChunk = 0xFFFFFFF0u;   // a buffer offset beyond every operand: loads zeros
+
+__device__ __forceinline__ float bf16_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+
+// Round to nearest even; a NaN stays a NaN.
+__device__ __forceinline__ uint16_t f32_bf16(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+
+// One operand: element (x, k) is p[x * ld + k], or p[k * ld + x] when stored
+// with x contiguous; x < rows, k < depth, everything else reads as zero.  ld
+// and the contiguous extent are multiples of 8.
+struct Operand {
+    const uint16_t* p;
+    uint64_t ld;
+    uint32_t rows;
+    uint32_t depth;
+};
+
+// LDS image of R x kBk elements in 16-byte chunks.  k contiguous: row x has 8
+// chunks, chunk c at place c ^ (x & 7), so that the 8 rows that one pass of a
+// 16-byte read touches lie in different banks.  x contiguous: row k has R / 8
+// chunks, chunk c at place c ^ ((k & 3) << 2): the 4 rows of k that a
+// transposing read touches lie 64 bytes apart.
+template <bool kXContig, uint32_t R, uint32_t kThreads>
+__device__ __forceinline__ void load_stage(uint16_t* lds, const Operand& o, uint32_t x0, uint32_t k0) {
+    constexpr uint32_t kChunks = R * kBk / 8;
+    static_assert(kChunks % kThreads == 0, "whole rounds");
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint16_t* base;
+    uint32_t bytes;
+    if (kXContig) {
+        const uint32_t left = o.depth > k0 ? o.depth - k0 : 0;
+        base = o.p + (uint64_t)k0 * o.ld;
+        bytes = (uint32_t)((left < kBk ? left : kBk) * o.ld * 2);
+    } else {
+        const uint32_t left = o.rows > x0 ? o.rows - x0 : 0;
+        base = o.p + (uint64_t)x0 * o.ld;
+        bytes = (uint32_t)((left < R ? left : R) * o.ld * 2);
+    }
+    const __amdgpu_buffer_rsrc_t rsrc =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), 0, (int)bytes, 0x00027000);
+#pragma unroll
+    for (uint32_t i = 0; i < kChunks / kThreads; ++i) {
+        const uint32_t q = i * kThreads + threadIdx.x;
+        uint32_t off;
+        if (kXContig) {
+            const uint32_t k = q / (R / 8), c = (q % (R / 8)) ^ ((k & 3u) << 2);
+            off = x0 + c * 8 < o.rows ? (uint32_t)((k * o.ld + x0 + c * 8) * 2) : kNoChunk;
+        } else {
+            const uint32_t x = q / 8, c = (q % 8) ^ (x & 7u);
+            off = k0 + c * 8 < o.depth ? (uint32_t)((x * o.ld + k0 + c * 8) * 2) : kNoChunk;
+        }
+        uint16_t* dst = lds + (i * kThreads + wave * 64u) * 8u;   // a wave's 64 chunks are consecutive
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)dst, 16, off, 0, 0, 0);
+    }
+}
+
+// The fragment of rows x .. x + 31, k .. k + 15 of a stage: lane l holds row
+// x + l % 32, k + 8 (l / 32) .. + 7.
+template <bool kXContig, uint32_t R>
+__device__ __forceinline__ bf16x8 fragment(const uint16_t* lds, uint32_t x, uint32_t k) {
+    const uint32_t lane = threadIdx.x & 63u;
+    if (!kXContig) {
+        const uint32_t row = x + (lane & 31u), c = (k / 8 + (lane >> 5)) ^ (row & 7u);
+        return *reinterpret_cast<const bf16x8*>(lds + row * kBk + c * 8);
+    }
+    // 16 lanes read a block of 4 k by 16 x (lane i: row k + i / 4, x + 4 (i % 4)) and receive it transposed
+    // (lane i: x + i, 4 values of k)
+    const uint32_t i = lane & 15u, xb = x + ((lane >> 4) & 1u) * 16u + (i & 3u) * 4u;
+    const uint32_t kr = k + (lane >> 5) * 8u + (i >> 2);
+    const uint32_t at = kr * R + (((xb / 8) ^ ((kr & 3u) << 2)) * 8) + (xb & 7u);
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + at));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + at + 4 * R));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// A workgroup's tile: kBm x kBn outputs over kWavesM x kWavesN waves.
+template <bool kAx, bool kBx, uint32_t kBm_, uint32_t kBn_, uint32_t kWavesM_, uint32_t kWavesN_>
+struct Tile {
+    static constexpr uint32_t kBm = kBm_, kBn = kBn_, kWavesM = kWavesM_, kWavesN = kWavesN_;
+    static constexpr uint32_t kThreads = 64 * kWavesM * kWavesN;
+    static constexpr uint32_t kMi = kBm / kWavesM / 32, kNi = kBn / kWavesN / 32;
+    static constexpr uint32_t kLdsElems = (kBm + kBn) * kBk;
+
+    // acc = sum over k in [k_begin, k_end) of A(m0 + ., k) B(n0 + ., k); k_begin is a multiple of kBk
+    __device__ static __forceinline__ void product(uint16_t* lds, const Operand& A, const Operand& B, uint32_t m0,
+                                                   uint32_t n0, uint32_t k_begin, uint32_t k_end,
+                                                   f32x16 (&acc)[kMi][kNi]) {
+        const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const uint32_t wm = wave % kWavesM * (kBm / kWavesM), wn = wave / kWavesM * (kBn / kWavesN);
+        uint16_t* const la = lds;
+        uint16_t* const lb = lds + kBm * kBk;
+#pragma unroll
+        for (uint32_t i = 0; i < kMi; ++i)
+#pragma unroll
+            for (uint32_t j = 0; j < kNi; ++j) acc[i][j] = (f32x16)(0.0f);
+        for (uint32_t k0 = k_begin; k0 < k_end; k0 += kBk) {
+            load_stage<kAx, kBm, kThreads>(la, A, m0, k0);
+            load_stage<kBx, kBn, kThreads>(lb, B, n0, k0);
+            // a barrier alone does not wait for loads into LDS
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+#pragma unroll
+            for (uint32_t kk = 0; kk < kBk; kk += 16) {
+                bf16x8 a[kMi], b[kNi];
+#pragma unroll
+                for (uint32_t i = 0; i < kMi; ++i) a[i] = fragment<kAx, kBm>(la, wm + i * 32, kk);
+#pragma unroll
+                for (uint32_t j = 0; j < kNi; ++j) b[j] = fragment<kBx, kBn>(lb, wn + j * 32, kk);
+#pragma unroll
+                for (uint32_t i = 0; i < kMi; ++i)
+#pragma unroll
+                    for (uint32_t j = 0; j < kNi; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+            }
+            __syncthreads();
+        }
+    }
+    // The tile row of accumulator element r of block i (its column is n()).
+    __device__ static __forceinline__ uint32_t m(uint32_t i, uint32_t r) {
+        const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u;
+        return wave % kWavesM * (kBm / kWavesM) + i * 32 + (r >> 2) * 8 + (lane >> 5) * 4 + (r & 3u);
+    }
+    __device__ static __forceinline__ uint32_t n(uint32_t j) {
+        const uint32_t wave = threadIdx.x >> 6;
+        return wave / kWavesM * (kBn / kWavesN) + j * 32 + (threadIdx.x & 31u);
+    }
+};
+
+struct CeParams {
+    const uint16_t* h;
+    const uint16_t* W;
+    const void* targets;
+    uint32_t target_bytes;     // 4 or 8
+    uint32_t tokens, vocab, dim;
+    float* loss;
+    float* lse;
+    const float* dloss;
+    uint16_t* dh;
+    uint16_t* dW;
+    // workspace
+    float2* part;              // loss: per vocabulary tile and token, {maximum, sum of exp(z - maximum)}
+    float* own;                // loss: the target's logit; gradient: the rounding of the target's d
+    uint16_t* d;               // gradient: d of one piece, [token][ldd]
+    float* dh_part;            // gradient: dh in fp32, [split][token][dim]
+    uint32_t ldd;
+    uint32_t piece_begin, piece_end;   // the piece's vocabulary
+    uint32_t split_k;          // vocabulary per split of dh's product, a multiple of kBk
+    uint32_t splits;
+    uint32_t first;            // the first piece: dh_part is written, not added to
+};
+
+// The token's target, or vocab where it has none.
+__device__ __forceinline__ uint32_t target_of(const CeParams& p, uint32_t t) {
+    const int64_t v = p.target_bytes == 8 ? static_cast<const int64_t*>(p.targets)[t]
+                                          : (int64_t) static_cast<const int32_t*>(p.targets)[t];
+    return v >= 0 && v < (int64_t)p.vocab ? (uint32_t)v : p.vocab;
+}
+
+template <class T>
+__global__ __launch_bounds__(T::kThreads) void ce_loss_kernel(CeParams p) {
+    __shared__ __align__(16) uint16_t lds[T::kLdsElems];
+    const uint32_t tile = blockIdx.x, m0 = tile * T::kBm, n0 = blockIdx.y * T::kBn;
+    const Operand A{p.W, p.dim, p.vocab, p.dim}, B{p.h, p.dim, p.tokens, p.dim};
+    f32x16 acc[T::kMi][T::kNi];
+    T::product(lds, A, B, m0, n0, 0, p.dim, acc);
+
+    float2* const seen = reinterpret_cast<float2*>(lds);   // [kWavesM][kBn]
+    const uint32_t wave_m = (threadIdx.x >> 6) % T::kWavesM;
+#pragma unroll
+    for (uint32_t j = 0; j < T::kNi; ++j) {
+        const uint32_t n = T::n(j), t = n0 + n;
+        const uint32_t own = t < p.tokens ? target_of(p, t) : p.vocab;
+        float top = -INFINITY;
+#pragma unroll
+        for (uint32_t i = 0; i < T::kMi; ++i)
+#pragma unroll
+            for (uint32_t r = 0; r < 16; ++r) {
+                const uint32_t v = m0 + T::m(i, r);
+                const float z = v < p.vocab ? acc[i][j][r] : -INFINITY;
+                acc[i][j][r] = z;
+                if (v == own && v < p.vocab) p.own[t] = z;
+                // a NaN must not be lost in a maximum: it stays in the sum
+                top = fmaxf(top, z);
+            }
+        top = fmaxf(top, __shfl_xor(top, 32));
+        float sum = 0.0f;
+        const float from = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+        for (uint32_t i = 0; i < T::kMi; ++i)
+#pragma unroll
+            for (uint32_t r = 0; r < 16; ++r) sum += __expf(acc[i][j][r] - from);
+        sum += __shfl_xor(sum, 32);
+        if ((threadIdx.x & 32u) == 0) seen[wave_m * T::kBn + n] = make_float2(top, sum);
+    }
+    __syncthreads();
+    for (uint32_t n = threadIdx.x; n < T::kBn; n += T::kThreads) {
+        if (n0 + n >= p.tokens) continue;
+        float2 a = seen[n];
+#pragma unroll
+        for (uint32_t w = 1; w < T::kWavesM; ++w) {
+            const float2 b = seen[w * T::kBn + n];
+            const float top = fmaxf(a.x, b.x), from = top == -INFINITY ? 0.0f : top;
+            a = make_float2(top, a.y * __expf(a.x - from) + b.y * __expf(b.x - from));
+        }
+        p.part[(uint64_t)tile * p.tokens + n0 + n] = a;
+    }
+}
+
+constexpr uint32_t kJoinTokens = 16, kJoinLanes = 16;   // tokens per workgroup, threads per token
+
+// Joins a token's tiles: 16 threads take the tiles in turn, then a butterfly.
+__global__ __launch_bounds__(kJoinTokens* kJoinLanes) void ce_join_kernel(CeParams p, uint32_t tiles) {
+    const uint32_t t = blockIdx.x * kJoinTokens + threadIdx.x % kJoinTokens, lane = threadIdx.x / kJoinTokens;
+    __shared__ float2 seen[kJoinLanes][kJoinTokens];
+    float top = -INFINITY, sum = 0.0f;
+    if (t < p.tokens)
+        for (uint32_t i = lane; i < tiles; i += kJoinLanes) {
+            const float2 b = p.part[(uint64_t)i * p.tokens + t];
+            const float m = fmaxf(top, b.x), from = m == -INFINITY ? 0.0f : m;
+            sum = sum * __expf(top - from) + b.y * __expf(b.x - from);
+            top = m;
+        }
+    seen[lane][threadIdx.x % kJoinTokens] = make_float2(top, sum);
+    __syncthreads();
+    if (lane != 0 || t >= p.tokens) return;
+    for (uint32_t w = 1; w < kJoinLanes; ++w) {
+        const float2 b = seen[w][threadIdx.x];
+        const float m = fmaxf(top, b.x), from = m == -INFINITY ? 0.0f : m;
+        sum = sum * __expf(top - from) + b.y * __expf(b.x - from);
+        top = m;
+    }
+    const float lse = top + logf(sum);
+    p.lse[t] = lse;
+    p.loss[t] = target_of(p, t) < p.vocab ? lse - p.own[t] : 0.0f;
+}
+
+// d of one piece, in bf16.
+template <class T>
+__global__ __launch_bounds__(T::kThreads) void ce_d_kernel(CeParams p) {
+    __shared__ __align__(16) uint16_t lds[T::kLdsElems];
+    const uint32_t m0 = p.piece_begin + blockIdx.x * T::kBm, n0 = blockIdx.y * T::kBn;
+    const Operand A{p.W, p.dim, p.vocab, p.dim}, B{p.h, p.dim, p.tokens, p.dim};
+    f32x16 acc[T::kMi][T::kNi];
+    T::product(lds, A, B, m0, n0, 0, p.dim, acc);
+#pragma unroll
+    for (uint32_t j = 0; j < T::kNi; ++j) {
+        const uint32_t t = n0 + T::n(j);
+        if (t >= p.tokens) continue;
+        const uint32_t own = target_of(p, t);
+        const float g = own < p.vocab ? p.dloss[t] : 0.0f, lse = p.lse[t];
+        uint16_t* const row = p.d + (uint64_t)t * p.ldd + blockIdx.x * T::kBm;
+#pragma unroll
+        for (uint32_t i = 0; i < T::kMi; ++i)
+#pragma unroll
+            for (uint32_t r = 0; r < 16; r += 4) {
+                uint16_t b[4];
+#pragma unroll
+                for (uint32_t e = 0; e < 4; ++e) {
+                    const uint32_t v = m0 + T::m(i, r + e);
+                    float x = __expf(acc[i][j][r + e] - lse);
+                    if (v == own) x -= 1.0f;
+                    x = v < p.piece_end && own < p.vocab ? x * g : 0.0f;
+                    b[e] = f32_bf16(x);
+                    if (v == own && v < p.piece_end) p.own[t] = x - bf16_f32(b[e]);
+                }
+                const u32x2 w = {b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16};
+                *reinterpret_cast<u32x2*>(row + T::m(i, r)) = w;
+            }
+    }
+}
+
+// dh += d W over the piece, in fp32, the vocabulary split over blockIdx.z.
+template <class T>
+__global__ __launch_bounds__(T::kThreads) void ce_dh_kernel(CeParams p) {
+    __shared__ __align__(16) uint16_t lds[T::kLdsElems];
+    const uint32_t m0 = blockIdx.x * T::kBm, n0 = blockIdx.y * T::kBn;
+    const uint32_t len = p.piece_end - p.piece_begin;
+    const Operand A{p.W + (uint64_t)p.piece_begin * p.dim, p.dim, p.dim, len}, B{p.d, p.ldd, p.tokens, p.ldd};
+    const uint32_t k_begin = blockIdx.z * p.split_k, k_end = min(k_begin + p.split_k, len);
+    f32x16 acc[T::kMi][T::kNi];
+    T::product(lds, A, B, m0, n0, k_begin, k_end, acc);
+    float* const out = p.dh_part + (uint64_t)blockIdx.z * p.tokens * p.dim;
+#pragma unroll
+    for (uint32_t j = 0; j < T::kNi; ++j) {
+        const uint32_t t = n0 + T::n(j);
+        if (t >= p.tokens) continue;
+#pragma unroll
+        for (uint32_t i = 0; i < T::kMi; ++i)
+#pragma unroll
+            for (uint32_t r = 0; r < 16; r += 4) {
+                const uint32_t m = m0 + T::m(i, r);
+                if (m >= p.dim) continue;
+                f32x4* const at = reinterpret_cast<f32x4*>(out + (uint64_t)t * p.dim + m);
+                f32x4 v = {acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]};
+                if (!p.first) v += *at;
+                *at = v;
+            }
+    }
+}
+
+// dW of the piece = d^T h.
+template <class T>
+__global__ __launch_bounds__(T::kThreads) void ce_dw_kernel(CeParams p) {
+    __shared__ __align__(16) uint16_t lds[T::kLdsElems];
+    const uint32_t m0 = blockIdx.x * T::kBm, n0 = blockIdx.y * T::kBn;
+    const uint32_t len = p.piece_end - p.piece_begin;
+    const Operand A{p.h, p.dim, p.dim, p.tokens}, B{p.d, p.ldd, p.ldd, p.tokens};
+    f32x16 acc[T::kMi][T::kNi];
+    T::product(lds, A, B, m0, n0, 0, p.tokens, acc);
+#pragma unroll
+    for (uint32_t j = 0; j < T::kNi; ++j) {
+        const uint32_t v = n0 + T::n(j);
+        if (v >= len) continue;
+        uint16_t* const row = p.dW + (uint64_t)(p.piece_begin + v) * p.dim;
+#pragma unroll
+        for (uint32_t i = 0; i < T::kMi; ++i)
+#pragma unroll
+            for (uint32_t r = 0; r < 16; r += 4) {
+                const uint32_t m = m0 + T::m(i, r);
+                if (m >= p.dim) continue;
+                const u32x2 w = {f32_bf16(acc[i][j][r]) | (uint32_t)f32_bf16(acc[i][j][r + 1]) << 16,
+                                 f32_bf16(acc[i][j][r + 2]) | (uint32_t)f32_bf16(acc[i][j][r + 3]) << 16};
+                *reinterpret_cast<u32x2*>(row + m) = w;
+            }
+    }
+}
+
+// dW of no tokens.
+__global__ __launch_bounds__(256) void ce_zero_kernel(uint16_t* dW, uint64_t chunks) {
+    for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < chunks; i += (uint64_t)gridDim.x * 256)
+        reinterpret_cast<f32x4*>(dW)[i] = (f32x4)(0.0f);
+}
+
+// dh in bf16: the splits in order, plus what d's target value lost to its rounding times W[target].
+__global__ __launch_bounds__(256) void ce_dh_round_kernel(CeParams p) {
+    const uint32_t t = blockIdx.x, at = (blockIdx.y * 256 + threadIdx.x) * 4;
+    if (at >= p.dim) return;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (uint32_t s = 0; s < p.splits; ++s)
+        v += *reinterpret_cast<const f32x4*>(p.dh_part + ((uint64_t)s * p.tokens + t) * p.dim + at);
+    const uint32_t own = target_of(p, t);
+    if (own < p.vocab) {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(p.W + (uint64_t)own * p.dim + at);
+        const float c = p.own[t];
+        v[0] += c * __uint_as_float(w.x << 16);
+        v[1] += c * __uint_as_float(w.x & 0xFFFF0000u);
+        v[2] += c * __uint_as_float(w.y << 16);
+        v[3] += c * __uint_as_float(w.y & 0xFFFF0000u);
+    }
+    const u32x2 w = {f32_bf16(v[0]) | (uint32_t)f32_bf16(v[1]) << 16, f32_bf16(v[2]) | (uint32_t)f32_bf16(v[3]) << 16};
+    *reinterpret_cast<u32x2*>(p.dh + (uint64_t)t * p.dim + at) = w;
+}
+
+using TileZ = Tile<false, false, 128, 128, 2, 2>;    // W and h: k (dim) contiguous
+using TileDh = Tile<true, false, 128, 128, 2, 2>;    // W^T: m (dim) contiguous; d: k (vocabulary) contiguous
+using TileDw = Tile<true, true, 128, 128, 2, 2>;     // h^T and d^T: the output indexes contiguous
+
+constexpr uint64_t kAlign = 256;
+uint64_t up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
+
+// Workspace: the loss's tile results and target logits; the gradient's d, fp32
+// dh and target roundings.  A piece of the vocabulary is what keeps d within
+// 256 MiB, at least 1024 entries, whole tiles.
+struct CeLayout {
+    uint32_t piece, splits, split_k;
+    uint64_t own, part, d, dh_part, loss_bytes, grad_bytes;
+};
+
+CeLayout layout(uint64_t tokens, uint32_t vocab, uint32_t dim) {
+    CeLayout l{};
+    const uint64_t tiles = up(vocab, TileZ::kBm) / TileZ::kBm;
+    l.own = 0;
+    const uint64_t own_bytes = up(tokens * 4, kAlign);
+    l.part = own_bytes;
+    l.loss_bytes = l.part + up(tiles * tokens * 8, kAlign);
+    uint64_t piece = (256ull << 20) / (2 * tokens) / 1024 * 1024;
+    piece = piece < 1024 ? 1024 : piece;
+    piece = piece < up(vocab, 256) ? piece : up(vocab, 256);
+    l.piece = (uint32_t)piece;
+    const uint64_t out_tiles = up(dim, TileDh::kBm) / TileDh::kBm * (up(tokens, TileDh::kBn) / TileDh::kBn);
+    uint64_t splits = 512 / out_tiles;
+    splits = splits < 1 ? 1 : splits > piece / 1024 ? (piece < 1024 ? 1 : piece / 1024) : splits;
+    l.split_k = (uint32_t)up((piece + splits - 1) / splits, kBk);
+    l.splits = (uint32_t)((piece + l.split_k - 1) / l.split_k);
+    l.d = own_bytes;
+    l.dh_part = l.d + up(tokens * piece * 2, kAlign);
+    l.grad_bytes = l.dh_part + up((uint64_t)l.splits * tokens * dim * 4, kAlign);
+    return l;
+}
+
+bool sizes_fit(uint64_t tokens, uint32_t vocab, uint32_t dim) {
+    return tokens <= WC_MAX_TOKENS && vocab != 0 && vocab <= WC_MAX_VOCAB && dim != 0 && dim % 8 == 0 &&
+           dim <= WC_MAX_DIM;
+}
+
+bool aligned(const void* p, uintptr_t a) { return p && (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+}  // namespace
+}  // namespace wc
+
+using namespace wc;
+
+extern "C" int wc_ce_work_bytes(uint64_t tokens, uint32_t vocab, uint32_t dim, int grad, uint64_t* work_bytes) {
+    if (!work_bytes || !sizes_fit(tokens, vocab, dim)) return WC_ERR_INVALID_ARG;
+    *work_bytes = 0;
+    if (tokens == 0) return WC_OK;
+    const CeLayout l = layout(tokens, vocab, dim);
+    *work_bytes = grad && l.grad_bytes > l.loss_bytes ? l.grad_bytes : l.loss_bytes;
+    return WC_OK;
+}
+
+extern "C" int wc_ce_loss_async(const uint16_t* h, const uint16_t* W, const void* targets, uint32_t target_bytes,
+                                uint64_t tokens, uint32_t vocab, uint32_t dim, float* loss, float* lse,
+                                void* work_dev, uint64_t work_bytes, void* stream) {
+    if (!sizes_fit(tokens, vocab, dim) || (target_bytes != 4 && target_bytes != 8)) return WC_ERR_INVALID_ARG;
+    if (tokens == 0) return WC_OK;
+    const CeLayout l = layout(tokens, vocab, dim);
+    if (!aligned(h, 16) || !aligned(W, 16) || !aligned(targets, target_bytes) || !aligned(loss, 4) ||
+        !aligned(lse, 4) || !aligned(work_dev, kAlign) || work_bytes < l.loss_bytes)
+        return WC_ERR_INVALID_ARG;
+    CeParams p{};
+    p.h = h, p.W = W, p.targets = targets, p.target_bytes = target_bytes;
+    p.tokens = (uint32_t)tokens, p.vocab = vocab, p.dim = dim;
+    p.loss = loss, p.lse = lse;
+    uint8_t* const w = static_cast<uint8_t*>(work_dev);
+    p.own = reinterpret_cast<float*>(w + l.own);
+    p.part = reinterpret_cast<float2*>(w + l.part);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const uint32_t tiles = (vocab + TileZ::kBm - 1) / TileZ::kBm;
+    hipLaunchKernelGGL(ce_loss_kernel<TileZ>, dim3(tiles, (p.tokens + TileZ::kBn - 1) / TileZ::kBn),
+                       dim3(TileZ::kThreads), 0, s, p);
+    hipLaunchKernelGGL(ce_join_kernel, dim3((p.tokens + kJoinTokens - 1) / kJoinTokens),
+                       dim3(kJoinTokens * kJoinLanes), 0, s, p, tiles);
+    return hipGetLastError() == hipSuccess ? WC_OK : WC_ERR_HIP;
+}
+
+extern "C" int wc_ce_grad_async(const uint16_t* h, const uint16_t* W, const void* targets, uint32_t target_bytes,
+                                uint64_t tokens, uint32_t vocab, uint32_t dim, const float* lse, const float* dloss,
+                                uint16_t* dh, uint16_t* dW, void* work_dev, uint64_t work_bytes, void* stream) {
+    if (!sizes_fit(tokens, vocab, dim) || (target_bytes != 4 && target_bytes != 8) || (!dh && !dW))
+        return WC_ERR_INVALID_ARG;
+    if (!aligned(W, 16) || (dW && !aligned(dW, 16))) return WC_ERR_INVALID_ARG;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (tokens == 0) {   // dW is zero, dh has no rows
+        const uint64_t chunks = (uint64_t)vocab * dim / 8;
+        if (!dW) return WC_OK;
+        hipLaunchKernelGGL(ce_zero_kernel, dim3((uint32_t)(chunks < 2048 * 256 ? (chunks + 255) / 256 : 2048)), dim3(256),
+                           0, s, dW, chunks);
+        return hipGetLastError() == hipSuccess ? WC_OK : WC_ERR_HIP;
+    }
+    const CeLayout l = layout(tokens, vocab, dim);
+    if (!aligned(h, 16) || !aligned(targets, target_bytes) || !aligned(lse, 4) || !aligned(dloss, 4) ||
+        (dh && !aligned(dh, 16)) || !aligned(work_dev, kAlign) || work_bytes < l.grad_bytes)
+        return WC_ERR_INVALID_ARG;
+    CeParams p{};
+    p.h = h, p.W = W, p.targets = targets, p.target_bytes = target_bytes;
+    p.tokens = (uint32_t)tokens, p.vocab = vocab, p.dim = dim;
+    p.lse = const_cast<float*>(lse), p.dloss = dloss, p.dh = dh, p.dW = dW;
+    uint8_t* const w = static_cast<uint8_t*>(work_dev);
+    p.own = reinterpret_cast<float*>(w + l.own);
+    p.d = reinterpret_cast<uint16_t*>(w + l.d);
+    p.dh_part = reinterpret_cast<float*>(w + l.dh_part);
+    p.ldd = l.piece, p.split_k = l.split_k, p.splits = l.splits;
+    const auto cdiv = [](uint32_t a, uint32_t b) { return (a + b - 1) / b; };
+    for (uint64_t v0 = 0; v0 < vocab; v0 += l.piece) {
+        p.piece_begin = (uint32_t)v0;
+        p.piece_end = (uint32_t)(v0 + l.piece < vocab ? v0 + l.piece : vocab);
+        p.first = v0 == 0;
+        const uint32_t len = p.piece_end - p.piece_begin;
+        hipLaunchKernelGGL(ce_d_kernel<TileZ>, dim3(cdiv(len, TileZ::kBm), cdiv(p.tokens, TileZ::kBn)),
+                           dim3(TileZ::kThreads), 0, s, p);
+        if (dh)
+            hipLaunchKernelGGL(ce_dh_kernel<TileDh>,
+                               dim3(cdiv(dim, TileDh::kBm), cdiv(p.tokens, TileDh::kBn), l.splits),
+                               dim3(TileDh::kThreads), 0, s, p);
+        if (dW)
+            hipLaunchKernelGGL(ce_dw_kernel<TileDw>, dim3(cdiv(dim, TileDw::kBm), cdiv(len, TileDw::kBn)),
+                               dim3(TileDw::kThreads), 0, s, p);
+    }
+    if (dh)
+        hipLaunchKernelGGL(ce_dh_round_kernel, dim3(p.tokens, cdiv(dim, 1024)), dim3(256), 0, s, p);
+    return hipGetLastError() == hipSuccess ? WC_OK : WC_ERR_HIP;
+}

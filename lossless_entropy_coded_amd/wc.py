@@ -86,6 +86,29 @@ _lib.wc_decode_gemv_async.restype = ctypes.c_int
 _lib.wc_decode_gemv_noalloc_async.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.POINTER(GemvOperand),
                                               ctypes.c_uint32, ctypes.c_void_p]
 _lib.wc_decode_gemv_noalloc_async.restype = ctypes.c_int
+
+
+class _Q4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
+                ("rows", ctypes.c_uint32), ("cols", ctypes.c_uint32), ("group", ctypes.c_uint32)]
+
+
+_void_p, _u32, _u64, _int, _float = (ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int, ctypes.c_float)
+for _name, _args in {
+        "wc_q4_check": [_void_p],
+        "wc_gemv_q4_async": [_void_p, _void_p, _u32, _void_p, _void_p],
+        "wc_embed_async": [_void_p, _u32, _u32, _void_p, _u32, _u64, _float, _void_p, _void_p],
+        "wc_embed_q4_async": [_void_p, _void_p, _u32, _u64, _float, _void_p, _void_p],
+        "wc_embed_grad_work_bytes": [_u64, _u32, _u64p],
+        "wc_embed_grad_async": [_void_p, _void_p, _u32, _u64, _float, _void_p, _u32, _u32, _u32, _int, _void_p, _u64,
+                                _void_p],
+        "wc_ce_work_bytes": [_u64, _u32, _u32, _int, _u64p],
+        "wc_ce_loss_async": [_void_p, _void_p, _void_p, _u32, _u64, _u32, _u32, _void_p, _void_p, _void_p, _u64,
+                             _void_p],
+        "wc_ce_grad_async": [_void_p, _void_p, _void_p, _u32, _u64, _u32, _u32, _void_p, _void_p, _void_p, _void_p,
+                             _void_p, _u64, _void_p]}.items():
+    getattr(_lib, _name).argtypes = _args
+    getattr(_lib, _name).restype = ctypes.c_int
 _lib.wc_stream_reference_async.argtypes = [ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_uint64,
                                            ctypes.c_void_p]
 _lib.wc_stream_reference_async.restype = ctypes.c_int
@@ -139,6 +162,8 @@ EXPORTED = ("wc_encode_host", "wc_encode_u8_host", "wc_free_host", "wc_plan", "w
             "wc_plan_format", "wc_plan_decode_shape", "wc_decode_u8_async",
             "wc_decode_async", "wc_gemv_bf16_async", "wc_decode_gemv_work_bytes", "wc_decode_gemv_async",
             "wc_decode_gemv_noalloc_async", "wc_stream_reference_async", "wc_plan_debug_status",
+            "wc_q4_check", "wc_gemv_q4_async", "wc_embed_async", "wc_embed_q4_async", "wc_embed_grad_work_bytes",
+            "wc_embed_grad_async", "wc_ce_work_bytes", "wc_ce_loss_async", "wc_ce_grad_async",
             "wc_plan_destroy", "wc_status_str")
 
 
@@ -440,6 +465,176 @@ def decode_gemv_noalloc_async(plan: Plan, blob_dev, ops, stream=None) -> None:
     _check(_lib.wc_decode_gemv_noalloc_async(plan.handle, ctypes.c_void_p(_ptr(blob_dev)), _operands(ops), len(ops),
                                              ctypes.c_void_p(_stream_handle(stream))),
            "wc_decode_gemv_noalloc_async")
+
+
+# ---- operators on decoded tensors ------------------------------------------------
+
+# limits (include/wc.h)
+MAX_VOCAB = 1 << 22
+MAX_DIM = 1 << 16
+MAX_TOKENS = 1 << 20
+GEMV_Q4_MAX_VECS = 16
+OUT_KINDS = {"f32": 0, "bf16": 1}
+
+
+def _bytes_ok(t, nbytes: int, device, what: str, call: str) -> int:
+    """The device pointer of a tensor that _require accepts (or of a raw integer pointer)."""
+    try:
+        if t.is_cuda and t.get_device() == device and t.nbytes >= nbytes and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _require(t, nbytes, device, what, call)
+    return _ptr(t)
+
+
+def _sizes(call: str, **sizes) -> None:
+    """Sizes must be whole numbers that the C types hold; C checks the rest."""
+    for what, v in sizes.items():
+        if not 0 <= v < 1 << 32:
+            raise WCError(WC_ERR_INVALID_ARG, call, f"{what} is {v}")
+
+
+def _index_bytes(ids, what: str, call: str) -> int:
+    """4 for int32 ids, 8 for int64 ids (raw pointers are taken as int64)."""
+    if not hasattr(ids, "dtype"):
+        return 8
+    name = str(ids.dtype)
+    if name not in ("torch.int32", "torch.int64"):
+        raise WCError(WC_ERR_INVALID_ARG, call, f"{what} is {name}, not int32 or int64")
+    return 4 if name == "torch.int32" else 8
+
+
+class Q4Matrix:
+    """A wc_q4_matrix over device tensors (kept alive by this handle): 4-bit codes, two per byte and the first in
+    the low nibble (an int4 plane as decode_u8_async leaves it), bf16 scales and optional uint8 zero points
+    (8 without them), rows x ceil(cols / group) each."""
+
+    def __init__(self, codes, scales, rows: int, cols: int, group: int, zeros=None):
+        _sizes("wc_q4_check", rows=rows, cols=cols, group=group)
+        self.rows, self.cols, self.group = int(rows), int(cols), int(group)
+        self._tensors = (codes, scales, zeros)
+        self.device = _current_device()
+        n = self.rows * -(-self.cols // max(self.group, 1))
+        c = _bytes_ok(codes, self.rows * self.cols // 2, self.device, "codes", "wc_q4_check")
+        s = _bytes_ok(scales, 2 * n, self.device, "scales", "wc_q4_check")
+        z = _bytes_ok(zeros, n, self.device, "zeros", "wc_q4_check") if zeros is not None else 0
+        self._struct = _Q4(c, s, z, self.rows, self.cols, self.group)
+        self._ref = ctypes.addressof(self._struct)
+        _check(_lib.wc_q4_check(self._ref), "wc_q4_check")
+
+
+def _on_device(W: Q4Matrix, call: str):
+    dev = _current_device()
+    if W.device != dev:
+        raise WCError(WC_ERR_INVALID_ARG, call, f"the matrix is on cuda:{W.device}, not on cuda:{dev}")
+    return dev
+
+
+def gemv_q4_async(W: Q4Matrix, x_dev, n_vecs: int, y_dev, stream=None) -> None:
+    """wc_gemv_q4_async: y[t] = W x[t] for n_vecs (at most GEMV_Q4_MAX_VECS) bf16 vectors, fp32 y, one launch.
+
+    x_dev: n_vecs x cols bf16; y_dev: n_vecs x rows float32."""
+    call = "wc_gemv_q4_async"
+    dev = _on_device(W, call)
+    _sizes(call, n_vecs=n_vecs)
+    x = _bytes_ok(x_dev, 2 * n_vecs * W.cols, dev, "x", call)
+    y = _bytes_ok(y_dev, 4 * n_vecs * W.rows, dev, "y", call)
+    _check(_lib.wc_gemv_q4_async(W._ref, x, n_vecs, y, _stream_handle(stream)), call)
+
+
+def embed_async(table_dev, vocab: int, dim: int, ids_dev, n: int, out_dev, scale: float = 1.0, stream=None) -> None:
+    """wc_embed_async: out[t] = scale * table[ids[t]] (bf16), zero where ids[t] is outside [0, vocab); one launch."""
+    call = "wc_embed_async"
+    dev = _current_device()
+    _sizes(call, vocab=vocab, dim=dim, n=n)
+    width = _index_bytes(ids_dev, "ids", call)
+    table = _bytes_ok(table_dev, 2 * vocab * dim, dev, "table", call)
+    ids = _bytes_ok(ids_dev, width * n, dev, "ids", call)
+    out = _bytes_ok(out_dev, 2 * n * dim, dev, "out", call)
+    _check(_lib.wc_embed_async(table, vocab, dim, ids, width, n, scale, out, _stream_handle(stream)), call)
+
+
+def embed_q4_async(W: Q4Matrix, ids_dev, n: int, out_dev, scale: float = 1.0, stream=None) -> None:
+    """wc_embed_q4_async: embed_async from a 4-bit table of W.rows entries."""
+    call = "wc_embed_q4_async"
+    dev = _on_device(W, call)
+    _sizes(call, n=n)
+    width = _index_bytes(ids_dev, "ids", call)
+    ids = _bytes_ok(ids_dev, width * n, dev, "ids", call)
+    out = _bytes_ok(out_dev, 2 * n * W.cols, dev, "out", call)
+    _check(_lib.wc_embed_q4_async(W._ref, ids, width, n, scale, out, _stream_handle(stream)), call)
+
+
+def embed_grad_work_bytes(n: int, dim: int) -> int:
+    """wc_embed_grad_work_bytes: device scratch of embed_grad_async for n tokens."""
+    _sizes("wc_embed_grad_work_bytes", n=n, dim=dim)
+    b = ctypes.c_uint64(0)
+    _check(_lib.wc_embed_grad_work_bytes(n, dim, ctypes.byref(b)), "wc_embed_grad_work_bytes")
+    return b.value
+
+
+def embed_grad_async(dout_dev, ids_dev, n: int, dtable_dev, vocab: int, dim: int, work_dev, work_bytes: int,
+                     out: str = "f32", scale: float = 1.0, accumulate: bool = False, stream=None) -> None:
+    """wc_embed_grad_async: dtable[v] = scale * sum of dout[t] over the t with ids[t] = v, in fp32 and token order.
+
+    out: "f32" or "bf16", dtable's type.  accumulate: add to dtable instead of writing every row."""
+    call = "wc_embed_grad_async"
+    dev = _current_device()
+    _sizes(call, n=n, vocab=vocab, dim=dim)
+    if out not in OUT_KINDS:
+        raise WCError(WC_ERR_INVALID_ARG, call, f"out is {out!r}, not one of {sorted(OUT_KINDS)}")
+    width = _index_bytes(ids_dev, "ids", call)
+    dout = _bytes_ok(dout_dev, 2 * n * dim, dev, "dout", call)
+    ids = _bytes_ok(ids_dev, width * n, dev, "ids", call)
+    dtable = _bytes_ok(dtable_dev, (4 if out == "f32" else 2) * vocab * dim, dev, "dtable", call)
+    work = _bytes_ok(work_dev, int(work_bytes), dev, "work", call)
+    _check(_lib.wc_embed_grad_async(dout, ids, width, n, scale, dtable, OUT_KINDS[out], vocab, dim, bool(accumulate),
+                                    work, int(work_bytes), _stream_handle(stream)), call)
+
+
+def ce_work_bytes(tokens: int, vocab: int, dim: int, grad: bool = True) -> int:
+    """wc_ce_work_bytes: device scratch of ce_loss_async (grad False) or of both ce_loss_async and ce_grad_async."""
+    _sizes("wc_ce_work_bytes", tokens=tokens, vocab=vocab, dim=dim)
+    b = ctypes.c_uint64(0)
+    _check(_lib.wc_ce_work_bytes(tokens, vocab, dim, bool(grad), ctypes.byref(b)), "wc_ce_work_bytes")
+    return b.value
+
+
+def ce_loss_async(h_dev, W_dev, targets_dev, tokens: int, vocab: int, dim: int, loss_dev, lse_dev, work_dev,
+                  work_bytes: int, stream=None) -> None:
+    """wc_ce_loss_async: loss[t] = lse[t] - z[t][target[t]], lse[t] = log sum exp z[t] for z = h W^T (bf16 h, W)."""
+    call = "wc_ce_loss_async"
+    dev = _current_device()
+    _sizes(call, tokens=tokens, vocab=vocab, dim=dim)
+    width = _index_bytes(targets_dev, "targets", call)
+    h = _bytes_ok(h_dev, 2 * tokens * dim, dev, "h", call)
+    W = _bytes_ok(W_dev, 2 * vocab * dim, dev, "W", call)
+    targets = _bytes_ok(targets_dev, width * tokens, dev, "targets", call)
+    loss = _bytes_ok(loss_dev, 4 * tokens, dev, "loss", call)
+    lse = _bytes_ok(lse_dev, 4 * tokens, dev, "lse", call)
+    work = _bytes_ok(work_dev, int(work_bytes), dev, "work", call)
+    _check(_lib.wc_ce_loss_async(h, W, targets, width, tokens, vocab, dim, loss, lse, work, int(work_bytes),
+                                 _stream_handle(stream)), call)
+
+
+def ce_grad_async(h_dev, W_dev, targets_dev, tokens: int, vocab: int, dim: int, lse_dev, dloss_dev, dh_dev, dW_dev,
+                  work_dev, work_bytes: int, stream=None) -> None:
+    """wc_ce_grad_async: dh and dW (bf16; either may be None) of sum dloss[t] * loss[t], with ce_loss_async's lse."""
+    call = "wc_ce_grad_async"
+    dev = _current_device()
+    _sizes(call, tokens=tokens, vocab=vocab, dim=dim)
+    width = _index_bytes(targets_dev, "targets", call)
+    h = _bytes_ok(h_dev, 2 * tokens * dim, dev, "h", call)
+    W = _bytes_ok(W_dev, 2 * vocab * dim, dev, "W", call)
+    targets = _bytes_ok(targets_dev, width * tokens, dev, "targets", call)
+    lse = _bytes_ok(lse_dev, 4 * tokens, dev, "lse", call)
+    dloss = _bytes_ok(dloss_dev, 4 * tokens, dev, "dloss", call)
+    dh = _bytes_ok(dh_dev, 2 * tokens * dim, dev, "dh", call) if dh_dev is not None else 0
+    dW = _bytes_ok(dW_dev, 2 * vocab * dim, dev, "dW", call) if dW_dev is not None else 0
+    work = _bytes_ok(work_dev, int(work_bytes), dev, "work", call)
+    _check(_lib.wc_ce_grad_async(h, W, targets, width, tokens, vocab, dim, lse, dloss, dh, dW, work, int(work_bytes),
+                                 _stream_handle(stream)), call)
 
 
 def exported_symbols():
