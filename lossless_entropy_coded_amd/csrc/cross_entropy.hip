@@ -39,6 +39,7 @@ typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr uint32_t kBk = 64;              // k per LDS stage
 constexpr uint32_t kNoChunk = 0xFFFFFFF0u;   // a buffer offset beyond every operand: loads zeros
@@ -47,6 +48,20 @@ __device__ __forceinline__ float bf16_f32(uint16_t b) { return __uint_as_float((
 
 // Round to nearest even; a NaN stays a NaN.
 __device__ __forceinline__ uint16_t f32_bf16(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+
+// The byte offset in LDS of a pointer into it.
+__device__ __forceinline__ uint32_t lds_address(const uint16_t* p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint16_t*)p;
+}
+
+// Start copying 16 bytes per lane from a buffer to consecutive LDS places from
+// `to` (uniform over the wave).  It writes no register.  In assembly because
+// the compiler, for the builtin, waits for every such copy before each
+// transposing LDS read; product() does the waiting that is needed.
+__device__ __forceinline__ void copy_to_lds(uint32_t to, const u32x4& rsrc, uint32_t offset) {
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(offset), "s"(rsrc)
+                 : "memory", "m0");
+}
 
 // One operand: element (x, k) is p[x * ld + k], or p[k * ld + x] when stored
 // with x contiguous; x < rows, k < depth, everything else reads as zero.  ld
@@ -63,39 +78,63 @@ struct Operand {
 // 16-byte read touches lie in different banks.  x contiguous: row k has R / 8
 // chunks, chunk c at place c ^ ((k & 3) << 2): the 4 rows of k that a
 // transposing read touches lie 64 bytes apart.
+//
+// The loader copies one such image per stage straight from memory to LDS
+// (each lane 16 bytes; the image's permutation is applied to the source
+// addresses, since a wave writes 64 consecutive chunks).  What lies outside
+// the operand is an offset outside its buffer: the load leaves zeros.
 template <bool kXContig, uint32_t R, uint32_t kThreads>
-__device__ __forceinline__ void load_stage(uint16_t* lds, const Operand& o, uint32_t x0, uint32_t k0) {
-    constexpr uint32_t kChunks = R * kBk / 8;
-    static_assert(kChunks % kThreads == 0, "whole rounds");
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+struct Loader {
+    static constexpr uint32_t kLoads = R * kBk / 8 / kThreads;   // per thread and stage
+    static_assert(R * kBk / 8 % kThreads == 0, "whole rounds");
+    static_assert(kXContig ? kThreads % (R / 8) == 0 && kThreads / (R / 8) % 4 == 0 : kThreads % 64 == 0,
+                  "a thread's chunks of one stage have the same place in their rows");
     const uint16_t* base;
-    uint32_t bytes;
-    if (kXContig) {
-        const uint32_t left = o.depth > k0 ? o.depth - k0 : 0;
-        base = o.p + (uint64_t)k0 * o.ld;
-        bytes = (uint32_t)((left < kBk ? left : kBk) * o.ld * 2);
-    } else {
-        const uint32_t left = o.rows > x0 ? o.rows - x0 : 0;
-        base = o.p + (uint64_t)x0 * o.ld;
-        bytes = (uint32_t)((left < R ? left : R) * o.ld * 2);
-    }
-    const __amdgpu_buffer_rsrc_t rsrc =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), 0, (int)bytes, 0x00027000);
-#pragma unroll
-    for (uint32_t i = 0; i < kChunks / kThreads; ++i) {
-        const uint32_t q = i * kThreads + threadIdx.x;
-        uint32_t off;
+    uint32_t ld, depth, bytes;
+    uint32_t k;            // k contiguous: the chunk's k within a stage
+    uint32_t off[kLoads];
+
+    __device__ __forceinline__ Loader(const Operand& o, uint32_t x0) : ld((uint32_t)o.ld), depth(o.depth) {
+        const uint32_t tid = threadIdx.x;
         if (kXContig) {
-            const uint32_t k = q / (R / 8), c = (q % (R / 8)) ^ ((k & 3u) << 2);
-            off = x0 + c * 8 < o.rows ? (uint32_t)((k * o.ld + x0 + c * 8) * 2) : kNoChunk;
+            base = o.p;
+            bytes = 0;
+            const uint32_t row = tid / (R / 8), c = (tid % (R / 8)) ^ ((row & 3u) << 2);
+            k = 0;
+#pragma unroll
+            for (uint32_t i = 0; i < kLoads; ++i)
+                off[i] = x0 + c * 8 < o.rows ? ((row + i * (kThreads / (R / 8))) * ld + x0 + c * 8) * 2 : kNoChunk;
         } else {
-            const uint32_t x = q / 8, c = (q % 8) ^ (x & 7u);
-            off = k0 + c * 8 < o.depth ? (uint32_t)((x * o.ld + k0 + c * 8) * 2) : kNoChunk;
+            const uint32_t left = o.rows > x0 ? o.rows - x0 : 0;
+            base = o.p + (uint64_t)x0 * o.ld;
+            bytes = (left < R ? left : R) * ld * 2;
+            const uint32_t row = tid / 8, c = (tid % 8) ^ (row & 7u);
+            k = c * 8;
+#pragma unroll
+            for (uint32_t i = 0; i < kLoads; ++i) off[i] = ((row + i * (kThreads / 8)) * ld + c * 8) * 2;
         }
-        uint16_t* dst = lds + (i * kThreads + wave * 64u) * 8u;   // a wave's 64 chunks are consecutive
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)dst, 16, off, 0, 0, 0);
     }
-}
+
+    // Start copying the stage of k0 .. k0 + kBk - 1 (all zeros from the operand's end on).
+    __device__ __forceinline__ void start(uint16_t* lds, uint32_t k0) const {
+        const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const uint16_t* from = base;
+        uint32_t len = bytes;
+        if (kXContig) {
+            const uint32_t left = depth > k0 ? depth - k0 : 0;
+            from = base + (uint64_t)k0 * ld;
+            len = (left < kBk ? left : kBk) * ld * 2;
+        }
+        const uint64_t addr = reinterpret_cast<uint64_t>(from);
+        const u32x4 rsrc = {(uint32_t)addr, (uint32_t)(addr >> 32) & 0xFFFFu, len, 0x00027000u};
+        const bool inside = kXContig || k0 + k < depth;
+#pragma unroll
+        for (uint32_t i = 0; i < kLoads; ++i) {
+            const uint32_t at = kXContig ? off[i] : inside ? off[i] + k0 * 2 : kNoChunk;
+            copy_to_lds(lds_address(lds) + (i * kThreads + wave * 64u) * 16u, rsrc, at);
+        }
+    }
+};
 
 // The fragment of rows x .. x + 31, k .. k + 15 of a stage: lane l holds row
 // x + l % 32, k + 8 (l / 32) .. + 7.
@@ -117,47 +156,130 @@ __device__ __forceinline__ bf16x8 fragment(const uint16_t* lds, uint32_t x, uint
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// A workgroup's tile: kBm x kBn outputs over kWavesM x kWavesN waves.
-template <bool kAx, bool kBx, uint32_t kBm_, uint32_t kBn_, uint32_t kWavesM_, uint32_t kWavesN_>
+// A workgroup's tile: kBm x kBn outputs over kWavesM x kWavesN waves, operands
+// through kStages stages of LDS: while one is multiplied, the next kStages - 1
+// are on their way.
+//
+// What bounds a large product is the matrix cores: per stage of 64 k a 256 x 256
+// tile takes 2048 cycles of them on each SIMD and reads 192 KB of fragments
+// from LDS (1536 cycles at 128 bytes), so neither may wait for the other.
+// Measured at 4096 tokens x 131072 x 4096 (z, dh, dW in TFLOP/s):
+//   128 x 128, one stage, no overlap              686  805  831
+//   256 x 256, two stages, 8 waves                974  813  890
+//   the same, tiles dealt to dies (tile_of)      1159 1136 1133
+//   waves taking turns (kAlternate)              1249 1174 1182
+// 4 waves of 128 x 128 each, which read a third less LDS, reach 885: a lone
+// wave per SIMD cannot cover its own LDS reads.
+template <bool kAx, bool kBx, uint32_t kBm_, uint32_t kBn_, uint32_t kWavesM_, uint32_t kWavesN_, uint32_t kStages_>
 struct Tile {
-    static constexpr uint32_t kBm = kBm_, kBn = kBn_, kWavesM = kWavesM_, kWavesN = kWavesN_;
+    static constexpr uint32_t kBm = kBm_, kBn = kBn_, kWavesM = kWavesM_, kWavesN = kWavesN_, kStages = kStages_;
     static constexpr uint32_t kThreads = 64 * kWavesM * kWavesN;
     static constexpr uint32_t kMi = kBm / kWavesM / 32, kNi = kBn / kWavesN / 32;
-    static constexpr uint32_t kLdsElems = (kBm + kBn) * kBk;
+    static constexpr uint32_t kStageElems = (kBm + kBn) * kBk;
+    static constexpr uint32_t kLdsElems = kStages * kStageElems;
+    static constexpr bool kAlternate = kThreads == 512;
+    static_assert(!kAlternate || kStages == 2, "alternating waves take two stages");
+    using LoadA = Loader<kAx, kBm, kThreads>;
+    using LoadB = Loader<kBx, kBn, kThreads>;
 
-    // acc = sum over k in [k_begin, k_end) of A(m0 + ., k) B(n0 + ., k); k_begin is a multiple of kBk
+    // acc = sum over k in [k_begin, k_end) of A(m0 + ., k) B(n0 + ., k); k_begin
+    // is a multiple of kBk, k_end one too or the operands' end.
     __device__ static __forceinline__ void product(uint16_t* lds, const Operand& A, const Operand& B, uint32_t m0,
                                                    uint32_t n0, uint32_t k_begin, uint32_t k_end,
                                                    f32x16 (&acc)[kMi][kNi]) {
         const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         const uint32_t wm = wave % kWavesM * (kBm / kWavesM), wn = wave / kWavesM * (kBn / kWavesN);
-        uint16_t* const la = lds;
-        uint16_t* const lb = lds + kBm * kBk;
+        const LoadA la(A, m0);
+        const LoadB lb(B, n0);
 #pragma unroll
         for (uint32_t i = 0; i < kMi; ++i)
 #pragma unroll
             for (uint32_t j = 0; j < kNi; ++j) acc[i][j] = (f32x16)(0.0f);
-        for (uint32_t k0 = k_begin; k0 < k_end; k0 += kBk) {
-            load_stage<kAx, kBm, kThreads>(la, A, m0, k0);
-            load_stage<kBx, kBn, kThreads>(lb, B, n0, k0);
-            // a barrier alone does not wait for loads into LDS
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            __syncthreads();
+        uint32_t next = k_begin;   // the stage to start next (past k_end: its products are not taken)
 #pragma unroll
-            for (uint32_t kk = 0; kk < kBk; kk += 16) {
-                bf16x8 a[kMi], b[kNi];
-#pragma unroll
-                for (uint32_t i = 0; i < kMi; ++i) a[i] = fragment<kAx, kBm>(la, wm + i * 32, kk);
-#pragma unroll
-                for (uint32_t j = 0; j < kNi; ++j) b[j] = fragment<kBx, kBn>(lb, wn + j * 32, kk);
-#pragma unroll
-                for (uint32_t i = 0; i < kMi; ++i)
-#pragma unroll
-                    for (uint32_t j = 0; j < kNi; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
-            }
-            __syncthreads();
+        for (uint32_t s = 0; s + 1 < kStages; ++s, next += kBk) {
+            la.start(lds + s * kStageElems, next);
+            lb.start(lds + s * kStageElems + kBm * kBk, next);
         }
+        uint32_t at = 0, to = (kStages - 1) * kStageElems;
+        if constexpr (kAlternate) {
+            // The two waves of each SIMD take turns: waves 4..7 run half a step behind waves 0..3, so that one
+            // group reads its fragments while the other one's products keep the matrix cores busy.  Every wave
+            // passes the same barriers: the late group has one more at the start, the other one at the end.
+            // Stage k0 + kBk is copied while stage k0 is multiplied, into the LDS of the stage before, which both
+            // groups have read: a group's reads have returned before the barrier behind them.
+            const bool late = wave >= 4;
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            if (late) __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            for (uint32_t k0 = k_begin; k0 < k_end; k0 += kBk) {
+                const uint16_t* const sa = lds + at;
+                const uint16_t* const sb = lds + at + kBm * kBk;
+#pragma unroll
+                for (uint32_t kk = 0; kk < kBk; kk += 16) {
+                    bf16x8 a[kMi], b[kNi];
+#pragma unroll
+                    for (uint32_t i = 0; i < kMi; ++i) a[i] = fragment<kAx, kBm>(sa, wm + i * 32, kk);
+#pragma unroll
+                    for (uint32_t j = 0; j < kNi; ++j) b[j] = fragment<kBx, kBn>(sb, wn + j * 32, kk);
+                    if (kk == 0) la.start(lds + to, next);
+                    if (kk == 16) lb.start(lds + to + kBm * kBk, next);
+                    if (kk == kBk - 16) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                    __builtin_amdgcn_s_barrier();
+                    asm volatile("" ::: "memory");
+                    __builtin_amdgcn_sched_barrier(0);
+                    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+                    for (uint32_t i = 0; i < kMi; ++i)
+#pragma unroll
+                        for (uint32_t j = 0; j < kNi; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+                    __builtin_amdgcn_s_setprio(0);
+                    __builtin_amdgcn_sched_barrier(0);
+                    __builtin_amdgcn_s_barrier();
+                    asm volatile("" ::: "memory");
+                }
+                next += kBk;
+                to = at;
+                at = at + kStageElems == kLdsElems ? 0 : at + kStageElems;
+            }
+            if (!late) __builtin_amdgcn_s_barrier();
+        } else {
+            for (uint32_t k0 = k_begin; k0 < k_end; k0 += kBk) {
+                // this stage has landed once only the later ones' loads are outstanding (each wave waits for its own,
+                // the barrier joins them); past the barrier every wave is done with the stage before, which is refilled
+                constexpr uint32_t kLater = (kStages - 2) * (LoadA::kLoads + LoadB::kLoads);
+                static_assert(kLater < 64, "the load counter's range");
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kLater) : "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+                la.start(lds + to, next);
+                lb.start(lds + to + kBm * kBk, next);
+                next += kBk;
+                const uint16_t* const sa = lds + at;
+                const uint16_t* const sb = lds + at + kBm * kBk;
+#pragma unroll
+                for (uint32_t kk = 0; kk < kBk; kk += 16) {
+                    bf16x8 a[kMi], b[kNi];
+#pragma unroll
+                    for (uint32_t i = 0; i < kMi; ++i) a[i] = fragment<kAx, kBm>(sa, wm + i * 32, kk);
+#pragma unroll
+                    for (uint32_t j = 0; j < kNi; ++j) b[j] = fragment<kBx, kBn>(sb, wn + j * 32, kk);
+#pragma unroll
+                    for (uint32_t i = 0; i < kMi; ++i)
+#pragma unroll
+                        for (uint32_t j = 0; j < kNi; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+                }
+                to = at;
+                at = at + kStageElems == kLdsElems ? 0 : at + kStageElems;
+            }
+        }
+        // nothing is on its way into LDS any more, and every wave is done reading it
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
     }
     // The tile row of accumulator element r of block i (its column is n()).
     __device__ static __forceinline__ uint32_t m(uint32_t i, uint32_t r) {
@@ -169,6 +291,22 @@ struct Tile {
         return wave / kWavesM * (kBn / kWavesN) + j * 32 + (threadIdx.x & 31u);
     }
 };
+
+// Which tile a workgroup takes.  Workgroups go to the 8 dies in turn: each die
+// gets a contiguous run of tiles (its L2 is its own), and within a run 4 tiles
+// of m go with each tile of n, so that the tiles in work at one time share
+// operands both ways.
+__device__ __forceinline__ bool tile_of(uint32_t id, uint32_t ms, uint32_t ns, uint32_t& m, uint32_t& n) {
+    const uint32_t total = ms * ns, per = (total + 7) / 8, t = id % 8 * per + id / 8;
+    if (id / 8 >= per || t >= total) return false;
+    constexpr uint32_t kBand = 4;
+    const uint32_t band = t / (kBand * ns), left = ms - band * kBand, width = left < kBand ? left : kBand;
+    const uint32_t in = t - band * kBand * ns;
+    m = band * kBand + in % width;
+    n = in / width;
+    return true;
+}
+uint32_t tile_grid(uint32_t ms, uint32_t ns) { return (ms * ns + 7) / 8 * 8; }
 
 struct CeParams {
     const uint16_t* h;
@@ -203,7 +341,9 @@ __device__ __forceinline__ uint32_t target_of(const CeParams& p, uint32_t t) {
 template <class T>
 __global__ __launch_bounds__(T::kThreads) void ce_loss_kernel(CeParams p) {
     __shared__ __align__(16) uint16_t lds[T::kLdsElems];
-    const uint32_t tile = blockIdx.x, m0 = tile * T::kBm, n0 = blockIdx.y * T::kBn;
+    uint32_t tile, nt;
+    if (!tile_of(blockIdx.x, (p.vocab + T::kBm - 1) / T::kBm, (p.tokens + T::kBn - 1) / T::kBn, tile, nt)) return;
+    const uint32_t m0 = tile * T::kBm, n0 = nt * T::kBn;
     const Operand A{p.W, p.dim, p.vocab, p.dim}, B{p.h, p.dim, p.tokens, p.dim};
     f32x16 acc[T::kMi][T::kNi];
     T::product(lds, A, B, m0, n0, 0, p.dim, acc);
@@ -282,7 +422,11 @@ __global__ __launch_bounds__(kJoinTokens* kJoinLanes) void ce_join_kernel(CePara
 template <class T>
 __global__ __launch_bounds__(T::kThreads) void ce_d_kernel(CeParams p) {
     __shared__ __align__(16) uint16_t lds[T::kLdsElems];
-    const uint32_t m0 = p.piece_begin + blockIdx.x * T::kBm, n0 = blockIdx.y * T::kBn;
+    uint32_t mt, nt;
+    if (!tile_of(blockIdx.x, (p.piece_end - p.piece_begin + T::kBm - 1) / T::kBm, (p.tokens + T::kBn - 1) / T::kBn, mt,
+                 nt))
+        return;
+    const uint32_t m0 = p.piece_begin + mt * T::kBm, n0 = nt * T::kBn;
     const Operand A{p.W, p.dim, p.vocab, p.dim}, B{p.h, p.dim, p.tokens, p.dim};
     f32x16 acc[T::kMi][T::kNi];
     T::product(lds, A, B, m0, n0, 0, p.dim, acc);
@@ -292,7 +436,7 @@ __global__ __launch_bounds__(T::kThreads) void ce_d_kernel(CeParams p) {
         if (t >= p.tokens) continue;
         const uint32_t own = target_of(p, t);
         const float g = own < p.vocab ? p.dloss[t] : 0.0f, lse = p.lse[t];
-        uint16_t* const row = p.d + (uint64_t)t * p.ldd + blockIdx.x * T::kBm;
+        uint16_t* const row = p.d + (uint64_t)t * p.ldd + mt * T::kBm;
 #pragma unroll
         for (uint32_t i = 0; i < T::kMi; ++i)
 #pragma unroll
@@ -313,17 +457,19 @@ __global__ __launch_bounds__(T::kThreads) void ce_d_kernel(CeParams p) {
     }
 }
 
-// dh += d W over the piece, in fp32, the vocabulary split over blockIdx.z.
+// dh += d W over the piece, in fp32, the vocabulary split over blockIdx.y.
 template <class T>
 __global__ __launch_bounds__(T::kThreads) void ce_dh_kernel(CeParams p) {
     __shared__ __align__(16) uint16_t lds[T::kLdsElems];
-    const uint32_t m0 = blockIdx.x * T::kBm, n0 = blockIdx.y * T::kBn;
+    uint32_t mt, nt;
+    if (!tile_of(blockIdx.x, (p.dim + T::kBm - 1) / T::kBm, (p.tokens + T::kBn - 1) / T::kBn, mt, nt)) return;
+    const uint32_t m0 = mt * T::kBm, n0 = nt * T::kBn;
     const uint32_t len = p.piece_end - p.piece_begin;
     const Operand A{p.W + (uint64_t)p.piece_begin * p.dim, p.dim, p.dim, len}, B{p.d, p.ldd, p.tokens, p.ldd};
-    const uint32_t k_begin = blockIdx.z * p.split_k, k_end = min(k_begin + p.split_k, len);
+    const uint32_t k_begin = blockIdx.y * p.split_k, k_end = min(k_begin + p.split_k, len);
     f32x16 acc[T::kMi][T::kNi];
     T::product(lds, A, B, m0, n0, k_begin, k_end, acc);
-    float* const out = p.dh_part + (uint64_t)blockIdx.z * p.tokens * p.dim;
+    float* const out = p.dh_part + (uint64_t)blockIdx.y * p.tokens * p.dim;
 #pragma unroll
     for (uint32_t j = 0; j < T::kNi; ++j) {
         const uint32_t t = n0 + T::n(j);
@@ -346,8 +492,10 @@ __global__ __launch_bounds__(T::kThreads) void ce_dh_kernel(CeParams p) {
 template <class T>
 __global__ __launch_bounds__(T::kThreads) void ce_dw_kernel(CeParams p) {
     __shared__ __align__(16) uint16_t lds[T::kLdsElems];
-    const uint32_t m0 = blockIdx.x * T::kBm, n0 = blockIdx.y * T::kBn;
     const uint32_t len = p.piece_end - p.piece_begin;
+    uint32_t mt, nt;
+    if (!tile_of(blockIdx.x, (p.dim + T::kBm - 1) / T::kBm, (len + T::kBn - 1) / T::kBn, mt, nt)) return;
+    const uint32_t m0 = mt * T::kBm, n0 = nt * T::kBn;
     const Operand A{p.h, p.dim, p.dim, p.tokens}, B{p.d, p.ldd, p.ldd, p.tokens};
     f32x16 acc[T::kMi][T::kNi];
     T::product(lds, A, B, m0, n0, 0, p.tokens, acc);
@@ -395,9 +543,9 @@ __global__ __launch_bounds__(256) void ce_dh_round_kernel(CeParams p) {
     *reinterpret_cast<u32x2*>(p.dh + (uint64_t)t * p.dim + at) = w;
 }
 
-using TileZ = Tile<false, false, 128, 128, 2, 2>;    // W and h: k (dim) contiguous
-using TileDh = Tile<true, false, 128, 128, 2, 2>;    // W^T: m (dim) contiguous; d: k (vocabulary) contiguous
-using TileDw = Tile<true, true, 128, 128, 2, 2>;     // h^T and d^T: the output indexes contiguous
+using TileZ = Tile<false, false, 256, 256, 2, 4, 2>;    // W and h: k (dim) contiguous
+using TileDh = Tile<true, false, 256, 256, 2, 4, 2>;    // W^T: m (dim) contiguous; d: k (vocabulary) contiguous
+using TileDw = Tile<true, true, 256, 256, 2, 4, 2>;     // h^T and d^T: the output indexes contiguous
 
 constexpr uint64_t kAlign = 256;
 uint64_t up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
@@ -471,7 +619,7 @@ extern "C" int wc_ce_loss_async(const uint16_t* h, const uint16_t* W, const void
     p.part = reinterpret_cast<float2*>(w + l.part);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     const uint32_t tiles = (vocab + TileZ::kBm - 1) / TileZ::kBm;
-    hipLaunchKernelGGL(ce_loss_kernel<TileZ>, dim3(tiles, (p.tokens + TileZ::kBn - 1) / TileZ::kBn),
+    hipLaunchKernelGGL(ce_loss_kernel<TileZ>, dim3(tile_grid(tiles, (p.tokens + TileZ::kBn - 1) / TileZ::kBn)),
                        dim3(TileZ::kThreads), 0, s, p);
     hipLaunchKernelGGL(ce_join_kernel, dim3((p.tokens + kJoinTokens - 1) / kJoinTokens),
                        dim3(kJoinTokens * kJoinLanes), 0, s, p, tiles);
@@ -511,14 +659,14 @@ extern "C" int wc_ce_grad_async(const uint16_t* h, const uint16_t* W, const void
         p.piece_end = (uint32_t)(v0 + l.piece < vocab ? v0 + l.piece : vocab);
         p.first = v0 == 0;
         const uint32_t len = p.piece_end - p.piece_begin;
-        hipLaunchKernelGGL(ce_d_kernel<TileZ>, dim3(cdiv(len, TileZ::kBm), cdiv(p.tokens, TileZ::kBn)),
+        hipLaunchKernelGGL(ce_d_kernel<TileZ>, dim3(tile_grid(cdiv(len, TileZ::kBm), cdiv(p.tokens, TileZ::kBn))),
                            dim3(TileZ::kThreads), 0, s, p);
         if (dh)
             hipLaunchKernelGGL(ce_dh_kernel<TileDh>,
-                               dim3(cdiv(dim, TileDh::kBm), cdiv(p.tokens, TileDh::kBn), l.splits),
+                               dim3(tile_grid(cdiv(dim, TileDh::kBm), cdiv(p.tokens, TileDh::kBn)), l.splits),
                                dim3(TileDh::kThreads), 0, s, p);
         if (dW)
-            hipLaunchKernelGGL(ce_dw_kernel<TileDw>, dim3(cdiv(dim, TileDw::kBm), cdiv(len, TileDw::kBn)),
+            hipLaunchKernelGGL(ce_dw_kernel<TileDw>, dim3(tile_grid(cdiv(dim, TileDw::kBm), cdiv(len, TileDw::kBn))),
                                dim3(TileDw::kThreads), 0, s, p);
     }
     if (dh)
