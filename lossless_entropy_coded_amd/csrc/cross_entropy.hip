@@ -29,6 +29,7 @@
 #include <cstdint>
 
 #include "../../include/wc.h"
+#include "lds_copy.h"
 
 namespace wc {
 namespace {
@@ -39,29 +40,13 @@ typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr uint32_t kBk = 64;              // k per LDS stage
-constexpr uint32_t kNoChunk = 0xFFFFFFF0u;   // a buffer offset beyond every operand: loads zeros
 
 __device__ __forceinline__ float bf16_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 
 // Round to nearest even; a NaN stays a NaN.
 __device__ __forceinline__ uint16_t f32_bf16(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
-
-// The byte offset in LDS of a pointer into it.
-__device__ __forceinline__ uint32_t lds_address(const uint16_t* p) {
-    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint16_t*)p;
-}
-
-// Start copying 16 bytes per lane from a buffer to consecutive LDS places from
-// `to` (uniform over the wave).  It writes no register.  In assembly because
-// the compiler, for the builtin, waits for every such copy before each
-// transposing LDS read; product() does the waiting that is needed.
-__device__ __forceinline__ void copy_to_lds(uint32_t to, const u32x4& rsrc, uint32_t offset) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(offset), "s"(rsrc)
-                 : "memory", "m0");
-}
 
 // One operand: element (x, k) is p[x * ld + k], or p[k * ld + x] when stored
 // with x contiguous; x < rows, k < depth, everything else reads as zero.  ld
@@ -125,8 +110,7 @@ struct Loader {
             from = base + (uint64_t)k0 * ld;
             len = (left < kBk ? left : kBk) * ld * 2;
         }
-        const uint64_t addr = reinterpret_cast<uint64_t>(from);
-        const u32x4 rsrc = {(uint32_t)addr, (uint32_t)(addr >> 32) & 0xFFFFu, len, 0x00027000u};
+        const u32x4 rsrc = buffer_words(from, len);
         const bool inside = kXContig || k0 + k < depth;
 #pragma unroll
         for (uint32_t i = 0; i < kLoads; ++i) {

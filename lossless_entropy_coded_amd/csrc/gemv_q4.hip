@@ -7,55 +7,321 @@
 // Codes are two per byte, the first in the low nibble; zero points are 8 where
 // none are given.
 //
-// A wave owns one row: lane l takes the 8-column chunks l, l + 64, ...,
-// multiplies codes less zero point (exact in fp32) with x, sums 8 products,
-// and adds them, times the group's scale, to its fp32 partial; a butterfly adds
-// the lanes.
+// A product of this kind reads every weight once and is bound by memory, if the
+// vector units keep up: at 8 TB/s a CU has 2.4 operations per weight, and
+// converting and multiplying weights one at a time takes that for one vector
+// and more for each further one.  So the products are the matrix cores':
+//   - v_mfma_f32_16x16x32_bf16, its 16 rows the vectors (those not there are
+//     zero), its 16 columns weight rows, 32 columns of W at a time;
+//   - a code's signed value code - 8 becomes bf16 (exactly, over 16) with one
+//     conversion, v_cvt_off_f32_i4 on a selected byte, and half a byte
+//     permutation: 1.75 operations per weight whatever the number of vectors;
+//     With zero points, code less zero point is made as a signed byte first
+//     (2.4 operations per weight): subtracting zero * sum(x) afterwards would
+//     lose small products next to a large x that its zero point cancels;
+//   - the products are exact in fp32 and sums are held in fp32; a group's sum
+//     times its scale is added to the row's.
+//
+// A wave takes 16 kTiles rows and a part of the columns, 128 columns per step:
+// lane (r, q) loads the 16 bytes of row r's q-th 32 columns, four rows of lanes
+// exchange dwords (2 + 2 lane swaps) so that each of the four products of a
+// step has 32 neighbouring columns, and x comes through the wave's own LDS.
+// The waves of a workgroup share the rows and split the columns, and add their
+// sums in order at the end: everything is summed in a fixed order.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
 
 #include "../../include/wc.h"
+#include "lds_copy.h"
 
 namespace wc {
 namespace {
 
-constexpr uint32_t kQ4Waves = 4;   // waves, and rows, per workgroup
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr uint32_t kStepCols = 128;
+constexpr uint32_t kMaxWaves = 8;
 
 struct Q4Params {
-    const uint32_t* codes;
+    const uint8_t* codes;
     const uint16_t* scales;
     const uint8_t* zeros;
     const uint16_t* x;
     float* y;
-    uint32_t rows, cols, group, groups;
+    uint32_t rows, cols, group, groups, vecs;
+    uint32_t group_magic;      // chunk / (group / 32) = mulhi(chunk, group_magic) + (chunk & group_one)
+    uint32_t group_one;
+    uint32_t slabs_per_wave;
 };
 
-__global__ __launch_bounds__(64 * kQ4Waves) void gemv_q4_kernel(Q4Params p) {
-    const uint32_t lane = threadIdx.x & 63u;
-    const uint64_t row = (uint64_t)blockIdx.x * kQ4Waves + (threadIdx.x >> 6);
-    if (row >= p.rows) return;
-    const uint32_t chunks = p.cols / 8;
-    const uint32_t* const w = p.codes + row * chunks;
-    const uint4* const x = reinterpret_cast<const uint4*>(p.x + (uint64_t)blockIdx.y * p.cols);
-    float acc = 0.0f;
-    for (uint32_t c = lane; c < chunks; c += 64) {
-        const uint32_t q = w[c], g = c * 8 / p.group;
-        const uint4 xv = x[c];
-        const float scale = __uint_as_float((uint32_t)p.scales[row * p.groups + g] << 16);
-        const float zero = p.zeros ? (float)p.zeros[row * p.groups + g] : 8.0f;
-        const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w};
-        float sum = 0.0f;
+// A slab is what a wave has on its way at a time: kSlab steps.  LDS of one wave:
+// x of two slabs, [vector][column], 1 KB per copy.
+template <int kVecs>
+struct Q4Shape {
+    static constexpr uint32_t kSlab = kVecs == 1 ? 4 : kVecs == 16 ? 1 : 2;
+    static constexpr uint32_t kRowBytes = kSlab * kStepCols * 2;   // of one vector
+    static constexpr uint32_t kXBytes = kVecs * kRowBytes;
+    static constexpr uint32_t kCopies = kXBytes / 1024;
+    static_assert(kXBytes % 1024 == 0, "whole copies");
+    static constexpr uint32_t kWaveBytes = 2 * kXBytes;
+};
+
+__device__ __forceinline__ float bf16_f32(uint32_t b) { return __uint_as_float(b << 16); }
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, uint64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)(uint32_t)bytes, 0x00027000);
+}
+
+// (code - 8) / 16 in bf16 for the 8 codes of a dword (^ 0x88888888: signed nibbles), in order.
+__device__ __forceinline__ bf16x8 weights(uint32_t codes) {
+    const uint32_t even = codes ^ 0x88888888u, odd = even >> 4;
+    u32x4 w;
 #pragma unroll
-        for (uint32_t i = 0; i < 8; ++i) {
-            const float xi = __uint_as_float(i & 1 ? xs[i / 2] & 0xFFFF0000u : xs[i / 2] << 16);
-            sum = __builtin_fmaf((float)((q >> (4 * i)) & 15u) - zero, xi, sum);
+    for (uint32_t i = 0; i < 4; ++i)
+        w[i] = __builtin_amdgcn_perm(
+            __float_as_uint(__builtin_amdgcn_cvt_off_f32_i4((odd >> (8 * i)) & 0xFFu)),
+            __float_as_uint(__builtin_amdgcn_cvt_off_f32_i4((even >> (8 * i)) & 0xFFu)), 0x07060302u);
+    return __builtin_bit_cast(bf16x8, w);
+}
+
+// code - zero point, at most 128 (four times in zz), in bf16 for the 8 codes of a dword, in order: bytes
+// 128 + code - zero point, which borrow nothing from each other, less 128.
+__device__ __forceinline__ bf16x8 weights(uint32_t codes, uint32_t zz) {
+    const uint32_t even = (((codes & 0x0F0F0F0Fu) | 0x80808080u) - zz) ^ 0x80808080u;
+    const uint32_t odd = ((((codes >> 4) & 0x0F0F0F0Fu) | 0x80808080u) - zz) ^ 0x80808080u;
+    u32x4 w;
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i)
+        w[i] = __builtin_amdgcn_perm(__float_as_uint((float)(int8_t)(odd >> (8 * i))),
+                                     __float_as_uint((float)(int8_t)(even >> (8 * i))), 0x07060302u);
+    return __builtin_bit_cast(bf16x8, w);
+}
+
+// Transposes four dwords of four rows of 16 lanes: out[j] in row q is in[q] of row j.
+__device__ __forceinline__ u32x4 transpose_rows(const u32x4& in) {
+    const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(in[0], in[2], false, false));
+    const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(in[1], in[3], false, false));
+    const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(a.x, b.x, false, false));
+    const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(a.y, b.y, false, false));
+    return u32x4{lo.x, lo.y, hi.x, hi.y};
+}
+
+// out[j]: row j's value, in all four rows of 16 lanes.
+__device__ __forceinline__ u32x4 spread_rows(uint32_t v) {
+    const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(v, v, false, false));
+    const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(a.x, a.x, false, false));
+    const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(a.y, a.y, false, false));
+    return u32x4{lo.x, lo.y, hi.x, hi.y};
+}
+
+// The products of n columns of one weight row with x, term by term.
+__device__ __attribute__((noinline)) float exact_block(const uint16_t* x, const uint8_t* codes, uint32_t n,
+                                                       float scale, float zero) {
+    float sum = 0.0f;
+    for (uint32_t i = 0; i < n; ++i)
+        sum += scale * ((float)(i & 1 ? codes[i / 2] >> 4 : codes[i / 2] & 15u) - zero) * bf16_f32(x[i]);
+    return sum;
+}
+
+// What a wave has in registers for one slab: its codes, and scale bits << 16 |
+// zero point of each lane's chunk.
+template <int kSlab, int kTiles>
+struct Slab {
+    u32x4 w[kSlab][kTiles];
+    uint32_t scale[kSlab][kTiles];
+    uint32_t zero[kSlab][kTiles];
+};
+
+// kVecs: vectors, rounded up.  kBlock: chunks of 32 columns (1, 2 or 4) that
+// always share a group.  kWhole: columns are a multiple of 32, so that a lane's
+// chunk is one 16-byte load; kZeros: zero points are given (they may be, if
+// not kWhole).
+template <int kVecs, int kTiles, int kBlock, bool kWhole, bool kZeros>
+__global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
+    using S = Q4Shape<kVecs>;
+    constexpr bool kGiven = kZeros || !kWhole;
+    using Loads = Slab<S::kSlab, kTiles>;
+    extern __shared__ __align__(16) uint8_t lds[];
+    const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t waves = blockDim.x >> 6;
+    uint8_t* const xs = lds + wave * S::kWaveBytes;
+    uint8_t* const none = lds + waves * S::kWaveBytes;   // 16 zero bytes: vectors that are not there
+    if (threadIdx.x < 4) reinterpret_cast<uint32_t*>(none)[threadIdx.x] = 0;
+    __syncthreads();
+
+    const uint32_t r = lane & 15u, q = lane >> 4;   // weight row of a tile (or vector, holding x); chunk of a step
+    const uint32_t row0 = blockIdx.x * 16 * kTiles, rows = min(p.rows - row0, 16u * kTiles);
+    const uint32_t row_bytes = p.cols / 2;
+    const auto codes_buf = buffer(p.codes + (uint64_t)row0 * row_bytes, (uint64_t)rows * row_bytes);
+    const auto scale_buf = buffer(p.scales + (uint64_t)row0 * p.groups, (uint64_t)rows * p.groups * 2);
+    const auto zero_buf = buffer(p.zeros + (uint64_t)row0 * p.groups, p.zeros ? (uint64_t)rows * p.groups : 0);
+    const uint32_t no_zeros = p.zeros ? 0 : 8;
+    const auto x_buf = buffer(p.x, (uint64_t)p.vecs * p.cols * 2);
+
+    // Where the lane reads its vector's x.  64-byte pieces of a step stand at piece ^ (vector & 3), so that four
+    // vectors' lie in different banks.
+    const bool there = r < (uint32_t)kVecs;
+    const uint32_t x_at = r * S::kRowBytes + q * 16;
+
+    // Start the loads of a slab: x first, which has arrived when the registers have.
+    const auto load = [&](uint32_t slab, uint32_t half) {
+        Loads l;
+        const uint32_t c0 = slab * S::kSlab * kStepCols;
+#pragma unroll
+        for (uint32_t k = 0; k < S::kCopies; ++k) {
+            const uint32_t to = k * 1024 + lane * 16, v = to / S::kRowBytes, b = to % S::kRowBytes;
+            const uint32_t c = c0 + (b ^ ((v & 3u) * 64)) / 2;
+            copy_to_lds_counted(xs + half * S::kXBytes + k * 1024, x_buf,
+                                v < p.vecs && c < p.cols ? (v * p.cols + c) * 2 : kNoChunk);
         }
-        acc = __builtin_fmaf(scale, sum, acc);
-    }
 #pragma unroll
-    for (uint32_t m = 32; m >= 1; m >>= 1) acc += __shfl_xor(acc, (int)m, 64);
-    if (lane == 0) p.y[(uint64_t)blockIdx.y * p.rows + row] = acc;
+        for (uint32_t st = 0; st < S::kSlab; ++st) {
+            const uint32_t c = c0 + st * kStepCols + q * 32;
+            const uint32_t g = __umulhi(c / 32, p.group_magic) + (c / 32 & p.group_one);
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+                const uint32_t row = i * 16 + r, at = row * row_bytes + c / 2;
+                if (kWhole) {
+                    l.w[st][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                        codes_buf, c < p.cols ? at : kNoChunk, 0, 0));
+                } else {
+#pragma unroll
+                    for (uint32_t d = 0; d < 4; ++d)
+                        l.w[st][i][d] = __builtin_amdgcn_raw_buffer_load_b32(
+                            codes_buf, c + d * 8 < p.cols ? at + d * 4 : kNoChunk, 0, 0);
+                }
+                const uint32_t at_g = c < p.cols ? row * p.groups + g : kNoChunk / 2;
+                l.scale[st][i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(scale_buf, at_g * 2, 0, 0);
+                l.zero[st][i] =   // the buffer is empty where none are given
+                    kGiven ? (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(zero_buf, at_g, 0, 0) + no_zeros : 8u;
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);   // started before what is multiplied next
+        return l;
+    };
+
+    f32x4 acc[kTiles];   // of weight row r and vectors 4 q ..  4 q + 3
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const auto process = [&](Loads& l, uint32_t slab, uint32_t half) {
+        // the registers loaded last have arrived, so x has too
+        asm volatile("" : "+v"(l.scale[S::kSlab - 1][kTiles - 1]), "+v"(l.w[S::kSlab - 1][kTiles - 1])::"memory");
+        const uint8_t* const from = there ? xs + half * S::kXBytes + x_at : none;
+#pragma unroll
+        for (uint32_t st = 0; st < S::kSlab; ++st) {
+            bf16x8 x[4];
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j)
+                x[j] = *reinterpret_cast<const bf16x8*>(from + (there ? st * 256 + ((j ^ (r & 3u)) * 64) : 0));
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+                const u32x4 w = transpose_rows(l.w[st][i]);
+                const u32x4 sz = spread_rows(l.scale[st][i] << 16 | l.zero[st][i]);
+                const bool far = kGiven && __any(l.zero[st][i] > 128u);
+#pragma unroll
+                for (uint32_t b = 0; b < 4 / kBlock; ++b) {
+                    const uint32_t word = sz[b * kBlock];
+                    const float scale = __uint_as_float(word & 0xFFFF0000u);
+                    if (far) {   // no 4-bit code's zero point, but a byte may hold it
+                        const uint32_t c = (slab * S::kSlab + st) * kStepCols + b * kBlock * 32;
+                        const uint32_t row = row0 + i * 16 + r;
+#pragma unroll
+                        for (uint32_t e = 0; e < 4; ++e) {
+                            const uint32_t v = q * 4 + e;
+                            if (v < p.vecs && row < p.rows && c < p.cols)
+                                acc[i][e] += exact_block(p.x + (uint64_t)v * p.cols + c,
+                                                         p.codes + (uint64_t)row * row_bytes + c / 2,
+                                                         min(kBlock * 32u, p.cols - c), scale, (float)(word & 0xFFu));
+                        }
+                        continue;
+                    }
+                    const uint32_t zz = __builtin_amdgcn_perm(0, word, 0);
+                    f32x4 D = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (uint32_t j = b * kBlock; j < (b + 1) * kBlock; ++j)
+                        D = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[j], kGiven ? weights(w[j], zz) : weights(w[j]), D,
+                                                                     0, 0, 0);
+                    const float by = kGiven ? scale : scale * 16.0f;
+#pragma unroll
+                    for (uint32_t e = 0; e < 4; ++e) acc[i][e] = __builtin_fmaf(D[e], by, acc[i][e]);
+                }
+            }
+        }
+        // the slab's x has been read before its place is written again
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    };
+
+    // The next slab is on its way while one is multiplied.  Workgroups begin at different slabs of their part: rows
+    // lie a power of two apart more often than not, so that the same columns of all rows share a few memory
+    // channels, which all workgroups would use at the same time.
+    const uint32_t steps = (p.cols + kStepCols - 1) / kStepCols, slabs = (steps + S::kSlab - 1) / S::kSlab;
+    const uint32_t begin = wave * p.slabs_per_wave, end = min(begin + p.slabs_per_wave, slabs);
+    const uint32_t count = end > begin ? end - begin : 0;
+    uint32_t at = count ? blockIdx.x % count : 0;
+    const auto following = [&](uint32_t i) { return i + 1 < count ? i + 1 : 0; };
+    Loads one = load(begin + at, 0);
+    for (uint32_t i = 0; i < count; i += 2) {
+        const uint32_t at1 = following(at), at2 = following(at1);
+        Loads two = load(i + 1 < count ? begin + at1 : slabs, 1);   // past the last one: zeros
+        process(one, begin + at, 0);
+        if (i + 1 >= count) break;
+        one = load(i + 2 < count ? begin + at2 : slabs, 0);
+        process(two, begin + at1, 1);
+        at = at2;
+    }
+
+    // the waves in order; nothing is on its way into LDS any more
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    float* const sums = reinterpret_cast<float*>(lds);   // [wave][kVecs][16 kTiles]
+    constexpr uint32_t kOut = kVecs * 16 * kTiles;
+    static_assert(kOut * 4 <= S::kWaveBytes, "the sums fit where x was");
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e)
+            if (q * 4 + e < kVecs) sums[wave * kOut + (q * 4 + e) * 16 * kTiles + i * 16 + r] = acc[i][e];
+    __syncthreads();
+    for (uint32_t o = threadIdx.x; o < kOut; o += blockDim.x) {
+        const uint32_t v = o / (16 * kTiles), row = row0 + o % (16 * kTiles);
+        if (v >= p.vecs || row >= p.rows) continue;
+        float sum = sums[o];
+        for (uint32_t k = 1; k < waves; ++k) sum += sums[k * kOut + o];
+        p.y[(uint64_t)v * p.rows + row] = sum;
+    }
+}
+
+template <int kVecs, int kTiles>
+void launch(Q4Params& p, uint32_t waves, hipStream_t s) {
+    using S = Q4Shape<kVecs>;
+    const uint32_t steps = (p.cols + kStepCols - 1) / kStepCols, slabs = (steps + S::kSlab - 1) / S::kSlab;
+    waves = waves < slabs ? waves : slabs;
+    p.slabs_per_wave = (slabs + waves - 1) / waves;
+    waves = (slabs + p.slabs_per_wave - 1) / p.slabs_per_wave;
+    const dim3 grid((p.rows + 16 * kTiles - 1) / (16 * kTiles)), block(64 * waves);
+    const uint32_t bytes = waves * S::kWaveBytes + 16;
+    const auto go = [&](auto* kernel) { hipLaunchKernelGGL(kernel, grid, block, bytes, s, p); };
+    const bool whole = p.cols % 32 == 0;
+    if (!whole) return go(gemv_q4_kernel<kVecs, kTiles, 1, false, true>);
+    if (p.group % 128 == 0 || p.group >= p.cols)
+        p.zeros ? go(gemv_q4_kernel<kVecs, kTiles, 4, true, true>) : go(gemv_q4_kernel<kVecs, kTiles, 4, true, false>);
+    else if (p.group % 64 == 0)
+        p.zeros ? go(gemv_q4_kernel<kVecs, kTiles, 2, true, true>) : go(gemv_q4_kernel<kVecs, kTiles, 2, true, false>);
+    else
+        p.zeros ? go(gemv_q4_kernel<kVecs, kTiles, 1, true, true>) : go(gemv_q4_kernel<kVecs, kTiles, 1, true, false>);
+}
+
+// Rows per workgroup: 16, so that small matrices still fill the card; 32, which
+// share the work on x, where there are vectors enough for that to count and
+// still a workgroup per CU.
+template <int kVecs>
+void launch_rows(Q4Params& p, hipStream_t s) {
+    if (kVecs >= 8 && p.rows >= 32 * 256) return launch<kVecs, 2>(p, 4, s);
+    launch<kVecs, 1>(p, kVecs >= 8 ? 8 : 4, s);
 }
 
 }  // namespace
@@ -82,11 +348,18 @@ extern "C" int wc_gemv_q4_async(const wc_q4_matrix* W, const uint16_t* x, uint32
     if (!x || !y || (reinterpret_cast<uintptr_t>(x) & 15u) || (reinterpret_cast<uintptr_t>(y) & 3u))
         return WC_ERR_INVALID_ARG;
     Q4Params p{};
-    p.codes = reinterpret_cast<const uint32_t*>(W->codes);
-    p.scales = W->scales, p.zeros = W->zeros, p.x = x, p.y = y;
-    p.rows = W->rows, p.cols = W->cols, p.group = W->group;
+    p.codes = W->codes, p.scales = W->scales, p.zeros = W->zeros, p.x = x, p.y = y;
+    p.rows = W->rows, p.cols = W->cols, p.group = W->group, p.vecs = n_vecs;
     p.groups = (W->cols + W->group - 1) / W->group;
-    hipLaunchKernelGGL(gemv_q4_kernel, dim3((W->rows + kQ4Waves - 1) / kQ4Waves, n_vecs), dim3(64 * kQ4Waves), 0,
-                       static_cast<hipStream_t>(stream), p);
+    // ceil(2^32 / m), m chunks per group: exact for fewer than 2^16 chunks of m < 2^16 (there are 2^11 at most)
+    const uint32_t m = W->group < W->cols ? W->group / 32 : 1u << 15;
+    p.group_magic = m == 1 ? 0 : (uint32_t)((0x100000000ull + m - 1) / m);
+    p.group_one = m == 1 ? ~0u : 0;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (n_vecs == 1) launch_rows<1>(p, s);
+    else if (n_vecs == 2) launch_rows<2>(p, s);
+    else if (n_vecs <= 4) launch_rows<4>(p, s);
+    else if (n_vecs <= 8) launch_rows<8>(p, s);
+    else launch_rows<16>(p, s);
     return hipGetLastError() == hipSuccess ? WC_OK : WC_ERR_HIP;
 }

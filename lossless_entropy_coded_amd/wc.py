@@ -377,6 +377,8 @@ def decode_u8_async(plan: Plan, blob_dev, out_dev, stream=None) -> None:
 def _stream_handle(stream) -> int:
     if stream is None:
         import torch
+        if torch.cuda.is_initialized():   # the handle itself: a Stream object costs 3 us
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return int(torch.cuda.current_stream().cuda_stream)
     if hasattr(stream, "cuda_stream"):
         return int(stream.cuda_stream)
@@ -412,6 +414,8 @@ def stream_reference_async(src_dev, src_bytes: int, dst_dev, dst_bytes: int, str
 
 def _current_device():
     import torch
+    if torch.cuda.is_initialized():
+        return torch._C._cuda_getDevice()
     return torch.cuda.current_device() if torch.cuda.is_available() else None
 
 
@@ -491,7 +495,7 @@ def _bytes_ok(t, nbytes: int, device, what: str, call: str) -> int:
 def _sizes(call: str, **sizes) -> None:
     """Sizes must be whole numbers that the C types hold; C checks the rest."""
     for what, v in sizes.items():
-        if not 0 <= v < 1 << 32:
+        if not 0 <= v <= 0xFFFFFFFF:
             raise WCError(WC_ERR_INVALID_ARG, call, f"{what} is {v}")
 
 
