@@ -67,6 +67,7 @@ struct Q4Shape {
     static constexpr uint32_t kCopies = kXBytes / 1024;
     static_assert(kXBytes % 1024 == 0, "whole copies");
     static constexpr uint32_t kWaveBytes = 2 * kXBytes;
+    static constexpr uint32_t kNoneBytes = kSlab * 256;
 };
 
 __device__ __forceinline__ float bf16_f32(uint32_t b) { return __uint_as_float(b << 16); }
@@ -77,7 +78,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, uint64_t
 
 // (code - 8) / 16 in bf16 for the 8 codes of a dword (^ 0x88888888: signed nibbles), in order.
 __device__ __forceinline__ bf16x8 weights(uint32_t codes) {
-    const uint32_t even = codes ^ 0x88888888u, odd = even >> 4;
+    const uint32_t even = codes ^ 0x88888888u;
+    uint32_t odd = even >> 4;
+    asm("" : "+v"(odd));   // else each byte of it is taken from `even` with an operation of its own
     u32x4 w;
 #pragma unroll
     for (uint32_t i = 0; i < 4; ++i)
@@ -148,8 +151,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t waves = blockDim.x >> 6;
     uint8_t* const xs = lds + wave * S::kWaveBytes;
-    uint8_t* const none = lds + waves * S::kWaveBytes;   // 16 zero bytes: vectors that are not there
-    if (threadIdx.x < 4) reinterpret_cast<uint32_t*>(none)[threadIdx.x] = 0;
+    uint8_t* const none = lds + waves * S::kWaveBytes;   // zeros, for vectors that are not there
+    for (uint32_t i = threadIdx.x; i < S::kNoneBytes / 4; i += blockDim.x) reinterpret_cast<uint32_t*>(none)[i] = 0;
     __syncthreads();
 
     const uint32_t r = lane & 15u, q = lane >> 4;   // weight row of a tile (or vector, holding x); chunk of a step
@@ -160,11 +163,21 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
     const auto zero_buf = buffer(p.zeros + (uint64_t)row0 * p.groups, p.zeros ? (uint64_t)rows * p.groups : 0);
     const uint32_t no_zeros = p.zeros ? 0 : 8;
     const auto x_buf = buffer(p.x, (uint64_t)p.vecs * p.cols * 2);
+    uint32_t code_at[kTiles], group_at[kTiles];   // of the lane's rows; those past the last repeat it
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+        const uint32_t row = min(i * 16 + r, rows - 1);
+        code_at[i] = row * row_bytes + q * 16;
+        group_at[i] = row * p.groups;
+    }
 
     // Where the lane reads its vector's x.  64-byte pieces of a step stand at piece ^ (vector & 3), so that four
     // vectors' lie in different banks.
     const bool there = r < (uint32_t)kVecs;
-    const uint32_t x_at = r * S::kRowBytes + q * 16;
+    const uint8_t* x_at[4];
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j)
+        x_at[j] = there ? xs + r * S::kRowBytes + q * 16 + ((j ^ (r & 3u)) * 64) : none;
 
     // Start the loads of a slab: x first, which has arrived when the registers have.
     const auto load = [&](uint32_t slab, uint32_t half) {
@@ -177,26 +190,37 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
             copy_to_lds_counted(xs + half * S::kXBytes + k * 1024, x_buf,
                                 v < p.vecs && c < p.cols ? (v * p.cols + c) * 2 : kNoChunk);
         }
+        // the loads below stay behind the copies: loads return in order, which process() relies on
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (uint32_t st = 0; st < S::kSlab; ++st) {
-            const uint32_t c = c0 + st * kStepCols + q * 32;
-            const uint32_t g = __umulhi(c / 32, p.group_magic) + (c / 32 & p.group_one);
+            const uint32_t cs = c0 + st * kStepCols, c = cs + q * 32;
+            const bool inside = c < p.cols;
+            // one group for the step (a scalar), or each lane's own chunk's
+            const uint32_t chunk = (kBlock == 4 ? min(cs, p.cols - 1) : min(c, p.cols - 1)) / 32;
+            const uint32_t g = __umulhi(chunk, p.group_magic) + (chunk & p.group_one);
 #pragma unroll
             for (int i = 0; i < kTiles; ++i) {
-                const uint32_t row = i * 16 + r, at = row * row_bytes + c / 2;
                 if (kWhole) {
                     l.w[st][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                        codes_buf, c < p.cols ? at : kNoChunk, 0, 0));
+                        codes_buf, inside ? code_at[i] : kNoChunk, cs / 2, 0));
                 } else {
 #pragma unroll
                     for (uint32_t d = 0; d < 4; ++d)
                         l.w[st][i][d] = __builtin_amdgcn_raw_buffer_load_b32(
-                            codes_buf, c + d * 8 < p.cols ? at + d * 4 : kNoChunk, 0, 0);
+                            codes_buf, c + d * 8 < p.cols ? code_at[i] + d * 4 : kNoChunk, cs / 2, 0);
                 }
-                const uint32_t at_g = c < p.cols ? row * p.groups + g : kNoChunk / 2;
-                l.scale[st][i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(scale_buf, at_g * 2, 0, 0);
-                l.zero[st][i] =   // the buffer is empty where none are given
-                    kGiven ? (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(zero_buf, at_g, 0, 0) + no_zeros : 8u;
+                if (kBlock == 4) {
+                    l.scale[st][i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(scale_buf, group_at[i] * 2, g * 2, 0);
+                    l.zero[st][i] = kZeros ? (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(zero_buf, group_at[i], g, 0) : 8u;
+                } else {
+                    l.scale[st][i] =
+                        (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(scale_buf, (group_at[i] + g) * 2, 0, 0);
+                    l.zero[st][i] =   // the buffer is empty where none are given
+                        kGiven ? (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(zero_buf, group_at[i] + g, 0, 0) + no_zeros
+                               : 8u;
+                }
             }
         }
         __builtin_amdgcn_sched_barrier(0);   // started before what is multiplied next
@@ -210,17 +234,17 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
     const auto process = [&](Loads& l, uint32_t slab, uint32_t half) {
         // the registers loaded last have arrived, so x has too
         asm volatile("" : "+v"(l.scale[S::kSlab - 1][kTiles - 1]), "+v"(l.w[S::kSlab - 1][kTiles - 1])::"memory");
-        const uint8_t* const from = there ? xs + half * S::kXBytes + x_at : none;
+        const uint32_t skip = there ? half * S::kXBytes : 0;
 #pragma unroll
         for (uint32_t st = 0; st < S::kSlab; ++st) {
             bf16x8 x[4];
 #pragma unroll
-            for (uint32_t j = 0; j < 4; ++j)
-                x[j] = *reinterpret_cast<const bf16x8*>(from + (there ? st * 256 + ((j ^ (r & 3u)) * 64) : 0));
+            for (uint32_t j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const bf16x8*>(x_at[j] + skip + st * 256);
 #pragma unroll
             for (int i = 0; i < kTiles; ++i) {
                 const u32x4 w = transpose_rows(l.w[st][i]);
-                const u32x4 sz = spread_rows(l.scale[st][i] << 16 | l.zero[st][i]);
+                const uint32_t own = kGiven ? l.scale[st][i] << 16 | l.zero[st][i] : l.scale[st][i] << 16;
+                const u32x4 sz = kBlock == 4 ? u32x4{own, own, own, own} : spread_rows(own);
                 const bool far = kGiven && __any(l.zero[st][i] > 128u);
 #pragma unroll
                 for (uint32_t b = 0; b < 4 / kBlock; ++b) {
@@ -303,7 +327,7 @@ void launch(Q4Params& p, uint32_t waves, hipStream_t s) {
     p.slabs_per_wave = (slabs + waves - 1) / waves;
     waves = (slabs + p.slabs_per_wave - 1) / p.slabs_per_wave;
     const dim3 grid((p.rows + 16 * kTiles - 1) / (16 * kTiles)), block(64 * waves);
-    const uint32_t bytes = waves * S::kWaveBytes + 16;
+    const uint32_t bytes = waves * S::kWaveBytes + S::kNoneBytes;
     const auto go = [&](auto* kernel) { hipLaunchKernelGGL(kernel, grid, block, bytes, s, p); };
     const bool whole = p.cols % 32 == 0;
     if (!whole) return go(gemv_q4_kernel<kVecs, kTiles, 1, false, true>);
