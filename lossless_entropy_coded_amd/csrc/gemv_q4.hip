@@ -11,16 +11,25 @@
 // vector units keep up: at 8 TB/s a CU has 2.4 operations per weight, and
 // converting and multiplying weights one at a time takes that for one vector
 // and more for each further one.  So the products are the matrix cores':
-//   - v_mfma_f32_16x16x32_bf16, its 16 rows the vectors (those not there are
+//   - v_mfma_f32_16x16x32_f16, its 16 rows the vectors (those not there are
 //     zero), its 16 columns weight rows, 32 columns of W at a time;
-//   - a code's signed value code - 8 becomes bf16 (exactly, over 16) with one
-//     conversion, v_cvt_off_f32_i4 on a selected byte, and half a byte
-//     permutation: 1.75 operations per weight whatever the number of vectors;
-//     With zero points, code less zero point is made as a signed byte first
-//     (2.4 operations per weight): subtracting zero * sum(x) afterwards would
-//     lose small products next to a large x that its zero point cancels;
-//   - the products are exact in fp32 and sums are held in fp32; a group's sum
-//     times its scale is added to the row's.
+//   - code less zero point is made exactly in f16, two at a time: a nibble put
+//     into the mantissa of 1024 is 1024 + code (four bits higher: 1024 + 16
+//     code), and one packed addition of -(1024 + zero) (or one packed fma, by
+//     1 / 16, of -(64 + zero)) leaves the difference: 9 operations per 8
+//     weights whatever the zero point and the number of vectors;
+//   - x is scaled by a power of two, so that the largest value of a vector's
+//     slab of 128 to 512 columns is just below 2^16, and put into f16.  That
+//     is exact for values down to 2^-32 of the largest (a bf16 value has 8
+//     significant bits), and off by less than 2^-39 of it below; an infinity
+//     or NaN stays one;
+//   - the products are exact in fp32 and sums are held in fp32: a group's sum
+//     times its scale is added to the slab's, the slab's times its power of
+//     two to the row's.
+// (Subtracting zero * sum(x) from sum(code x) instead would lose small products
+// next to a large x that its zero point cancels.  bf16 in place of f16, code
+// by code through v_cvt_off_f32_i4, needs no scaling of x but 1.75 operations
+// per weight, 2.4 with zero points: 12.2 us at 14336 x 4096, one vector.)
 //
 // A wave takes 16 kTiles rows and a part of the columns, 128 columns per step:
 // lane (r, q) loads the 16 bytes of row r's q-th 32 columns, four rows of lanes
@@ -33,17 +42,20 @@
 #include <cstdint>
 
 #include "../../include/wc.h"
-#include "lds_copy.h"
 
 namespace wc {
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr uint32_t kStepCols = 128;
 constexpr uint32_t kMaxWaves = 8;
+constexpr uint32_t kNoChunk = 0xFFFFFFF0u;   // a buffer offset beyond every operand: loads zeros
 
 struct Q4Params {
     const uint8_t* codes;
@@ -58,15 +70,15 @@ struct Q4Params {
 };
 
 // A slab is what a wave has on its way at a time: kSlab steps.  LDS of one wave:
-// x of two slabs, [vector][column], 1 KB per copy.
+// x of a slab in f16, [vector][column], and 2^(E - 15) of each vector, 2^E the
+// largest power of two in its slab.
 template <int kVecs>
 struct Q4Shape {
     static constexpr uint32_t kSlab = kVecs == 1 ? 4 : kVecs == 16 ? 1 : 2;
     static constexpr uint32_t kRowBytes = kSlab * kStepCols * 2;   // of one vector
+    static constexpr uint32_t kRounds = kVecs * kSlab / 4;         // 64 lanes of 8 columns
     static constexpr uint32_t kXBytes = kVecs * kRowBytes;
-    static constexpr uint32_t kCopies = kXBytes / 1024;
-    static_assert(kXBytes % 1024 == 0, "whole copies");
-    static constexpr uint32_t kWaveBytes = 2 * kXBytes;
+    static constexpr uint32_t kWaveBytes = kXBytes + 64;
     static constexpr uint32_t kNoneBytes = kSlab * 256;
 };
 
@@ -76,31 +88,37 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, uint64_t
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)(uint32_t)bytes, 0x00027000);
 }
 
-// (code - 8) / 16 in bf16 for the 8 codes of a dword (^ 0x88888888: signed nibbles), in order.
-__device__ __forceinline__ bf16x8 weights(uint32_t codes) {
-    const uint32_t even = codes ^ 0x88888888u;
-    uint32_t odd = even >> 4;
-    asm("" : "+v"(odd));   // else each byte of it is taken from `even` with an operation of its own
-    u32x4 w;
+// code - zero point in f16 for the 8 codes of a dword, in the order 0 4 1 5 2 6 3 7; by1: -(1024 + zero point), by16:
+// -(64 + zero point), both twice.
+__device__ __forceinline__ f16x8 weights(uint32_t codes, f16x2 by1, f16x2 by16) {
+    const f16x2 sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
+    f16x2 w[4];
 #pragma unroll
-    for (uint32_t i = 0; i < 4; ++i)
-        w[i] = __builtin_amdgcn_perm(
-            __float_as_uint(__builtin_amdgcn_cvt_off_f32_i4((odd >> (8 * i)) & 0xFFu)),
-            __float_as_uint(__builtin_amdgcn_cvt_off_f32_i4((even >> (8 * i)) & 0xFFu)), 0x07060302u);
-    return __builtin_bit_cast(bf16x8, w);
+    for (uint32_t i = 0; i < 2; ++i, codes >>= 8) {
+        w[2 * i] = __builtin_bit_cast(f16x2, (codes & 0x000F000Fu) | 0x64006400u) + by1;
+        w[2 * i + 1] = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, (codes & 0x00F000F0u) | 0x64006400u),
+                                                 sixteenth, by16);
+    }
+    return __builtin_bit_cast(f16x8, u32x4{__builtin_bit_cast(uint32_t, w[0]), __builtin_bit_cast(uint32_t, w[1]),
+                                           __builtin_bit_cast(uint32_t, w[2]), __builtin_bit_cast(uint32_t, w[3])});
 }
 
-// code - zero point, at most 128 (four times in zz), in bf16 for the 8 codes of a dword, in order: bytes
-// 128 + code - zero point, which borrow nothing from each other, less 128.
-__device__ __forceinline__ bf16x8 weights(uint32_t codes, uint32_t zz) {
-    const uint32_t even = (((codes & 0x0F0F0F0Fu) | 0x80808080u) - zz) ^ 0x80808080u;
-    const uint32_t odd = ((((codes >> 4) & 0x0F0F0F0Fu) | 0x80808080u) - zz) ^ 0x80808080u;
-    u32x4 w;
-#pragma unroll
-    for (uint32_t i = 0; i < 4; ++i)
-        w[i] = __builtin_amdgcn_perm(__float_as_uint((float)(int8_t)(odd >> (8 * i))),
-                                     __float_as_uint((float)(int8_t)(even >> (8 * i))), 0x07060302u);
-    return __builtin_bit_cast(bf16x8, w);
+// The largest value of the lanes in 16 kRows lanes.
+template <int kRows>
+__device__ __forceinline__ uint32_t largest(uint32_t v) {
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));    // lane ^ 1
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));    // lane ^ 2
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true));   // half row mirrored
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, true));   // row mirrored
+    if (kRows >= 2) {
+        const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(v, v, false, false));
+        v = max(a.x, a.y);
+    }
+    if (kRows >= 4) {
+        const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(v, v, false, false));
+        v = max(a.x, a.y);
+    }
+    return v;
 }
 
 // Transposes four dwords of four rows of 16 lanes: out[j] in row q is in[q] of row j.
@@ -120,22 +138,19 @@ __device__ __forceinline__ u32x4 spread_rows(uint32_t v) {
     return u32x4{lo.x, lo.y, hi.x, hi.y};
 }
 
-// The products of n columns of one weight row with x, term by term.
-__device__ __attribute__((noinline)) float exact_block(const uint16_t* x, const uint8_t* codes, uint32_t n,
-                                                       float scale, float zero) {
-    float sum = 0.0f;
-    for (uint32_t i = 0; i < n; ++i)
-        sum += scale * ((float)(i & 1 ? codes[i / 2] >> 4 : codes[i / 2] & 15u) - zero) * bf16_f32(x[i]);
-    return sum;
-}
-
-// What a wave has in registers for one slab: its codes, and scale bits << 16 |
-// zero point of each lane's chunk.
-template <int kSlab, int kTiles>
+// What a wave has in registers for one slab: its codes, scale bits and zero
+// points, and x.  A row's scales, of the slab's blocks of kBlock chunks, are
+// loaded four at a time, one by each row of lanes: loads of two bytes by 64
+// lanes cost as much as loads of sixteen (one per step: 12.2 us at 14336 x
+// 4096, one vector; without any: 7.4).
+template <int kVecs, int kTiles, int kBlock>
 struct Slab {
-    u32x4 w[kSlab][kTiles];
-    uint32_t scale[kSlab][kTiles];
-    uint32_t zero[kSlab][kTiles];
+    using S = Q4Shape<kVecs>;
+    static constexpr uint32_t kBlocks = S::kSlab * 4 / kBlock, kScales = (kBlocks + 3) / 4;
+    u32x4 w[S::kSlab][kTiles];
+    uint32_t scale[kScales][kTiles];
+    uint32_t zero[kScales][kTiles];
+    u32x4 x[S::kRounds];
 };
 
 // kVecs: vectors, rounded up.  kBlock: chunks of 32 columns (1, 2 or 4) that
@@ -146,13 +161,15 @@ template <int kVecs, int kTiles, int kBlock, bool kWhole, bool kZeros>
 __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
     using S = Q4Shape<kVecs>;
     constexpr bool kGiven = kZeros || !kWhole;
-    using Loads = Slab<S::kSlab, kTiles>;
+    using Loads = Slab<kVecs, kTiles, kBlock>;
     extern __shared__ __align__(16) uint8_t lds[];
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t waves = blockDim.x >> 6;
     uint8_t* const xs = lds + wave * S::kWaveBytes;
+    float* const units = reinterpret_cast<float*>(xs + S::kXBytes);
     uint8_t* const none = lds + waves * S::kWaveBytes;   // zeros, for vectors that are not there
     for (uint32_t i = threadIdx.x; i < S::kNoneBytes / 4; i += blockDim.x) reinterpret_cast<uint32_t*>(none)[i] = 0;
+    if (lane < 16) units[lane] = 0.0f;
     __syncthreads();
 
     const uint32_t r = lane & 15u, q = lane >> 4;   // weight row of a tile (or vector, holding x); chunk of a step
@@ -179,27 +196,20 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
     for (uint32_t j = 0; j < 4; ++j)
         x_at[j] = there ? xs + r * S::kRowBytes + q * 16 + ((j ^ (r & 3u)) * 64) : none;
 
-    // Start the loads of a slab: x first, which has arrived when the registers have.
-    const auto load = [&](uint32_t slab, uint32_t half) {
+    // Start the loads of a slab.
+    const auto load = [&](uint32_t slab) {
         Loads l;
         const uint32_t c0 = slab * S::kSlab * kStepCols;
 #pragma unroll
-        for (uint32_t k = 0; k < S::kCopies; ++k) {
-            const uint32_t to = k * 1024 + lane * 16, v = to / S::kRowBytes, b = to % S::kRowBytes;
-            const uint32_t c = c0 + (b ^ ((v & 3u) * 64)) / 2;
-            copy_to_lds_counted(xs + half * S::kXBytes + k * 1024, x_buf,
-                                v < p.vecs && c < p.cols ? (v * p.cols + c) * 2 : kNoChunk);
+        for (uint32_t round = 0; round < S::kRounds; ++round) {
+            const uint32_t job = round * 4 + q, v = job / S::kSlab, c = c0 + job % S::kSlab * kStepCols + r * 8;
+            l.x[round] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                x_buf, v < p.vecs && c < p.cols ? (v * p.cols + c) * 2 : kNoChunk, 0, 0));
         }
-        // the loads below stay behind the copies: loads return in order, which process() relies on
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (uint32_t st = 0; st < S::kSlab; ++st) {
             const uint32_t cs = c0 + st * kStepCols, c = cs + q * 32;
             const bool inside = c < p.cols;
-            // one group for the step (a scalar), or each lane's own chunk's
-            const uint32_t chunk = (kBlock == 4 ? min(cs, p.cols - 1) : min(c, p.cols - 1)) / 32;
-            const uint32_t g = __umulhi(chunk, p.group_magic) + (chunk & p.group_one);
 #pragma unroll
             for (int i = 0; i < kTiles; ++i) {
                 if (kWhole) {
@@ -211,16 +221,18 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
                         l.w[st][i][d] = __builtin_amdgcn_raw_buffer_load_b32(
                             codes_buf, c + d * 8 < p.cols ? code_at[i] + d * 4 : kNoChunk, cs / 2, 0);
                 }
-                if (kBlock == 4) {
-                    l.scale[st][i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(scale_buf, group_at[i] * 2, g * 2, 0);
-                    l.zero[st][i] = kZeros ? (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(zero_buf, group_at[i], g, 0) : 8u;
-                } else {
-                    l.scale[st][i] =
-                        (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(scale_buf, (group_at[i] + g) * 2, 0, 0);
-                    l.zero[st][i] =   // the buffer is empty where none are given
-                        kGiven ? (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(zero_buf, group_at[i] + g, 0, 0) + no_zeros
-                               : 8u;
-                }
+            }
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < Loads::kScales; ++k) {
+            const uint32_t block = k * 4 + min(q, Loads::kBlocks - 1);
+            const uint32_t chunk = min(c0 + block * kBlock * 32, p.cols - 1) / 32;
+            const uint32_t g = __umulhi(chunk, p.group_magic) + (chunk & p.group_one);
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+                l.scale[k][i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(scale_buf, (group_at[i] + g) * 2, 0, 0);
+                l.zero[k][i] =   // the buffer is empty where none are given
+                    kGiven ? (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(zero_buf, group_at[i] + g, 0, 0) + no_zeros : 8u;
             }
         }
         __builtin_amdgcn_sched_barrier(0);   // started before what is multiplied next
@@ -231,52 +243,72 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    const auto process = [&](Loads& l, uint32_t slab, uint32_t half) {
-        // the registers loaded last have arrived, so x has too
-        asm volatile("" : "+v"(l.scale[S::kSlab - 1][kTiles - 1]), "+v"(l.w[S::kSlab - 1][kTiles - 1])::"memory");
-        const uint32_t skip = there ? half * S::kXBytes : 0;
+    const auto process = [&](const Loads& l) {
+        // x to f16, 8 columns per lane
+#pragma unroll
+        for (uint32_t round = 0; round < S::kRounds; ++round) {
+            const uint32_t job = round * 4 + q, v = job / S::kSlab, st = job % S::kSlab;
+            const u32x4 xw = l.x[round];
+            u16x2 m = __builtin_bit_cast(u16x2, xw[0] & 0x7FFF7FFFu);
+#pragma unroll
+            for (uint32_t i = 1; i < 4; ++i)
+                m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, xw[i] & 0x7FFF7FFFu));
+            const int e = (int)(largest<S::kSlab>(max((uint32_t)m.x, (uint32_t)m.y)) >> 7);   // E + 127
+            u32x4 to;
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) {   // columns i and i + 4
+                const float lo = __uint_as_float(i & 1 ? xw[i / 2] & 0xFFFF0000u : xw[i / 2] << 16);
+                const float hi = __uint_as_float(i & 1 ? xw[i / 2 + 2] & 0xFFFF0000u : xw[i / 2 + 2] << 16);
+                to[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(__builtin_ldexpf(lo, 142 - e),
+                                                                               __builtin_ldexpf(hi, 142 - e)));
+            }
+            *reinterpret_cast<u32x4*>(xs + v * S::kRowBytes + st * 256 + ((r * 16) ^ ((v & 3u) * 64))) = to;
+            if (st == 0 && r == 0) units[v] = __builtin_ldexpf(1.0f, e - 142);
+        }
+        // the wave's lanes exchange x through its own LDS, which it accesses in order
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+
+        u32x4 words[Loads::kScales][kTiles];   // scale bits << 16 | zero point of four blocks, in every row of lanes
+#pragma unroll
+        for (uint32_t k = 0; k < Loads::kScales; ++k)
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i)
+                words[k][i] = spread_rows(kGiven ? l.scale[k][i] << 16 | l.zero[k][i] : l.scale[k][i] << 16);
+        f32x4 sum[kTiles];
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) sum[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (uint32_t st = 0; st < S::kSlab; ++st) {
-            bf16x8 x[4];
+            f16x8 x[4];
 #pragma unroll
-            for (uint32_t j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const bf16x8*>(x_at[j] + skip + st * 256);
+            for (uint32_t j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const f16x8*>(x_at[j] + st * 256);
 #pragma unroll
             for (int i = 0; i < kTiles; ++i) {
                 const u32x4 w = transpose_rows(l.w[st][i]);
-                const uint32_t own = kGiven ? l.scale[st][i] << 16 | l.zero[st][i] : l.scale[st][i] << 16;
-                const u32x4 sz = kBlock == 4 ? u32x4{own, own, own, own} : spread_rows(own);
-                const bool far = kGiven && __any(l.zero[st][i] > 128u);
 #pragma unroll
                 for (uint32_t b = 0; b < 4 / kBlock; ++b) {
-                    const uint32_t word = sz[b * kBlock];
+                    const uint32_t block = st * (4 / kBlock) + b, word = words[block / 4][i][block % 4];
+                    const uint32_t z = kGiven ? word & 0xFFu : 8u;
                     const float scale = __uint_as_float(word & 0xFFFF0000u);
-                    if (far) {   // no 4-bit code's zero point, but a byte may hold it
-                        const uint32_t c = (slab * S::kSlab + st) * kStepCols + b * kBlock * 32;
-                        const uint32_t row = row0 + i * 16 + r;
-#pragma unroll
-                        for (uint32_t e = 0; e < 4; ++e) {
-                            const uint32_t v = q * 4 + e;
-                            if (v < p.vecs && row < p.rows && c < p.cols)
-                                acc[i][e] += exact_block(p.x + (uint64_t)v * p.cols + c,
-                                                         p.codes + (uint64_t)row * row_bytes + c / 2,
-                                                         min(kBlock * 32u, p.cols - c), scale, (float)(word & 0xFFu));
-                        }
-                        continue;
-                    }
-                    const uint32_t zz = __builtin_amdgcn_perm(0, word, 0);
+                    const f16x2 by1 = __builtin_bit_cast(f16x2, z * 0x00010001u + 0xE400E400u);
+                    const f16x2 by16 = by1 + f16x2{(_Float16)960.0f, (_Float16)960.0f};
                     f32x4 D = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (uint32_t j = b * kBlock; j < (b + 1) * kBlock; ++j)
-                        D = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[j], kGiven ? weights(w[j], zz) : weights(w[j]), D,
-                                                                     0, 0, 0);
-                    const float by = kGiven ? scale : scale * 16.0f;
+                        D = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[j], weights(w[j], by1, by16), D, 0, 0, 0);
 #pragma unroll
-                    for (uint32_t e = 0; e < 4; ++e) acc[i][e] = __builtin_fmaf(D[e], by, acc[i][e]);
+                    for (uint32_t e = 0; e < 4; ++e) sum[i][e] = __builtin_fmaf(D[e], scale, sum[i][e]);
                 }
             }
         }
-        // the slab's x has been read before its place is written again
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        const f32x4 unit = *reinterpret_cast<const f32x4*>(units + q * 4);   // of vectors 4 q ..
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e) acc[i][e] = __builtin_fmaf(sum[i][e], unit[e], acc[i][e]);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
     };
 
     // The next slab is on its way while one is multiplied.  Workgroups begin at different slabs of their part: rows
@@ -287,19 +319,18 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
     const uint32_t count = end > begin ? end - begin : 0;
     uint32_t at = count ? blockIdx.x % count : 0;
     const auto following = [&](uint32_t i) { return i + 1 < count ? i + 1 : 0; };
-    Loads one = load(begin + at, 0);
+    Loads one = load(begin + at);
     for (uint32_t i = 0; i < count; i += 2) {
         const uint32_t at1 = following(at), at2 = following(at1);
-        Loads two = load(i + 1 < count ? begin + at1 : slabs, 1);   // past the last one: zeros
-        process(one, begin + at, 0);
+        const Loads two = load(i + 1 < count ? begin + at1 : slabs);   // past the last one: zeros
+        process(one);
         if (i + 1 >= count) break;
-        one = load(i + 2 < count ? begin + at2 : slabs, 0);
-        process(two, begin + at1, 1);
+        one = load(i + 2 < count ? begin + at2 : slabs);
+        process(two);
         at = at2;
     }
 
-    // the waves in order; nothing is on its way into LDS any more
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    // the waves in order
     __syncthreads();
     float* const sums = reinterpret_cast<float*>(lds);   // [wave][kVecs][16 kTiles]
     constexpr uint32_t kOut = kVecs * 16 * kTiles;
