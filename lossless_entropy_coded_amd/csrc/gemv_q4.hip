@@ -88,16 +88,22 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, uint64_t
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)(uint32_t)bytes, 0x00027000);
 }
 
+// Constants in registers: an operation takes no second literal, and with these
+// "and" and "or" are one.
+struct Consts {
+    uint32_t low = 0x000F000Fu, high = 0x00F000F0u, magic = 0x64006400u;
+    __device__ __forceinline__ Consts() { asm("" : "+s"(low), "+s"(high), "+v"(magic)); }
+};
+
 // code - zero point in f16 for the 8 codes of a dword, in the order 0 4 1 5 2 6 3 7; by1: -(1024 + zero point), by16:
 // -(64 + zero point), both twice.
-__device__ __forceinline__ f16x8 weights(uint32_t codes, f16x2 by1, f16x2 by16) {
+__device__ __forceinline__ f16x8 weights(uint32_t codes, f16x2 by1, f16x2 by16, const Consts& k) {
     const f16x2 sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
     f16x2 w[4];
 #pragma unroll
     for (uint32_t i = 0; i < 2; ++i, codes >>= 8) {
-        w[2 * i] = __builtin_bit_cast(f16x2, (codes & 0x000F000Fu) | 0x64006400u) + by1;
-        w[2 * i + 1] = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, (codes & 0x00F000F0u) | 0x64006400u),
-                                                 sixteenth, by16);
+        w[2 * i] = __builtin_bit_cast(f16x2, (codes & k.low) | k.magic) + by1;
+        w[2 * i + 1] = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, (codes & k.high) | k.magic), sixteenth, by16);
     }
     return __builtin_bit_cast(f16x8, u32x4{__builtin_bit_cast(uint32_t, w[0]), __builtin_bit_cast(uint32_t, w[1]),
                                            __builtin_bit_cast(uint32_t, w[2]), __builtin_bit_cast(uint32_t, w[3])});
@@ -143,13 +149,15 @@ __device__ __forceinline__ u32x4 spread_rows(uint32_t v) {
 // loaded four at a time, one by each row of lanes: loads of two bytes by 64
 // lanes cost as much as loads of sixteen (one per step: 12.2 us at 14336 x
 // 4096, one vector; without any: 7.4).
-template <int kVecs, int kTiles, int kBlock>
+// kFour: a row's four scales of a step stand side by side and are loaded as one,
+// a step's by each row of lanes.
+template <int kVecs, int kTiles, int kBlock, bool kFour>
 struct Slab {
     using S = Q4Shape<kVecs>;
     static constexpr uint32_t kBlocks = S::kSlab * 4 / kBlock, kScales = (kBlocks + 3) / 4;
     u32x4 w[S::kSlab][kTiles];
-    uint32_t scale[kScales][kTiles];
-    uint32_t zero[kScales][kTiles];
+    uint32_t scale[kFour ? 2 : kScales][kTiles];
+    uint32_t zero[kFour ? 1 : kScales][kTiles];
     u32x4 x[S::kRounds];
 };
 
@@ -157,11 +165,11 @@ struct Slab {
 // always share a group.  kWhole: columns are a multiple of 32, so that a lane's
 // chunk is one 16-byte load; kZeros: zero points are given (they may be, if
 // not kWhole).
-template <int kVecs, int kTiles, int kBlock, bool kWhole, bool kZeros>
+template <int kVecs, int kTiles, int kBlock, bool kFour, bool kWhole, bool kZeros>
 __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
     using S = Q4Shape<kVecs>;
     constexpr bool kGiven = kZeros || !kWhole;
-    using Loads = Slab<kVecs, kTiles, kBlock>;
+    using Loads = Slab<kVecs, kTiles, kBlock, kFour>;
     extern __shared__ __align__(16) uint8_t lds[];
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t waves = blockDim.x >> 6;
@@ -196,15 +204,22 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
     for (uint32_t j = 0; j < 4; ++j)
         x_at[j] = there ? xs + r * S::kRowBytes + q * 16 + ((j ^ (r & 3u)) * 64) : none;
 
+    uint32_t x_from[S::kRounds];
+#pragma unroll
+    for (uint32_t round = 0; round < S::kRounds; ++round) {
+        const uint32_t job = round * 4 + q, v = job / S::kSlab;
+        x_from[round] = v < p.vecs ? (v * p.cols + job % S::kSlab * kStepCols + r * 8) * 2 : kNoChunk;
+    }
+
     // Start the loads of a slab.
     const auto load = [&](uint32_t slab) {
         Loads l;
         const uint32_t c0 = slab * S::kSlab * kStepCols;
 #pragma unroll
         for (uint32_t round = 0; round < S::kRounds; ++round) {
-            const uint32_t job = round * 4 + q, v = job / S::kSlab, c = c0 + job % S::kSlab * kStepCols + r * 8;
+            const uint32_t c = c0 + (round * 4 + q) % S::kSlab * kStepCols + r * 8;
             l.x[round] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                x_buf, v < p.vecs && c < p.cols ? (v * p.cols + c) * 2 : kNoChunk, 0, 0));
+                x_buf, c < p.cols ? x_from[round] : kNoChunk, c0 * 2, 0));
         }
 #pragma unroll
         for (uint32_t st = 0; st < S::kSlab; ++st) {
@@ -223,6 +238,16 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
                 }
             }
         }
+        if constexpr (kFour) {
+            const uint32_t first = min(slab * S::kSlab + min(q, S::kSlab - 1), p.cols / kStepCols - 1) * 4;
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+                const u32x2 s4 = __builtin_bit_cast(
+                    u32x2, __builtin_amdgcn_raw_buffer_load_b64(scale_buf, (group_at[i] + first) * 2, 0, 0));
+                l.scale[0][i] = s4.x, l.scale[1][i] = s4.y;
+                l.zero[0][i] = kGiven ? __builtin_amdgcn_raw_buffer_load_b32(zero_buf, group_at[i] + first, 0, 0) : 0;
+            }
+        } else
 #pragma unroll
         for (uint32_t k = 0; k < Loads::kScales; ++k) {
             const uint32_t block = k * 4 + min(q, Loads::kBlocks - 1);
@@ -239,6 +264,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
         return l;
     };
 
+    const Consts consts;
     f32x4 acc[kTiles];   // of weight row r and vectors 4 q ..  4 q + 3
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -270,11 +296,26 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
         __builtin_amdgcn_wave_barrier();
 
         u32x4 words[Loads::kScales][kTiles];   // scale bits << 16 | zero point of four blocks, in every row of lanes
+        if constexpr (kFour) {
 #pragma unroll
-        for (uint32_t k = 0; k < Loads::kScales; ++k)
+            for (int i = 0; i < kTiles; ++i) {
+                u32x4 own;   // of the row of lanes' step
 #pragma unroll
-            for (int i = 0; i < kTiles; ++i)
-                words[k][i] = spread_rows(kGiven ? l.scale[k][i] << 16 | l.zero[k][i] : l.scale[k][i] << 16);
+                for (uint32_t b = 0; b < 4; ++b) {
+                    const uint32_t two = l.scale[b / 2][i];
+                    own[b] = (b & 1 ? two & 0xFFFF0000u : two << 16) | (kGiven ? (l.zero[0][i] >> (8 * b)) & 0xFFu : 0);
+                }
+                own = transpose_rows(own);
+#pragma unroll
+                for (uint32_t k = 0; k < Loads::kScales; ++k) words[k][i] = spread_rows(own[k]);
+            }
+        } else {
+#pragma unroll
+            for (uint32_t k = 0; k < Loads::kScales; ++k)
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i)
+                    words[k][i] = spread_rows(kGiven ? l.scale[k][i] << 16 | l.zero[k][i] : l.scale[k][i] << 16);
+        }
         f32x4 sum[kTiles];
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) sum[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -296,7 +337,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
                     f32x4 D = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (uint32_t j = b * kBlock; j < (b + 1) * kBlock; ++j)
-                        D = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[j], weights(w[j], by1, by16), D, 0, 0, 0);
+                        D = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[j], weights(w[j], by1, by16, consts), D, 0, 0, 0);
 #pragma unroll
                     for (uint32_t e = 0; e < 4; ++e) sum[i][e] = __builtin_fmaf(D[e], scale, sum[i][e]);
                 }
@@ -360,23 +401,36 @@ void launch(Q4Params& p, uint32_t waves, hipStream_t s) {
     const dim3 grid((p.rows + 16 * kTiles - 1) / (16 * kTiles)), block(64 * waves);
     const uint32_t bytes = waves * S::kWaveBytes + S::kNoneBytes;
     const auto go = [&](auto* kernel) { hipLaunchKernelGGL(kernel, grid, block, bytes, s, p); };
-    const bool whole = p.cols % 32 == 0;
-    if (!whole) return go(gemv_q4_kernel<kVecs, kTiles, 1, false, true>);
+    if (p.cols % 32 != 0) return go(gemv_q4_kernel<kVecs, kTiles, 1, false, false, true>);
+    const bool zeros = p.zeros;
+    const bool four = p.group == 32 && p.cols % kStepCols == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 7u) == 0 &&
+                      (reinterpret_cast<uintptr_t>(p.zeros) & 3u) == 0;
     if (p.group % 128 == 0 || p.group >= p.cols)
-        p.zeros ? go(gemv_q4_kernel<kVecs, kTiles, 4, true, true>) : go(gemv_q4_kernel<kVecs, kTiles, 4, true, false>);
+        zeros ? go(gemv_q4_kernel<kVecs, kTiles, 4, false, true, true>)
+              : go(gemv_q4_kernel<kVecs, kTiles, 4, false, true, false>);
     else if (p.group % 64 == 0)
-        p.zeros ? go(gemv_q4_kernel<kVecs, kTiles, 2, true, true>) : go(gemv_q4_kernel<kVecs, kTiles, 2, true, false>);
+        zeros ? go(gemv_q4_kernel<kVecs, kTiles, 2, false, true, true>)
+              : go(gemv_q4_kernel<kVecs, kTiles, 2, false, true, false>);
+    else if (four)
+        zeros ? go(gemv_q4_kernel<kVecs, kTiles, 1, true, true, true>)
+              : go(gemv_q4_kernel<kVecs, kTiles, 1, true, true, false>);
     else
-        p.zeros ? go(gemv_q4_kernel<kVecs, kTiles, 1, true, true>) : go(gemv_q4_kernel<kVecs, kTiles, 1, true, false>);
+        zeros ? go(gemv_q4_kernel<kVecs, kTiles, 1, false, true, true>)
+              : go(gemv_q4_kernel<kVecs, kTiles, 1, false, true, false>);
 }
 
-// Rows per workgroup: 16, so that small matrices still fill the card; 32, which
-// share the work on x, where there are vectors enough for that to count and
-// still a workgroup per CU.
+// Rows and waves per workgroup.  From 8192 rows on there are workgroups of 16
+// rows enough for 4 waves each to fill the card (14336 x 4096, one vector: 9.4
+// us, with 8 waves 10.9); below, 8 waves split the columns further (4096 x
+// 14336: 8.7 us, with 4 waves 9.2).  32 rows share the work on x, where there
+// are vectors enough for that to count (8192 x 28672, 8 vectors: 43.5 us, with
+// 16 rows 51).
 template <int kVecs>
 void launch_rows(Q4Params& p, hipStream_t s) {
-    if (kVecs >= 8 && p.rows >= 32 * 256) return launch<kVecs, 2>(p, 4, s);
-    launch<kVecs, 1>(p, kVecs >= 8 ? 8 : 4, s);
+    const bool many = p.rows >= 8192;
+    if constexpr (kVecs >= 8)
+        if (many) return launch<kVecs, 2>(p, 4, s);
+    launch<kVecs, 1>(p, many ? 4 : 8, s);
 }
 
 }  // namespace

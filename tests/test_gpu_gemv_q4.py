@@ -175,3 +175,21 @@ def test_side_stream_and_graph(wc):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, eager[i])
+
+
+@pytest.mark.parametrize("vecs", [1, 2, 3, 8, 16])
+@pytest.mark.parametrize("cols", [128, 1152, 4096])
+def test_scales_off_their_alignment(wc, cols, vecs):
+    """Groups of 32 with scales and zero points that start off 8-byte places: the bits of aligned ones."""
+    rows, group = 21, 32
+    codes, scales, z, w = q4_case(rows, cols, group, True, cols)
+    x = torch.randn(vecs, cols, generator=torch.Generator().manual_seed(vecs)).to(torch.bfloat16)
+    groups = cols // group
+    shifted = torch.empty(rows * groups + 1, dtype=torch.bfloat16, device="cuda")[1:].reshape(rows, groups)
+    shifted_z = torch.empty(rows * groups + 3, dtype=torch.uint8, device="cuda")[3:].reshape(rows, groups)
+    shifted.copy_(scales), shifted_z.copy_(z)
+    log(f"case: gemv_q4 {rows}x{cols} group 32 vecs {vecs}, aligned and shifted scales")
+    y = _run(wc, wc.Q4Matrix(codes, scales, rows, cols, group, zeros=z), x.cuda())
+    assert within(y, x.double() @ w.t(), q4_tolerance(w, x.double()))
+    y2 = _run(wc, wc.Q4Matrix(codes, shifted, rows, cols, group, zeros=shifted_z), x.cuda())
+    assert torch.equal(y.view(torch.int32), y2.view(torch.int32))
