@@ -11,19 +11,26 @@
 // of bf16, 4 of codes), the tokens of a workgroup as many as fill it.
 //
 // The gradient sums each row's tokens in token order, so it is the same bits
-// on every run.  Keys {id, token} are sorted: blocks of 4096 in LDS, then every
-// key's place is its place in its block plus, for each other block, the number
-// of smaller keys there (a binary search; keys are distinct).  The sorted
-// tokens are cut into runs of kRun; a workgroup walks a run and sums each
-// row's tokens in fp32.  A row whose tokens lie in one run is finished there;
-// one that crosses runs leaves a partial sum per run, joined in run order by
-// the last kernel.  Rows without tokens are written as zeros (unless the call
-// accumulates) by further workgroups of the same launch.
+// on every run.  Tokens are sorted by row: blocks of 4096 by a bitonic network
+// whose keys (row, place in the block) fit 32 bits and stay in registers, four
+// per lane, with all but the ten widest of its 78 exchanges inside a wave
+// (about 10 us; 38 with every exchange through LDS and 64-bit keys).  Then
+// every token's place is its place in its block plus, for each other block,
+// the number of smaller keys there: binary searches over the blocks' sorted
+// rows, in LDS.  The sorted tokens
+// are cut into runs of kRun; a workgroup walks a run, eight rows of the
+// gradient on their way at a time, and sums each row's tokens in fp32.  A row
+// whose tokens lie in one run is finished there; one that crosses runs leaves
+// a partial sum per run, joined in run order by the last kernel.  Rows without
+// tokens are zero (unless the call accumulates): with a large table writing
+// them is most of the bytes, and the memory's rate for writes bounds the call,
+// so the table is set to zero beside the sort where that costs little.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
 
 #include "../../include/wc.h"
+#include "kernels.h"
 
 namespace wc {
 namespace {
@@ -94,71 +101,137 @@ __global__ __launch_bounds__(kLookupThreads) void embed_kernel(LookupParams p) {
 
 // ---- gradient --------------------------------------------------------------
 
-constexpr uint32_t kSortKeys = 4096;      // keys sorted in LDS by one workgroup
-constexpr uint32_t kSortThreads = 1024;
-constexpr uint32_t kRun = 32;             // sorted tokens per run
+constexpr uint32_t kSortThreads = 1024;   // a workgroup sorts four keys per thread
+constexpr uint32_t kRun = 32;             // sorted tokens per run at most
 constexpr uint32_t kSumThreads = 256;
 constexpr uint32_t kSumCols = kSumThreads * 8;   // columns per workgroup of the summing launch
+constexpr uint32_t kAhead = 8;            // tokens of a run on their way at a time
 constexpr uint32_t kFillRows = 16;        // rows per workgroup that looks for rows without tokens
 
 struct GradParams {
     const uint16_t* dout;
     const void* ids;
     void* dtable;
-    uint64_t* keys;       // blocks sorted (id << 32 | token)
-    uint64_t* sorted;
+    uint64_t* sorted;     // row << 32 | token, in order
     float* head;          // per run, the sum of its leading tokens whose row began in an earlier run
     float* tail;          // per run, the sum of its last row where that goes on in the next run
-    uint32_t id_bytes, n, vocab, dim, runs;
+    uint32_t id_bytes, n, vocab, dim, runs, run_log2;
     uint32_t bf16, accumulate;
     uint32_t col_blocks, row_blocks;
     float scale;
 };
 
-__global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(GradParams p, uint64_t* out) {
-    __shared__ uint64_t key[kSortKeys];
-    const uint32_t base = blockIdx.x * kSortKeys;
-    for (uint32_t i = threadIdx.x; i < kSortKeys; i += kSortThreads) {
-        const uint32_t t = base + i;
-        uint64_t k = ~0ull;
-        if (t < p.n) {
-            const int64_t id = id_at(p.ids, p.id_bytes, t);
-            const uint32_t row = id >= 0 && id < (int64_t)p.vocab ? (uint32_t)id : p.vocab;
-            k = (uint64_t)row << 32 | t;
-        }
-        key[i] = k;
+struct SortParams {
+    const void* ids;
+    uint32_t id_bytes, n, vocab;
+    uint32_t block_log2;   // keys per block: with a block's index beside it, a row fits 32 bits
+    uint32_t limit;        // the network's size: a power of two, >= 4
+    uint64_t* sorted;
+    uint32_t* rows;        // per block, in order (several blocks)
+    uint32_t* tokens;
+    uint32_t blocks;
+    u32x4* fill;           // memory that further workgroups of the launch set to zero
+    uint64_t fill_chunks;  // 16 bytes each
+};
+
+constexpr uint32_t kFillChunks = 2;   // per thread
+
+// The keys of a block in order: four per thread, keys 4 t .. 4 t + 3.
+__global__ __launch_bounds__(kSortThreads) void sort_block_kernel(SortParams p) {
+    __shared__ u32x4 shared[kSortThreads];
+    if (blockIdx.x >= p.blocks) {
+        uint64_t i = (uint64_t)(blockIdx.x - p.blocks) * blockDim.x * kFillChunks + threadIdx.x;
+#pragma unroll
+        for (uint32_t k = 0; k < kFillChunks; ++k, i += blockDim.x)
+            if (i < p.fill_chunks) __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, p.fill + i);
+        return;
     }
-    __syncthreads();
-    for (uint32_t size = 2; size <= kSortKeys; size <<= 1)
-        for (uint32_t stride = size >> 1; stride > 0; stride >>= 1) {
-            for (uint32_t i = threadIdx.x; i < kSortKeys / 2; i += kSortThreads) {
-                const uint32_t a = 2 * i - (i & (stride - 1)), b = a + stride;
-                const bool up = (a & size) == 0;
-                const uint64_t x = key[a], y = key[b];
-                if ((x > y) == up) key[a] = y, key[b] = x;
-            }
-            __syncthreads();
+    const uint32_t tid = threadIdx.x, base = blockIdx.x << p.block_log2;
+    const uint32_t count = min(p.n - base, 1u << p.block_log2);
+    u32x4 key;
+#pragma unroll
+    for (uint32_t e = 0; e < 4; ++e) {
+        const uint32_t i = tid * 4 + e;
+        uint32_t k = ~0u;
+        if (i < count) {
+            const int64_t id = id_at(p.ids, p.id_bytes, base + i);
+            k = (id >= 0 && id < (int64_t)p.vocab ? (uint32_t)id : p.vocab) << p.block_log2 | i;
         }
-    for (uint32_t i = threadIdx.x; i < kSortKeys && base + i < p.n; i += kSortThreads) out[base + i] = key[i];
+        key[e] = k;
+    }
+    const auto order = [&](uint32_t a, uint32_t b, bool up) {   // key[a] before key[b], or after it
+        const uint32_t lo = min(key[a], key[b]), hi = max(key[a], key[b]);
+        key[a] = up ? lo : hi;
+        key[b] = up ? hi : lo;
+    };
+    order(0, 1, true);
+    order(2, 3, false);
+    for (uint32_t size = 4; size <= p.limit; size <<= 1) {
+        const bool up = (tid * 4 & size) == 0;
+        for (uint32_t stride = size >> 1; stride >= 4; stride >>= 1) {
+            const uint32_t far = stride / 4;
+            u32x4 other;
+            if (far >= 64) {
+                __syncthreads();
+                shared[tid] = key;
+                __syncthreads();
+                other = shared[tid ^ far];
+            } else {
+#pragma unroll
+                for (uint32_t e = 0; e < 4; ++e) other[e] = (uint32_t)__shfl_xor((int)key[e], (int)far);
+            }
+            const bool low = ((tid & far) == 0) == up;
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e) key[e] = low ? min(key[e], other[e]) : max(key[e], other[e]);
+        }
+        order(0, 2, up);
+        order(1, 3, up);
+        order(0, 1, up);
+        order(2, 3, up);
+    }
+#pragma unroll
+    for (uint32_t e = 0; e < 4; ++e) {
+        const uint32_t i = tid * 4 + e;
+        if (i >= count) continue;
+        const uint32_t row = key[e] >> p.block_log2, token = base + (key[e] & ((1u << p.block_log2) - 1));
+        if (p.rows) {
+            p.rows[base + i] = row;
+            p.tokens[base + i] = token;
+        } else {
+            p.sorted[i] = (uint64_t)row << 32 | token;
+        }
+    }
 }
 
-__global__ __launch_bounds__(256) void embed_rank_kernel(GradParams p) {
-    const uint32_t i = blockIdx.x * 256 + threadIdx.x;
-    if (i >= p.n) return;
-    const uint64_t k = p.keys[i];
-    const uint32_t mine = i / kSortKeys;
-    uint32_t rank = i % kSortKeys;
-    for (uint32_t base = 0, b = 0; base < p.n; base += kSortKeys, ++b) {
-        if (b == mine) continue;
-        uint32_t lo = 0, hi = min(kSortKeys, p.n - base);   // keys [0, lo) are smaller, [hi, ..) larger
-        while (lo < hi) {
-            const uint32_t mid = (lo + hi) / 2;
-            if (p.keys[base + mid] < k) lo = mid + 1;
-            else hi = mid;
+constexpr uint32_t kRankThreads = 1024;
+constexpr uint32_t kRankKeys = 32768;   // rows of other blocks in LDS at a time (128 KB)
+
+// Every token's place: its place in its block, and the smaller keys of the
+// other blocks, whose sorted rows come through LDS.
+__global__ __launch_bounds__(kRankThreads) void sort_rank_kernel(SortParams p) {
+    __shared__ uint32_t rows[kRankKeys];
+    const uint32_t i = blockIdx.x * kRankThreads + threadIdx.x, log2 = p.block_log2, block = 1u << log2;
+    const bool there = i < p.n;
+    const uint32_t row = there ? p.rows[i] : 0, mine = i >> log2;
+    uint32_t rank = i & (block - 1);
+    for (uint32_t from = 0; from < p.n; from += kRankKeys) {
+        __syncthreads();
+        for (uint32_t k = threadIdx.x; k < kRankKeys; k += kRankThreads)
+            rows[k] = from + k < p.n ? p.rows[from + k] : ~0u;   // sorted last in its block
+        __syncthreads();
+        for (uint32_t b = 0; b < kRankKeys >> log2 && from + (b << log2) < p.n; ++b) {
+            const uint32_t at = (from >> log2) + b;
+            if (at == mine) continue;
+            // earlier blocks' keys of the same row or a smaller one, later blocks' of a smaller one
+            const uint32_t less = row + (at < mine);
+            const uint32_t* const in = rows + (b << log2);
+            uint32_t before = 0;
+            for (uint32_t step = block; step > 0; step >>= 1)
+                if (before + step <= block && in[before + step - 1] < less) before += step;
+            rank += before;
         }
-        rank += lo;
     }
-    p.sorted[rank] = k;
+    if (there) p.sorted[rank] = (uint64_t)row << 32 | p.tokens[i];
 }
 
 __device__ __forceinline__ uint32_t row_of(uint64_t key) { return (uint32_t)(key >> 32); }
@@ -228,7 +301,7 @@ __global__ __launch_bounds__(kSumThreads) void embed_sum_kernel(GradParams p) {
         return;
     }
     __shared__ uint64_t key[kRun + 2];   // the run's keys, the one before and the one after
-    const uint32_t first = job * kRun, len = min(kRun, p.n - first);
+    const uint32_t first = job << p.run_log2, len = min(1u << p.run_log2, p.n - first);
     for (uint32_t i = threadIdx.x; i < len + 2; i += kSumThreads) {
         const uint32_t at = first + i;   // key[i] is sorted[first + i - 1]
         key[i] = at >= 1 && at <= p.n ? p.sorted[at - 1] : ~0ull;
@@ -236,60 +309,113 @@ __global__ __launch_bounds__(kSumThreads) void embed_sum_kernel(GradParams p) {
     __syncthreads();
     if (col >= p.dim) return;
     float sum[8] = {};
-    for (uint32_t i = 0; i < len; ++i) {
-        const uint32_t row = row_of(key[i + 1]);
-        if (row >= p.vocab) return;   // tokens without a row come last
-        const u32x4 w =
-            *reinterpret_cast<const u32x4*>(p.dout + (uint64_t)(uint32_t)key[i + 1] * p.dim + col);
+    for (uint32_t i0 = 0; i0 < len; i0 += kAhead) {
+        u32x4 w[kAhead];
 #pragma unroll
-        for (uint32_t e = 0; e < 4; ++e) sum[2 * e] += bf16_lo(w[e]), sum[2 * e + 1] += bf16_hi(w[e]);
-        const bool ends = first + i + 1 == p.n || row_of(key[i + 2]) != row;
-        if (!ends && i + 1 < len) continue;
-        const bool began_here = !(first > 0 && row_of(key[0]) == row);
-        if (!began_here) put_partial(p.head, (uint64_t)job * p.dim + col, sum);
-        else if (ends) put_row(p, row, col, sum);
-        else put_partial(p.tail, (uint64_t)job * p.dim + col, sum);
+        for (uint32_t k = 0; k < kAhead; ++k) {
+            const uint64_t at = key[min(i0 + k, len - 1) + 1];   // past the run: its last token again, unused
+            w[k] = *reinterpret_cast<const u32x4*>(p.dout + (uint64_t)(uint32_t)at * p.dim + col);
+        }
 #pragma unroll
-        for (uint32_t e = 0; e < 8; ++e) sum[e] = 0.0f;
+        for (uint32_t k = 0; k < kAhead; ++k) {
+            const uint32_t i = i0 + k;
+            if (i >= len) return;
+            const uint32_t row = row_of(key[i + 1]);
+            if (row >= p.vocab) return;   // tokens without a row come last
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e) sum[2 * e] += bf16_lo(w[k][e]), sum[2 * e + 1] += bf16_hi(w[k][e]);
+            const bool ends = first + i + 1 == p.n || row_of(key[i + 2]) != row;
+            if (!ends && i + 1 < len) continue;
+            const bool began_here = !(first > 0 && row_of(key[0]) == row);
+            if (!began_here) put_partial(p.head, (uint64_t)job * p.dim + col, sum);
+            else if (ends) put_row(p, row, col, sum);
+            else put_partial(p.tail, (uint64_t)job * p.dim + col, sum);
+#pragma unroll
+            for (uint32_t e = 0; e < 8; ++e) sum[e] = 0.0f;
+        }
     }
 }
 
-// A row that goes on from run to run: the partial of the run where it begins,
-// then those of the runs after it, in order.
-__global__ __launch_bounds__(kSumThreads) void embed_join_kernel(GradParams p) {
-    const uint32_t cb = blockIdx.x % p.col_blocks, run = blockIdx.x / p.col_blocks;
-    const uint32_t col = cb * kSumCols + threadIdx.x * 8;
-    const uint32_t next = (run + 1) * kRun;
-    const uint32_t row = row_of(p.sorted[next - 1]);
-    if (row >= p.vocab || row_of(p.sorted[next]) != row) return;          // nothing goes on here
-    const uint32_t first = run * kRun;
-    if (first > 0 && row_of(p.sorted[first - 1]) == row && row_of(p.sorted[first]) == row) return;   // began earlier
-    if (col >= p.dim) return;
-    float sum[8];
-    const f32x4* s = reinterpret_cast<const f32x4*>(p.tail + (uint64_t)run * p.dim + col);
+constexpr uint32_t kJoinSlices = 8;                              // of a row's runs
+constexpr uint32_t kJoinCols = kSumThreads / kJoinSlices * 8;    // columns of a workgroup at a time
+constexpr uint32_t kJoinBlocks = 4;                              // workgroups per run at most
+
+// A row that goes on from run to run: the partial of the run where it begins
+// and those of the runs after it, in order within each of 8 slices of them,
+// then the slices in order.
+__global__ __launch_bounds__(kSumThreads) void embed_join_kernel(GradParams p, uint32_t join_blocks) {
+    const uint32_t run = blockIdx.x / join_blocks;
+    const uint32_t first = run << p.run_log2, next = first + (1u << p.run_log2);
+    // most runs have none, and are done after one trip to memory
+    const uint32_t row = row_of(p.sorted[next - 1]), after = row_of(p.sorted[next]);
+    const uint32_t before = row_of(p.sorted[first > 0 ? first - 1 : 0]);
+    if (row >= p.vocab || after != row || (first > 0 && before == row)) return;
+    // the runs that the row goes on in: up to the one that holds its last token, looked for in growing steps
+    uint32_t lo = next + 1, step = 1u << p.run_log2;   // tokens up to lo - 1 are the row's
+    while (lo + step <= p.n && row_of(p.sorted[lo + step - 1]) == row) lo += step, step *= 2;
+    for (; step > 0; step >>= 1)
+        if (lo + step <= p.n && row_of(p.sorted[lo + step - 1]) == row) lo += step;
+    const uint32_t runs = ((lo - 1) >> p.run_log2) - run, per = (runs + kJoinSlices - 1) / kJoinSlices;
+    const uint32_t slice = threadIdx.x / (kSumThreads / kJoinSlices), lane = threadIdx.x % (kSumThreads / kJoinSlices);
+    const uint32_t begin = run + 1 + slice * per, end = min(begin + per, run + 1 + runs);
+    __shared__ f32x4 shared[2][kSumThreads];
+    for (uint32_t col0 = blockIdx.x % join_blocks * kJoinCols; col0 < p.dim; col0 += join_blocks * kJoinCols) {
+        const uint32_t col = col0 + lane * 8;
+        const bool inside = col < p.dim;
+        float sum[8] = {};
+        if (inside) {
+            if (slice == 0) {
+                const f32x4* const tail = reinterpret_cast<const f32x4*>(p.tail + (uint64_t)run * p.dim + col);
 #pragma unroll
-    for (uint32_t e = 0; e < 8; ++e) sum[e] = s[e / 4][e % 4];
-    for (uint32_t r = run + 1; r < p.runs && row_of(p.sorted[r * kRun]) == row; ++r) {
-        s = reinterpret_cast<const f32x4*>(p.head + (uint64_t)r * p.dim + col);
+                for (uint32_t e = 0; e < 8; ++e) sum[e] = tail[e / 4][e % 4];
+            }
+            for (uint32_t r0 = begin; r0 < end; r0 += kAhead) {
+                f32x4 part[kAhead][2];
 #pragma unroll
-        for (uint32_t e = 0; e < 8; ++e) sum[e] += s[e / 4][e % 4];
+                for (uint32_t k = 0; k < kAhead; ++k) {
+                    const f32x4* const from =
+                        reinterpret_cast<const f32x4*>(p.head + (uint64_t)min(r0 + k, end - 1) * p.dim + col);
+                    part[k][0] = from[0], part[k][1] = from[1];
+                }
+#pragma unroll
+                for (uint32_t k = 0; k < kAhead; ++k)
+                    if (r0 + k < end)
+#pragma unroll
+                        for (uint32_t e = 0; e < 8; ++e) sum[e] += part[k][e / 4][e % 4];
+            }
+        }
+        __syncthreads();
+        shared[0][threadIdx.x] = f32x4{sum[0], sum[1], sum[2], sum[3]};
+        shared[1][threadIdx.x] = f32x4{sum[4], sum[5], sum[6], sum[7]};
+        __syncthreads();
+        if (slice != 0 || !inside) continue;
+#pragma unroll
+        for (uint32_t k = 1; k < kJoinSlices; ++k)
+#pragma unroll
+            for (uint32_t e = 0; e < 8; ++e) sum[e] += shared[e / 4][threadIdx.x + k * (kSumThreads / kJoinSlices)][e % 4];
+        put_row(p, row, col, sum);
     }
-    put_row(p, row, col, sum);
 }
 
 constexpr uint64_t kAlign = 256;
 uint64_t up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
 
 struct GradLayout {
-    uint64_t sorted, keys, head, tail, bytes;
-    uint32_t runs;
+    uint64_t sorted, scratch, head, tail, bytes;
+    uint32_t runs, run_log2;
 };
+// Runs of 32 tokens, or of 16 or 8 where that leaves fewer than 1024
+// workgroups: eight tokens are on their way at a time, so longer runs of a
+// small batch only wait.
 GradLayout grad_layout(uint64_t n, uint32_t dim) {
     GradLayout l{};
-    l.runs = (uint32_t)((n + kRun - 1) / kRun);
+    l.run_log2 = 5;
+    static_assert(kRun == 1u << 5, "the longest run");
+    while (l.run_log2 > 3 && (n >> l.run_log2) * ((dim + kSumCols - 1) / kSumCols) < 1024) --l.run_log2;
+    l.runs = (uint32_t)((n + (1u << l.run_log2) - 1) >> l.run_log2);
     l.sorted = 0;
-    l.keys = up(n * 8, kAlign);
-    l.head = l.keys + (n > kSortKeys ? up(n * 8, kAlign) : 0);
+    l.scratch = up(n * 8, kAlign);
+    l.head = l.scratch + up(n * 8, kAlign);
     l.tail = l.head + up((uint64_t)l.runs * dim * 4, kAlign);
     l.bytes = l.tail + up((uint64_t)l.runs * dim * 4, kAlign);
     return l;
@@ -312,6 +438,31 @@ int launch_lookup(LookupParams& p, bool q4, hipStream_t s) {
 }
 
 }  // namespace
+
+void launch_sort_ids(const void* ids, uint32_t id_bytes, uint32_t n, uint32_t vocab, uint64_t* sorted,
+                     uint32_t* scratch, hipStream_t stream, void* fill, uint64_t fill_bytes) {
+    SortParams p{};
+    p.ids = ids, p.id_bytes = id_bytes, p.n = n, p.vocab = vocab, p.sorted = sorted;
+    p.block_log2 = 12;
+    while (((uint64_t)(vocab + 1) << p.block_log2) > 0x100000000ull) --p.block_log2;
+    const uint32_t block = 1u << p.block_log2;
+    p.blocks = (n + block - 1) / block;
+    p.limit = 4;
+    while (p.limit < n && p.limit < block) p.limit <<= 1;
+    if (p.blocks > 1) p.rows = scratch, p.tokens = scratch + n;
+    uint32_t threads = p.limit / 4 < 64 ? 64 : p.limit / 4;
+    uint64_t fillers = 0;
+    if (fill) {
+        threads = threads < 256 ? 256 : threads;
+        p.fill = static_cast<u32x4*>(fill), p.fill_chunks = fill_bytes / 16;
+        fillers = (p.fill_chunks + threads * kFillChunks - 1) / (threads * kFillChunks);
+    }
+    hipLaunchKernelGGL(sort_block_kernel, dim3((uint32_t)(p.blocks + fillers)), dim3(threads), 0, stream, p);
+    if (p.blocks > 1)
+        hipLaunchKernelGGL(sort_rank_kernel, dim3((n + kRankThreads - 1) / kRankThreads), dim3(kRankThreads), 0, stream,
+                           p);
+}
+
 }  // namespace wc
 
 using namespace wc;
@@ -359,6 +510,7 @@ extern "C" int wc_embed_grad_async(const uint16_t* dout, const void* ids, uint32
     if (vocab == 0 || (n == 0 && accumulate)) return WC_OK;
     if (!aligned16(dtable)) return WC_ERR_INVALID_ARG;
     GradParams p{};
+    uint32_t* scratch = nullptr;
     const GradLayout l = grad_layout(n, dim);
     if (n) {
         if (!aligned16(dout) || !ids_fit(ids, id_bytes) || !work_dev ||
@@ -366,24 +518,26 @@ extern "C" int wc_embed_grad_async(const uint16_t* dout, const void* ids, uint32
             return WC_ERR_INVALID_ARG;
         uint8_t* const w = static_cast<uint8_t*>(work_dev);
         p.sorted = reinterpret_cast<uint64_t*>(w + l.sorted);
-        p.keys = reinterpret_cast<uint64_t*>(w + l.keys);
+        scratch = reinterpret_cast<uint32_t*>(w + l.scratch);
         p.head = reinterpret_cast<float*>(w + l.head);
         p.tail = reinterpret_cast<float*>(w + l.tail);
     }
     p.dout = dout, p.ids = ids, p.id_bytes = id_bytes, p.dtable = dtable;
-    p.n = (uint32_t)n, p.vocab = vocab, p.dim = dim, p.runs = l.runs;
+    p.n = (uint32_t)n, p.vocab = vocab, p.dim = dim, p.runs = l.runs, p.run_log2 = l.run_log2;
     p.bf16 = out_kind == WC_OUT_BF16, p.accumulate = accumulate != 0, p.scale = scale;
     p.col_blocks = (dim + kSumCols - 1) / kSumCols;
-    p.row_blocks = p.accumulate ? 0 : (vocab + kFillRows - 1) / kFillRows;
+    // Rows without tokens: where tokens are at most half as many as rows, the whole table is set to zero beside the
+    // sort, whose few workgroups leave the memory idle, and rows with tokens are written again; else the summing
+    // launch writes only the rows that have none.
+    const bool ahead = !p.accumulate && n && n <= vocab / 2;
+    p.row_blocks = p.accumulate || ahead ? 0 : (vocab + kFillRows - 1) / kFillRows;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    if (n) {
-        const bool one = n <= kSortKeys;
-        hipLaunchKernelGGL(embed_sort_kernel, dim3((p.n + kSortKeys - 1) / kSortKeys), dim3(kSortThreads), 0, s, p,
-                           one ? p.sorted : p.keys);
-        if (!one) hipLaunchKernelGGL(embed_rank_kernel, dim3((p.n + 255) / 256), dim3(256), 0, s, p);
-    }
+    const uint64_t table_bytes = (uint64_t)vocab * dim * (p.bf16 ? 2 : 4);
+    if (n) launch_sort_ids(ids, id_bytes, p.n, vocab, p.sorted, scratch, s, ahead ? dtable : nullptr, table_bytes);
     hipLaunchKernelGGL(embed_sum_kernel, dim3((p.runs + p.row_blocks) * p.col_blocks), dim3(kSumThreads), 0, s, p);
-    if (p.runs > 1)
-        hipLaunchKernelGGL(embed_join_kernel, dim3((p.runs - 1) * p.col_blocks), dim3(kSumThreads), 0, s, p);
+    if (p.runs > 1) {
+        const uint32_t blocks = (dim + kJoinCols - 1) / kJoinCols, join_blocks = blocks < kJoinBlocks ? blocks : kJoinBlocks;
+        hipLaunchKernelGGL(embed_join_kernel, dim3((p.runs - 1) * join_blocks), dim3(kSumThreads), 0, s, p, join_blocks);
+    }
     return hipGetLastError() == hipSuccess ? WC_OK : WC_ERR_HIP;
 }

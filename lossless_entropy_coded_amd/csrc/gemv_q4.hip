@@ -82,8 +82,6 @@ struct Q4Shape {
     static constexpr uint32_t kNoneBytes = kSlab * 256;
 };
 
-__device__ __forceinline__ float bf16_f32(uint32_t b) { return __uint_as_float(b << 16); }
-
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, uint64_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)(uint32_t)bytes, 0x00027000);
 }
