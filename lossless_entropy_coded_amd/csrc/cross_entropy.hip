@@ -276,6 +276,37 @@ struct Tile {
     }
 };
 
+// A tile of bf16 results, row n of them 2 kBm bytes: put together in LDS (four
+// neighbours of a row per lane, its 16-byte chunks at chunk ^ n, so that the 32
+// rows that a wave writes at a time lie in different banks), then written as
+// whole rows.  From the registers a row's lines would be written 16 bytes at a
+// time: at 16 tokens x 131072 x 4096, where writing dW is all there is to do,
+// that took 441 us.  value(i, j, r): four results from r on, as two words; rows
+// and columns from n_end and m_end on are left out.  LDS is free when it begins.
+template <class T, class Value>
+__device__ __forceinline__ void store_rows(uint16_t* lds, uint16_t* out, uint64_t ld, uint32_t m_end, uint32_t n_end,
+                                           Value value) {
+    constexpr uint32_t kChunks = T::kBm / 8;
+    static_assert(T::kBm * T::kBn <= T::kLdsElems, "the tile fits the stages' LDS");
+#pragma unroll
+    for (uint32_t j = 0; j < T::kNi; ++j)
+#pragma unroll
+        for (uint32_t i = 0; i < T::kMi; ++i)
+#pragma unroll
+            for (uint32_t r = 0; r < 16; r += 4) {
+                const uint32_t n = T::n(j), m = T::m(i, r);
+                *reinterpret_cast<u32x2*>(lds + n * T::kBm + (((m / 8) ^ (n & (kChunks - 1))) * 8) + (m & 7u)) =
+                    value(i, j, r);
+            }
+    __syncthreads();
+    for (uint32_t at = threadIdx.x; at < kChunks * T::kBn; at += T::kThreads) {
+        const uint32_t n = at / kChunks, c = at % kChunks;
+        if (n < n_end && c * 8 < m_end)
+            *reinterpret_cast<u32x4*>(out + n * ld + c * 8) =
+                *reinterpret_cast<const u32x4*>(lds + n * T::kBm + ((c ^ (n & (kChunks - 1))) * 8));
+    }
+}
+
 // Which tile a workgroup takes.  Workgroups go to the 8 dies in turn: each die
 // gets a contiguous run of tiles (its L2 is its own), and within a run 4 tiles
 // of m go with each tile of n, so that the tiles in work at one time share
@@ -414,31 +445,30 @@ __global__ __launch_bounds__(T::kThreads) void ce_d_kernel(CeParams p) {
     const Operand A{p.W, p.dim, p.vocab, p.dim}, B{p.h, p.dim, p.tokens, p.dim};
     f32x16 acc[T::kMi][T::kNi];
     T::product(lds, A, B, m0, n0, 0, p.dim, acc);
+    // per column of the lane: its token's target, upstream gradient and lse
+    uint32_t own[T::kNi];
+    float g[T::kNi], lse[T::kNi];
 #pragma unroll
     for (uint32_t j = 0; j < T::kNi; ++j) {
         const uint32_t t = n0 + T::n(j);
-        if (t >= p.tokens) continue;
-        const uint32_t own = target_of(p, t);
-        const float g = own < p.vocab ? p.dloss[t] : 0.0f, lse = p.lse[t];
-        uint16_t* const row = p.d + (uint64_t)t * p.ldd + mt * T::kBm;
-#pragma unroll
-        for (uint32_t i = 0; i < T::kMi; ++i)
-#pragma unroll
-            for (uint32_t r = 0; r < 16; r += 4) {
-                uint16_t b[4];
-#pragma unroll
-                for (uint32_t e = 0; e < 4; ++e) {
-                    const uint32_t v = m0 + T::m(i, r + e);
-                    float x = __expf(acc[i][j][r + e] - lse);
-                    if (v == own) x -= 1.0f;
-                    x = v < p.piece_end && own < p.vocab ? x * g : 0.0f;
-                    b[e] = f32_bf16(x);
-                    if (v == own && v < p.piece_end) p.own[t] = x - bf16_f32(b[e]);
-                }
-                const u32x2 w = {b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16};
-                *reinterpret_cast<u32x2*>(row + T::m(i, r)) = w;
-            }
+        own[j] = t < p.tokens ? target_of(p, t) : p.vocab;
+        g[j] = own[j] < p.vocab ? p.dloss[t] : 0.0f;
+        lse[j] = t < p.tokens ? p.lse[t] : 0.0f;
     }
+    store_rows<T>(lds, p.d + (uint64_t)n0 * p.ldd + mt * T::kBm, p.ldd, T::kBm, p.tokens - n0,
+                  [&](uint32_t i, uint32_t j, uint32_t r) {
+                      uint16_t b[4];
+#pragma unroll
+                      for (uint32_t e = 0; e < 4; ++e) {
+                          const uint32_t v = m0 + T::m(i, r + e);
+                          float x = __expf(acc[i][j][r + e] - lse[j]);
+                          if (v == own[j]) x -= 1.0f;
+                          x = v < p.piece_end && own[j] < p.vocab ? x * g[j] : 0.0f;
+                          b[e] = f32_bf16(x);
+                          if (v == own[j] && v < p.piece_end) p.own[n0 + T::n(j)] = x - bf16_f32(b[e]);
+                      }
+                      return u32x2{b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16};
+                  });
 }
 
 // dh += d W over the piece, in fp32, the vocabulary split over blockIdx.y.
@@ -483,22 +513,11 @@ __global__ __launch_bounds__(T::kThreads) void ce_dw_kernel(CeParams p) {
     const Operand A{p.h, p.dim, p.dim, p.tokens}, B{p.d, p.ldd, p.ldd, p.tokens};
     f32x16 acc[T::kMi][T::kNi];
     T::product(lds, A, B, m0, n0, 0, p.tokens, acc);
-#pragma unroll
-    for (uint32_t j = 0; j < T::kNi; ++j) {
-        const uint32_t v = n0 + T::n(j);
-        if (v >= len) continue;
-        uint16_t* const row = p.dW + (uint64_t)(p.piece_begin + v) * p.dim;
-#pragma unroll
-        for (uint32_t i = 0; i < T::kMi; ++i)
-#pragma unroll
-            for (uint32_t r = 0; r < 16; r += 4) {
-                const uint32_t m = m0 + T::m(i, r);
-                if (m >= p.dim) continue;
-                const u32x2 w = {f32_bf16(acc[i][j][r]) | (uint32_t)f32_bf16(acc[i][j][r + 1]) << 16,
-                                 f32_bf16(acc[i][j][r + 2]) | (uint32_t)f32_bf16(acc[i][j][r + 3]) << 16};
-                *reinterpret_cast<u32x2*>(row + m) = w;
-            }
-    }
+    store_rows<T>(lds, p.dW + (uint64_t)(p.piece_begin + n0) * p.dim + m0, p.dim, p.dim - m0, len - n0,
+                  [&](uint32_t i, uint32_t j, uint32_t r) {
+                      return u32x2{f32_bf16(acc[i][j][r]) | (uint32_t)f32_bf16(acc[i][j][r + 1]) << 16,
+                                   f32_bf16(acc[i][j][r + 2]) | (uint32_t)f32_bf16(acc[i][j][r + 3]) << 16};
+                  });
 }
 
 // dW of no tokens.
@@ -527,9 +546,42 @@ __global__ __launch_bounds__(256) void ce_dh_round_kernel(CeParams p) {
     *reinterpret_cast<u32x2*>(p.dh + (uint64_t)t * p.dim + at) = w;
 }
 
-using TileZ = Tile<false, false, 256, 256, 2, 4, 2>;    // W and h: k (dim) contiguous
-using TileDh = Tile<true, false, 256, 256, 2, 4, 2>;    // W^T: m (dim) contiguous; d: k (vocabulary) contiguous
-using TileDw = Tile<true, true, 256, 256, 2, 4, 2>;     // h^T and d^T: the output indexes contiguous
+// The products' operands: z takes W and h with k (dim) contiguous; dh takes W^T
+// with m (dim) contiguous and d with k (vocabulary) contiguous; dW takes h^T and
+// d^T, the output indexes contiguous.
+template <bool kAx, bool kBx>
+using Big = Tile<kAx, kBx, 256, 256, 2, 4, 2>;     // one workgroup per CU
+template <bool kAx, bool kBx>
+using Mid = Tile<kAx, kBx, 128, 128, 2, 2, 2>;     // two per CU, each at 3/4 of the rate of one big one in all
+template <bool kAx, bool kBx>
+using Thin = Tile<kAx, kBx, 256, 64, 4, 1, 3>;     // few tokens: bound by reading W, two stages ahead
+constexpr uint32_t kThinTokens = 64;
+constexpr uint32_t kCus = 256;
+
+uint32_t cdiv(uint64_t a, uint32_t b) { return (uint32_t)((a + b - 1) / b); }
+
+// z of few tokens takes thin tiles where the vocabulary has enough of them to
+// keep the memory busy (z, thin and mid, us: 16 x 131072 x 4096 190 and 204; 64
+// x 5000 x 512 24 and 16).
+bool takes_thin(uint64_t tokens, uint32_t vocab) { return tokens <= kThinTokens && cdiv(vocab, 256) >= kCus / 2; }
+
+// Whether m x n outputs take big tiles: by the rounds that the card needs of
+// either kind, a round of mid tiles (two per CU) taking 2/3 of one of big
+// tiles.  Measured (z, big and mid, us): 515 tokens x 32003 x 1160 84 and 83;
+// 1000 x 20000 x 2048 112 and 100; 200 x 100000 x 1024 81 and 90; 3000 x 4000 x
+// 704 33 and 33; 4096 x 131072 x 4096 3520 and 6400.
+bool takes_big(uint64_t m, uint64_t n) {
+    const uint64_t big = (uint64_t)cdiv(m, 256) * cdiv(n, 256), mid = (uint64_t)cdiv(m, 128) * cdiv(n, 128);
+    return 3 * cdiv(big, kCus) < 2 * cdiv(mid, 2 * kCus);
+}
+// dh has few outputs and a long sum, which is split: big tiles unless they are
+// very few (dh, big and mid, us: 515 x 32003 x 1160, 15 tiles, 111 and 96; 200 x
+// 100000 x 1024, 4 tiles, 160 and 91; 1000 x 20000 x 2048, 32 tiles, 95 and 116).
+bool dh_takes_big(uint64_t tokens, uint32_t dim) { return (uint64_t)cdiv(dim, 256) * cdiv(tokens, 256) >= 24; }
+// dW: a short sum leaves the stores the most of the time, which two workgroups
+// per CU overlap with products (dW, big and mid, us: 515 x 32003 x 1160 74 and
+// 62; 200 x 100000 x 1024 142 and 120).
+bool dw_takes_big(uint64_t tokens, uint32_t len, uint32_t dim) { return tokens >= 1024 && takes_big(dim, len); }
 
 constexpr uint64_t kAlign = 256;
 uint64_t up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
@@ -544,7 +596,7 @@ struct CeLayout {
 
 CeLayout layout(uint64_t tokens, uint32_t vocab, uint32_t dim) {
     CeLayout l{};
-    const uint64_t tiles = up(vocab, TileZ::kBm) / TileZ::kBm;
+    const uint64_t tiles = cdiv(vocab, 128);   // the narrowest that a tile of z is
     l.own = 0;
     const uint64_t own_bytes = up(tokens * 4, kAlign);
     l.part = own_bytes;
@@ -553,8 +605,9 @@ CeLayout layout(uint64_t tokens, uint32_t vocab, uint32_t dim) {
     piece = piece < 1024 ? 1024 : piece;
     piece = piece < up(vocab, 256) ? piece : up(vocab, 256);
     l.piece = (uint32_t)piece;
-    const uint64_t out_tiles = up(dim, TileDh::kBm) / TileDh::kBm * (up(tokens, TileDh::kBn) / TileDh::kBn);
-    uint64_t splits = 512 / out_tiles;
+    const uint32_t edge = tokens > kThinTokens && !dh_takes_big(tokens, dim) ? 128 : 256;
+    const uint64_t out_tiles = (uint64_t)cdiv(dim, edge) * cdiv(tokens, tokens <= kThinTokens ? kThinTokens : edge);
+    uint64_t splits = kCus * (edge == 128 ? 2 : 1) / out_tiles;
     splits = splits < 1 ? 1 : splits > piece / 1024 ? (piece < 1024 ? 1 : piece / 1024) : splits;
     l.split_k = (uint32_t)up((piece + splits - 1) / splits, kBk);
     l.splits = (uint32_t)((piece + l.split_k - 1) / l.split_k);
@@ -570,6 +623,30 @@ bool sizes_fit(uint64_t tokens, uint32_t vocab, uint32_t dim) {
 }
 
 bool aligned(const void* p, uintptr_t a) { return p && (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+template <class T>
+void run_loss(CeParams& p, hipStream_t s) {
+    const uint32_t tiles = cdiv(p.vocab, T::kBm);
+    hipLaunchKernelGGL(ce_loss_kernel<T>, dim3(tile_grid(tiles, cdiv(p.tokens, T::kBn))), dim3(T::kThreads), 0, s, p);
+    hipLaunchKernelGGL(ce_join_kernel, dim3(cdiv(p.tokens, kJoinTokens)), dim3(kJoinTokens * kJoinLanes), 0, s, p, tiles);
+}
+template <class T>
+void run_d(CeParams& p, hipStream_t s) {
+    const uint32_t len = p.piece_end - p.piece_begin;
+    hipLaunchKernelGGL(ce_d_kernel<T>, dim3(tile_grid(cdiv(len, T::kBm), cdiv(p.tokens, T::kBn))), dim3(T::kThreads), 0, s,
+                       p);
+}
+template <class T>
+void run_dh(CeParams& p, hipStream_t s) {
+    hipLaunchKernelGGL(ce_dh_kernel<T>, dim3(tile_grid(cdiv(p.dim, T::kBm), cdiv(p.tokens, T::kBn)), p.splits),
+                       dim3(T::kThreads), 0, s, p);
+}
+template <class T>
+void run_dw(CeParams& p, hipStream_t s) {
+    const uint32_t len = p.piece_end - p.piece_begin;
+    hipLaunchKernelGGL(ce_dw_kernel<T>, dim3(tile_grid(cdiv(p.dim, T::kBm), cdiv(len, T::kBn))), dim3(T::kThreads), 0, s,
+                       p);
+}
 
 }  // namespace
 }  // namespace wc
@@ -602,11 +679,9 @@ extern "C" int wc_ce_loss_async(const uint16_t* h, const uint16_t* W, const void
     p.own = reinterpret_cast<float*>(w + l.own);
     p.part = reinterpret_cast<float2*>(w + l.part);
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    const uint32_t tiles = (vocab + TileZ::kBm - 1) / TileZ::kBm;
-    hipLaunchKernelGGL(ce_loss_kernel<TileZ>, dim3(tile_grid(tiles, (p.tokens + TileZ::kBn - 1) / TileZ::kBn)),
-                       dim3(TileZ::kThreads), 0, s, p);
-    hipLaunchKernelGGL(ce_join_kernel, dim3((p.tokens + kJoinTokens - 1) / kJoinTokens),
-                       dim3(kJoinTokens * kJoinLanes), 0, s, p, tiles);
+    if (takes_thin(tokens, vocab)) run_loss<Thin<false, false>>(p, s);
+    else if (takes_big(vocab, tokens)) run_loss<Big<false, false>>(p, s);
+    else run_loss<Mid<false, false>>(p, s);
     return hipGetLastError() == hipSuccess ? WC_OK : WC_ERR_HIP;
 }
 
@@ -637,21 +712,23 @@ extern "C" int wc_ce_grad_async(const uint16_t* h, const uint16_t* W, const void
     p.d = reinterpret_cast<uint16_t*>(w + l.d);
     p.dh_part = reinterpret_cast<float*>(w + l.dh_part);
     p.ldd = l.piece, p.split_k = l.split_k, p.splits = l.splits;
-    const auto cdiv = [](uint32_t a, uint32_t b) { return (a + b - 1) / b; };
     for (uint64_t v0 = 0; v0 < vocab; v0 += l.piece) {
         p.piece_begin = (uint32_t)v0;
         p.piece_end = (uint32_t)(v0 + l.piece < vocab ? v0 + l.piece : vocab);
         p.first = v0 == 0;
         const uint32_t len = p.piece_end - p.piece_begin;
-        hipLaunchKernelGGL(ce_d_kernel<TileZ>, dim3(tile_grid(cdiv(len, TileZ::kBm), cdiv(p.tokens, TileZ::kBn))),
-                           dim3(TileZ::kThreads), 0, s, p);
-        if (dh)
-            hipLaunchKernelGGL(ce_dh_kernel<TileDh>,
-                               dim3(tile_grid(cdiv(dim, TileDh::kBm), cdiv(p.tokens, TileDh::kBn)), l.splits),
-                               dim3(TileDh::kThreads), 0, s, p);
-        if (dW)
-            hipLaunchKernelGGL(ce_dw_kernel<TileDw>, dim3(tile_grid(cdiv(dim, TileDw::kBm), cdiv(len, TileDw::kBn))),
-                               dim3(TileDw::kThreads), 0, s, p);
+        if (takes_thin(tokens, len)) run_d<Thin<false, false>>(p, s);
+        else if (takes_big(len, tokens)) run_d<Big<false, false>>(p, s);
+        else run_d<Mid<false, false>>(p, s);
+        if (dh) {
+            if (tokens <= kThinTokens) run_dh<Thin<true, false>>(p, s);
+            else if (dh_takes_big(tokens, dim)) run_dh<Big<true, false>>(p, s);
+            else run_dh<Mid<true, false>>(p, s);
+        }
+        if (dW) {
+            if (dw_takes_big(tokens, len, dim)) run_dw<Big<true, true>>(p, s);
+            else run_dw<Mid<true, true>>(p, s);
+        }
     }
     if (dh)
         hipLaunchKernelGGL(ce_dh_round_kernel, dim3(p.tokens, cdiv(dim, 1024)), dim3(256), 0, s, p);
