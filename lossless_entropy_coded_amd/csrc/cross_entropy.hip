@@ -59,8 +59,9 @@ struct Operand {
 };
 
 // LDS image of R x kBk elements in 16-byte chunks.  k contiguous: row x has 8
-// chunks, chunk c at place c ^ (x & 7), so that the 8 rows that one pass of a
-// 16-byte read touches lie in different banks.  x contiguous: row k has R / 8
+// chunks, chunk c at place c ^ (x / 2 & 7), so that the 16 rows (two per turn
+// of the 64 banks) that one pass of a 16-byte read touches lie in different
+// banks (with c ^ (x & 7) half of the LDS's time was conflicts).  x contiguous: row k has R / 8
 // chunks, chunk c at place c ^ ((k & 3) << 2): the 4 rows of k that a
 // transposing read touches lie 64 bytes apart.
 //
@@ -72,7 +73,7 @@ template <bool kXContig, uint32_t R, uint32_t kThreads>
 struct Loader {
     static constexpr uint32_t kLoads = R * kBk / 8 / kThreads;   // per thread and stage
     static_assert(R * kBk / 8 % kThreads == 0, "whole rounds");
-    static_assert(kXContig ? kThreads % (R / 8) == 0 && kThreads / (R / 8) % 4 == 0 : kThreads % 64 == 0,
+    static_assert(kXContig ? kThreads % (R / 8) == 0 && kThreads / (R / 8) % 4 == 0 : kThreads % 128 == 0,
                   "a thread's chunks of one stage have the same place in their rows");
     const uint16_t* base;
     uint32_t ld, depth, bytes;
@@ -93,7 +94,7 @@ struct Loader {
             const uint32_t left = o.rows > x0 ? o.rows - x0 : 0;
             base = o.p + (uint64_t)x0 * o.ld;
             bytes = (left < R ? left : R) * ld * 2;
-            const uint32_t row = tid / 8, c = (tid % 8) ^ (row & 7u);
+            const uint32_t row = tid / 8, c = (tid % 8) ^ (row / 2 & 7u);
             k = c * 8;
 #pragma unroll
             for (uint32_t i = 0; i < kLoads; ++i) off[i] = ((row + i * (kThreads / 8)) * ld + c * 8) * 2;
@@ -126,7 +127,7 @@ template <bool kXContig, uint32_t R>
 __device__ __forceinline__ bf16x8 fragment(const uint16_t* lds, uint32_t x, uint32_t k) {
     const uint32_t lane = threadIdx.x & 63u;
     if (!kXContig) {
-        const uint32_t row = x + (lane & 31u), c = (k / 8 + (lane >> 5)) ^ (row & 7u);
+        const uint32_t row = x + (lane & 31u), c = (k / 8 + (lane >> 5)) ^ (row / 2 & 7u);
         return *reinterpret_cast<const bf16x8*>(lds + row * kBk + c * 8);
     }
     // 16 lanes read a block of 4 k by 16 x (lane i: row k + i / 4, x + 4 (i % 4)) and receive it transposed

@@ -374,11 +374,25 @@ def decode_u8_async(plan: Plan, blob_dev, out_dev, stream=None) -> None:
                                    ctypes.c_void_p(_stream_handle(stream))), "wc_decode_u8_async")
 
 
+_torch = None   # torch, once it is there and holds a device
+
+
+def _torch_on_device():
+    """torch, if it has a device in use (None before): looked up once, for calls that take a few microseconds."""
+    global _torch
+    if _torch is None:
+        import torch
+        if torch.cuda.is_initialized():
+            _torch = torch
+    return _torch
+
+
 def _stream_handle(stream) -> int:
     if stream is None:
-        import torch
-        if torch.cuda.is_initialized():   # the handle itself: a Stream object costs 3 us
+        torch = _torch_on_device()
+        if torch is not None:   # the handle itself: a Stream object costs 3 us
             return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        import torch
         return int(torch.cuda.current_stream().cuda_stream)
     if hasattr(stream, "cuda_stream"):
         return int(stream.cuda_stream)
@@ -413,9 +427,10 @@ def stream_reference_async(src_dev, src_bytes: int, dst_dev, dst_bytes: int, str
 
 
 def _current_device():
-    import torch
-    if torch.cuda.is_initialized():
+    torch = _torch_on_device()
+    if torch is not None:
         return torch._C._cuda_getDevice()
+    import torch
     return torch.cuda.current_device() if torch.cuda.is_available() else None
 
 
@@ -499,14 +514,20 @@ def _sizes(call: str, **sizes) -> None:
             raise WCError(WC_ERR_INVALID_ARG, call, f"{what} is {v}")
 
 
+_INDEX_BYTES = {}   # dtype -> bytes, of the id types seen
+
+
 def _index_bytes(ids, what: str, call: str) -> int:
     """4 for int32 ids, 8 for int64 ids (raw pointers are taken as int64)."""
     if not hasattr(ids, "dtype"):
         return 8
-    name = str(ids.dtype)
-    if name not in ("torch.int32", "torch.int64"):
-        raise WCError(WC_ERR_INVALID_ARG, call, f"{what} is {name}, not int32 or int64")
-    return 4 if name == "torch.int32" else 8
+    width = _INDEX_BYTES.get(ids.dtype)
+    if width is None:
+        name = str(ids.dtype)
+        if name not in ("torch.int32", "torch.int64"):
+            raise WCError(WC_ERR_INVALID_ARG, call, f"{what} is {name}, not int32 or int64")
+        width = _INDEX_BYTES[ids.dtype] = 4 if name == "torch.int32" else 8
+    return width
 
 
 class Q4Matrix:
@@ -541,7 +562,8 @@ def gemv_q4_async(W: Q4Matrix, x_dev, n_vecs: int, y_dev, stream=None) -> None:
     x_dev: n_vecs x cols bf16; y_dev: n_vecs x rows float32."""
     call = "wc_gemv_q4_async"
     dev = _on_device(W, call)
-    _sizes(call, n_vecs=n_vecs)
+    if n_vecs >> 32:
+        _sizes(call, n_vecs=n_vecs)
     x = _bytes_ok(x_dev, 2 * n_vecs * W.cols, dev, "x", call)
     y = _bytes_ok(y_dev, 4 * n_vecs * W.rows, dev, "y", call)
     _check(_lib.wc_gemv_q4_async(W._ref, x, n_vecs, y, _stream_handle(stream)), call)
@@ -551,7 +573,8 @@ def embed_async(table_dev, vocab: int, dim: int, ids_dev, n: int, out_dev, scale
     """wc_embed_async: out[t] = scale * table[ids[t]] (bf16), zero where ids[t] is outside [0, vocab); one launch."""
     call = "wc_embed_async"
     dev = _current_device()
-    _sizes(call, vocab=vocab, dim=dim, n=n)
+    if (vocab | dim | n) >> 32:
+        _sizes(call, vocab=vocab, dim=dim, n=n)
     width = _index_bytes(ids_dev, "ids", call)
     table = _bytes_ok(table_dev, 2 * vocab * dim, dev, "table", call)
     ids = _bytes_ok(ids_dev, width * n, dev, "ids", call)
@@ -563,7 +586,8 @@ def embed_q4_async(W: Q4Matrix, ids_dev, n: int, out_dev, scale: float = 1.0, st
     """wc_embed_q4_async: embed_async from a 4-bit table of W.rows entries."""
     call = "wc_embed_q4_async"
     dev = _on_device(W, call)
-    _sizes(call, n=n)
+    if n >> 32:
+        _sizes(call, n=n)
     width = _index_bytes(ids_dev, "ids", call)
     ids = _bytes_ok(ids_dev, width * n, dev, "ids", call)
     out = _bytes_ok(out_dev, 2 * n * W.cols, dev, "out", call)
@@ -585,7 +609,8 @@ def embed_grad_async(dout_dev, ids_dev, n: int, dtable_dev, vocab: int, dim: int
     out: "f32" or "bf16", dtable's type.  accumulate: add to dtable instead of writing every row."""
     call = "wc_embed_grad_async"
     dev = _current_device()
-    _sizes(call, n=n, vocab=vocab, dim=dim)
+    if (vocab | dim | n) >> 32:
+        _sizes(call, n=n, vocab=vocab, dim=dim)
     if out not in OUT_KINDS:
         raise WCError(WC_ERR_INVALID_ARG, call, f"out is {out!r}, not one of {sorted(OUT_KINDS)}")
     width = _index_bytes(ids_dev, "ids", call)
@@ -610,7 +635,8 @@ def ce_loss_async(h_dev, W_dev, targets_dev, tokens: int, vocab: int, dim: int, 
     """wc_ce_loss_async: loss[t] = lse[t] - z[t][target[t]], lse[t] = log sum exp z[t] for z = h W^T (bf16 h, W)."""
     call = "wc_ce_loss_async"
     dev = _current_device()
-    _sizes(call, tokens=tokens, vocab=vocab, dim=dim)
+    if (tokens | vocab | dim) >> 32:
+        _sizes(call, tokens=tokens, vocab=vocab, dim=dim)
     width = _index_bytes(targets_dev, "targets", call)
     h = _bytes_ok(h_dev, 2 * tokens * dim, dev, "h", call)
     W = _bytes_ok(W_dev, 2 * vocab * dim, dev, "W", call)
@@ -627,7 +653,8 @@ def ce_grad_async(h_dev, W_dev, targets_dev, tokens: int, vocab: int, dim: int, 
     """wc_ce_grad_async: dh and dW (bf16; either may be None) of sum dloss[t] * loss[t], with ce_loss_async's lse."""
     call = "wc_ce_grad_async"
     dev = _current_device()
-    _sizes(call, tokens=tokens, vocab=vocab, dim=dim)
+    if (tokens | vocab | dim) >> 32:
+        _sizes(call, tokens=tokens, vocab=vocab, dim=dim)
     width = _index_bytes(targets_dev, "targets", call)
     h = _bytes_ok(h_dev, 2 * tokens * dim, dev, "h", call)
     W = _bytes_ok(W_dev, 2 * vocab * dim, dev, "W", call)
