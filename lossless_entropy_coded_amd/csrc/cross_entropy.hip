@@ -41,7 +41,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-constexpr uint32_t kBk = 64;              // k per LDS stage
+constexpr uint32_t kUnit = 64;            // splits of a sum over k begin at multiples of this
 
 __device__ __forceinline__ float bf16_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 
@@ -58,10 +58,10 @@ struct Operand {
     uint32_t depth;
 };
 
-// LDS image of R x kBk elements in 16-byte chunks.  k contiguous: row x has 8
-// chunks, chunk c at place c ^ (x / 2 & 7), so that the 16 rows (two per turn
-// of the 64 banks) that one pass of a 16-byte read touches lie in different
-// banks (with c ^ (x & 7) half of the LDS's time was conflicts).  x contiguous: row k has R / 8
+// LDS image of R x kBk elements in 16-byte chunks.  k contiguous: row x has
+// kBk / 8 chunks, chunk c at place c ^ place(x): one pass of a 16-byte read
+// touches 16 rows, 2 (kBk = 64) or 4 (32) per turn of the 64 banks, which so lie
+// in different banks (with c ^ (x & 7) half of the LDS's time was conflicts).  x contiguous: row k has R / 8
 // chunks, chunk c at place c ^ ((k & 3) << 2): the 4 rows of k that a
 // transposing read touches lie 64 bytes apart.
 //
@@ -69,11 +69,17 @@ struct Operand {
 // (each lane 16 bytes; the image's permutation is applied to the source
 // addresses, since a wave writes 64 consecutive chunks).  What lies outside
 // the operand is an offset outside its buffer: the load leaves zeros.
-template <bool kXContig, uint32_t R, uint32_t kThreads>
+template <uint32_t kBk>
+__device__ __forceinline__ uint32_t place(uint32_t x) {
+    static_assert(kBk == 64 || kBk == 32, "stages of 64 or 32 k");
+    return kBk == 64 ? x / 2 & 7u : x / 4 & 3u;
+}
+
+template <bool kXContig, uint32_t R, uint32_t kBk, uint32_t kThreads>
 struct Loader {
     static constexpr uint32_t kLoads = R * kBk / 8 / kThreads;   // per thread and stage
     static_assert(R * kBk / 8 % kThreads == 0, "whole rounds");
-    static_assert(kXContig ? kThreads % (R / 8) == 0 && kThreads / (R / 8) % 4 == 0 : kThreads % 128 == 0,
+    static_assert(kXContig ? kThreads % (R / 8) == 0 && kThreads / (R / 8) % 4 == 0 : kThreads / (kBk / 8) % 16 == 0,
                   "a thread's chunks of one stage have the same place in their rows");
     const uint16_t* base;
     uint32_t ld, depth, bytes;
@@ -94,10 +100,11 @@ struct Loader {
             const uint32_t left = o.rows > x0 ? o.rows - x0 : 0;
             base = o.p + (uint64_t)x0 * o.ld;
             bytes = (left < R ? left : R) * ld * 2;
-            const uint32_t row = tid / 8, c = (tid % 8) ^ (row / 2 & 7u);
+            constexpr uint32_t kRow = kBk / 8;   // chunks
+            const uint32_t row = tid / kRow, c = (tid % kRow) ^ place<kBk>(row);
             k = c * 8;
 #pragma unroll
-            for (uint32_t i = 0; i < kLoads; ++i) off[i] = ((row + i * (kThreads / 8)) * ld + c * 8) * 2;
+            for (uint32_t i = 0; i < kLoads; ++i) off[i] = ((row + i * (kThreads / kRow)) * ld + c * 8) * 2;
         }
     }
 
@@ -123,11 +130,11 @@ struct Loader {
 
 // The fragment of rows x .. x + 31, k .. k + 15 of a stage: lane l holds row
 // x + l % 32, k + 8 (l / 32) .. + 7.
-template <bool kXContig, uint32_t R>
+template <bool kXContig, uint32_t R, uint32_t kBk>
 __device__ __forceinline__ bf16x8 fragment(const uint16_t* lds, uint32_t x, uint32_t k) {
     const uint32_t lane = threadIdx.x & 63u;
     if (!kXContig) {
-        const uint32_t row = x + (lane & 31u), c = (k / 8 + (lane >> 5)) ^ (row / 2 & 7u);
+        const uint32_t row = x + (lane & 31u), c = (k / 8 + (lane >> 5)) ^ place<kBk>(row);
         return *reinterpret_cast<const bf16x8*>(lds + row * kBk + c * 8);
     }
     // 16 lanes read a block of 4 k by 16 x (lane i: row k + i / 4, x + 4 (i % 4)) and receive it transposed
@@ -155,8 +162,10 @@ __device__ __forceinline__ bf16x8 fragment(const uint16_t* lds, uint32_t x, uint
 //   waves taking turns (kAlternate)              1249 1174 1182
 // 4 waves of 128 x 128 each, which read a third less LDS, reach 885: a lone
 // wave per SIMD cannot cover its own LDS reads.
-template <bool kAx, bool kBx, uint32_t kBm_, uint32_t kBn_, uint32_t kWavesM_, uint32_t kWavesN_, uint32_t kStages_>
+template <bool kAx, bool kBx, uint32_t kBm_, uint32_t kBn_, uint32_t kWavesM_, uint32_t kWavesN_, uint32_t kStages_,
+          uint32_t kBk>
 struct Tile {
+    static_assert(kUnit % kBk == 0, "splits are whole stages");
     static constexpr uint32_t kBm = kBm_, kBn = kBn_, kWavesM = kWavesM_, kWavesN = kWavesN_, kStages = kStages_;
     static constexpr uint32_t kThreads = 64 * kWavesM * kWavesN;
     static constexpr uint32_t kMi = kBm / kWavesM / 32, kNi = kBn / kWavesN / 32;
@@ -164,11 +173,11 @@ struct Tile {
     static constexpr uint32_t kLdsElems = kStages * kStageElems;
     static constexpr bool kAlternate = kThreads == 512;
     static_assert(!kAlternate || kStages == 2, "alternating waves take two stages");
-    using LoadA = Loader<kAx, kBm, kThreads>;
-    using LoadB = Loader<kBx, kBn, kThreads>;
+    using LoadA = Loader<kAx, kBm, kBk, kThreads>;
+    using LoadB = Loader<kBx, kBn, kBk, kThreads>;
 
     // acc = sum over k in [k_begin, k_end) of A(m0 + ., k) B(n0 + ., k); k_begin
-    // is a multiple of kBk, k_end one too or the operands' end.
+    // is a multiple of kUnit, k_end one too or the operands' end.
     __device__ static __forceinline__ void product(uint16_t* lds, const Operand& A, const Operand& B, uint32_t m0,
                                                    uint32_t n0, uint32_t k_begin, uint32_t k_end,
                                                    f32x16 (&acc)[kMi][kNi]) {
@@ -205,12 +214,12 @@ struct Tile {
                 for (uint32_t kk = 0; kk < kBk; kk += 16) {
                     bf16x8 a[kMi], b[kNi];
 #pragma unroll
-                    for (uint32_t i = 0; i < kMi; ++i) a[i] = fragment<kAx, kBm>(sa, wm + i * 32, kk);
+                    for (uint32_t i = 0; i < kMi; ++i) a[i] = fragment<kAx, kBm, kBk>(sa, wm + i * 32, kk);
 #pragma unroll
-                    for (uint32_t j = 0; j < kNi; ++j) b[j] = fragment<kBx, kBn>(sb, wn + j * 32, kk);
+                    for (uint32_t j = 0; j < kNi; ++j) b[j] = fragment<kBx, kBn, kBk>(sb, wn + j * 32, kk);
                     if (kk == 0) la.start(lds + to, next);
                     if (kk == 16) lb.start(lds + to + kBm * kBk, next);
-                    if (kk == kBk - 16) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                    if (kk + 16 == kBk) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
                     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                     __builtin_amdgcn_s_barrier();
                     asm volatile("" ::: "memory");
@@ -249,9 +258,9 @@ struct Tile {
                 for (uint32_t kk = 0; kk < kBk; kk += 16) {
                     bf16x8 a[kMi], b[kNi];
 #pragma unroll
-                    for (uint32_t i = 0; i < kMi; ++i) a[i] = fragment<kAx, kBm>(sa, wm + i * 32, kk);
+                    for (uint32_t i = 0; i < kMi; ++i) a[i] = fragment<kAx, kBm, kBk>(sa, wm + i * 32, kk);
 #pragma unroll
-                    for (uint32_t j = 0; j < kNi; ++j) b[j] = fragment<kBx, kBn>(sb, wn + j * 32, kk);
+                    for (uint32_t j = 0; j < kNi; ++j) b[j] = fragment<kBx, kBn, kBk>(sb, wn + j * 32, kk);
 #pragma unroll
                     for (uint32_t i = 0; i < kMi; ++i)
 #pragma unroll
@@ -342,7 +351,7 @@ struct CeParams {
     float* dh_part;            // gradient: dh in fp32, [split][token][dim]
     uint32_t ldd;
     uint32_t piece_begin, piece_end;   // the piece's vocabulary
-    uint32_t split_k;          // vocabulary per split of dh's product, a multiple of kBk
+    uint32_t split_k;          // vocabulary per split of dh's product, a multiple of kUnit
     uint32_t splits;
     uint32_t first;            // the first piece: dh_part is written, not added to
 };
@@ -551,11 +560,13 @@ __global__ __launch_bounds__(256) void ce_dh_round_kernel(CeParams p) {
 // with m (dim) contiguous and d with k (vocabulary) contiguous; dW takes h^T and
 // d^T, the output indexes contiguous.
 template <bool kAx, bool kBx>
-using Big = Tile<kAx, kBx, 256, 256, 2, 4, 2>;     // one workgroup per CU
+using Big = Tile<kAx, kBx, 256, 256, 2, 4, 2, 64>;     // one workgroup per CU
 template <bool kAx, bool kBx>
-using Mid = Tile<kAx, kBx, 128, 128, 2, 2, 2>;     // two per CU, each at 3/4 of the rate of one big one in all
+using Mid = Tile<kAx, kBx, 128, 128, 2, 2, 2, 64>;     // two per CU, each at 3/4 of the rate of one big one in all
 template <bool kAx, bool kBx>
-using Thin = Tile<kAx, kBx, 256, 64, 4, 1, 3>;     // few tokens: bound by reading W, two stages ahead
+using MidDw = Tile<kAx, kBx, 128, 128, 2, 2, 3, 32>;   // rows of m and n either way: shorter stages, two ahead
+template <bool kAx, bool kBx>
+using Thin = Tile<kAx, kBx, 256, 64, 4, 1, 3, 64>;     // few tokens: bound by reading W, two stages ahead
 constexpr uint32_t kThinTokens = 64;
 constexpr uint32_t kCus = 256;
 
@@ -591,7 +602,7 @@ uint64_t up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
 // dh and target roundings.  A piece of the vocabulary is what keeps d within
 // 256 MiB, at least 1024 entries, whole tiles.
 struct CeLayout {
-    uint32_t piece, splits, split_k;
+    uint32_t piece, ldd, splits, split_k;
     uint64_t own, part, d, dh_part, loss_bytes, grad_bytes;
 };
 
@@ -606,14 +617,15 @@ CeLayout layout(uint64_t tokens, uint32_t vocab, uint32_t dim) {
     piece = piece < 1024 ? 1024 : piece;
     piece = piece < up(vocab, 256) ? piece : up(vocab, 256);
     l.piece = (uint32_t)piece;
+    l.ldd = (uint32_t)(piece + 128);   // an odd number of 256-byte lines: neighbouring rows in different memory channels
     const uint32_t edge = tokens > kThinTokens && !dh_takes_big(tokens, dim) ? 128 : 256;
     const uint64_t out_tiles = (uint64_t)cdiv(dim, edge) * cdiv(tokens, tokens <= kThinTokens ? kThinTokens : edge);
     uint64_t splits = kCus * (edge == 128 ? 2 : 1) / out_tiles;
     splits = splits < 1 ? 1 : splits > piece / 1024 ? (piece < 1024 ? 1 : piece / 1024) : splits;
-    l.split_k = (uint32_t)up((piece + splits - 1) / splits, kBk);
+    l.split_k = (uint32_t)up((piece + splits - 1) / splits, kUnit);
     l.splits = (uint32_t)((piece + l.split_k - 1) / l.split_k);
     l.d = own_bytes;
-    l.dh_part = l.d + up(tokens * piece * 2, kAlign);
+    l.dh_part = l.d + up(tokens * l.ldd * 2, kAlign);
     l.grad_bytes = l.dh_part + up((uint64_t)l.splits * tokens * dim * 4, kAlign);
     return l;
 }
@@ -712,7 +724,7 @@ extern "C" int wc_ce_grad_async(const uint16_t* h, const uint16_t* W, const void
     p.own = reinterpret_cast<float*>(w + l.own);
     p.d = reinterpret_cast<uint16_t*>(w + l.d);
     p.dh_part = reinterpret_cast<float*>(w + l.dh_part);
-    p.ldd = l.piece, p.split_k = l.split_k, p.splits = l.splits;
+    p.ldd = l.ldd, p.split_k = l.split_k, p.splits = l.splits;
     for (uint64_t v0 = 0; v0 < vocab; v0 += l.piece) {
         p.piece_begin = (uint32_t)v0;
         p.piece_end = (uint32_t)(v0 + l.piece < vocab ? v0 + l.piece : vocab);
@@ -728,7 +740,7 @@ extern "C" int wc_ce_grad_async(const uint16_t* h, const uint16_t* W, const void
         }
         if (dW) {
             if (dw_takes_big(tokens, len, dim)) run_dw<Big<true, true>>(p, s);
-            else run_dw<Mid<true, true>>(p, s);
+            else run_dw<MidDw<true, true>>(p, s);
         }
     }
     if (dh)
