@@ -31,10 +31,13 @@
 // by code through v_cvt_off_f32_i4, needs no scaling of x but 1.75 operations
 // per weight, 2.4 with zero points: 12.2 us at 14336 x 4096, one vector.)
 //
-// A wave takes 16 kTiles rows and a part of the columns, 128 columns per step:
-// lane (r, q) loads the 16 bytes of row r's q-th 32 columns, four rows of lanes
+// A wave takes 16 kTiles rows and a part of the columns, 128 columns per step.
+// Lane 4 r + q loads the 16 bytes of row r's q-th chunk of 32 columns, so that
+// four neighbouring lanes read 64 neighbouring bytes: memory instructions take
+// as long as their quads of lanes touch cache lines.  Through LDS the chunk
+// goes to lane 16 q + r, as the matrix operand wants it; four rows of lanes
 // exchange dwords (2 + 2 lane swaps) so that each of the four products of a
-// step has 32 neighbouring columns, and x comes through the wave's own LDS.
+// step has 32 neighbouring columns; and x comes through the wave's own LDS too.
 // The waves of a workgroup share the rows and split the columns, and add their
 // sums in order at the end: everything is summed in a fixed order.
 #include <hip/hip_runtime.h>
@@ -79,6 +82,7 @@ struct Q4Shape {
     static constexpr uint32_t kRounds = kVecs * kSlab / 4;         // 64 lanes of 8 columns
     static constexpr uint32_t kXBytes = kVecs * kRowBytes;
     static constexpr uint32_t kWaveBytes = kXBytes + 64;
+    static constexpr uint32_t kSwapBytes = 1024;                   // per tile, of each wave
     static constexpr uint32_t kNoneBytes = kSlab * 256;
 };
 
@@ -171,14 +175,16 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
     extern __shared__ __align__(16) uint8_t lds[];
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t waves = blockDim.x >> 6;
-    uint8_t* const xs = lds + wave * S::kWaveBytes;
+    uint8_t* const xs = lds + wave * (S::kWaveBytes + kTiles * S::kSwapBytes);
+    uint8_t* const swap = xs + S::kWaveBytes;
     float* const units = reinterpret_cast<float*>(xs + S::kXBytes);
-    uint8_t* const none = lds + waves * S::kWaveBytes;   // zeros, for vectors that are not there
+    uint8_t* const none = lds + waves * (S::kWaveBytes + kTiles * S::kSwapBytes);   // zeros, for vectors that are not there
     for (uint32_t i = threadIdx.x; i < S::kNoneBytes / 4; i += blockDim.x) reinterpret_cast<uint32_t*>(none)[i] = 0;
     if (lane < 16) units[lane] = 0.0f;
     __syncthreads();
 
     const uint32_t r = lane & 15u, q = lane >> 4;   // weight row of a tile (or vector, holding x); chunk of a step
+    const uint32_t lr = lane >> 2, lq = lane & 3u;  // the same, loading
     const uint32_t row0 = blockIdx.x * 16 * kTiles, rows = min(p.rows - row0, 16u * kTiles);
     const uint32_t row_bytes = p.cols / 2;
     const auto codes_buf = buffer(p.codes + (uint64_t)row0 * row_bytes, (uint64_t)rows * row_bytes);
@@ -189,8 +195,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
     uint32_t code_at[kTiles], group_at[kTiles];   // of the lane's rows; those past the last repeat it
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) {
-        const uint32_t row = min(i * 16 + r, rows - 1);
-        code_at[i] = row * row_bytes + q * 16;
+        const uint32_t row = min(i * 16 + lr, rows - 1);
+        code_at[i] = row * row_bytes + lq * 16;
         group_at[i] = row * p.groups;
     }
 
@@ -201,6 +207,11 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
 #pragma unroll
     for (uint32_t j = 0; j < 4; ++j)
         x_at[j] = there ? xs + r * S::kRowBytes + q * 16 + ((j ^ (r & 3u)) * 64) : none;
+
+    // from lane 4 r + q to lane 16 q + r: 16-byte pieces of a row at piece ^ (row / 4), in different banks
+    uint8_t* const swap_to = swap + lr * 64 + ((lq ^ (lr >> 2)) * 16);
+    const uint8_t* const swap_from = swap + r * 64 + ((q ^ (r >> 2)) * 16);
+    const int word_from = (int)(r * 4 + q) * 4;
 
     uint32_t x_from[S::kRounds];
 #pragma unroll
@@ -221,7 +232,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
         }
 #pragma unroll
         for (uint32_t st = 0; st < S::kSlab; ++st) {
-            const uint32_t cs = c0 + st * kStepCols, c = cs + q * 32;
+            const uint32_t cs = c0 + st * kStepCols, c = cs + lq * 32;
             const bool inside = c < p.cols;
 #pragma unroll
             for (int i = 0; i < kTiles; ++i) {
@@ -237,7 +248,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
             }
         }
         if constexpr (kFour) {
-            const uint32_t first = min(slab * S::kSlab + min(q, S::kSlab - 1), p.cols / kStepCols - 1) * 4;
+            const uint32_t first = min(slab * S::kSlab + min(lq, S::kSlab - 1), p.cols / kStepCols - 1) * 4;
 #pragma unroll
             for (int i = 0; i < kTiles; ++i) {
                 const u32x2 s4 = __builtin_bit_cast(
@@ -248,7 +259,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
         } else
 #pragma unroll
         for (uint32_t k = 0; k < Loads::kScales; ++k) {
-            const uint32_t block = k * 4 + min(q, Loads::kBlocks - 1);
+            const uint32_t block = k * 4 + min(lq, Loads::kBlocks - 1);
             const uint32_t chunk = min(c0 + block * kBlock * 32, p.cols - 1) / 32;
             const uint32_t g = __umulhi(chunk, p.group_magic) + (chunk & p.group_one);
 #pragma unroll
@@ -267,6 +278,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
+    const auto exchanged = [&](uint32_t v) { return (uint32_t)__builtin_amdgcn_ds_bpermute(word_from, (int)v); };
     const auto process = [&](const Loads& l) {
         // x to f16, 8 columns per lane
 #pragma unroll
@@ -301,7 +313,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
 #pragma unroll
                 for (uint32_t b = 0; b < 4; ++b) {
                     const uint32_t two = l.scale[b / 2][i];
-                    own[b] = (b & 1 ? two & 0xFFFF0000u : two << 16) | (kGiven ? (l.zero[0][i] >> (8 * b)) & 0xFFu : 0);
+                    own[b] = exchanged((b & 1 ? two & 0xFFFF0000u : two << 16) |
+                                       (kGiven ? (l.zero[0][i] >> (8 * b)) & 0xFFu : 0));
                 }
                 own = transpose_rows(own);
 #pragma unroll
@@ -312,7 +325,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
             for (uint32_t k = 0; k < Loads::kScales; ++k)
 #pragma unroll
                 for (int i = 0; i < kTiles; ++i)
-                    words[k][i] = spread_rows(kGiven ? l.scale[k][i] << 16 | l.zero[k][i] : l.scale[k][i] << 16);
+                    words[k][i] =
+                        spread_rows(exchanged(kGiven ? l.scale[k][i] << 16 | l.zero[k][i] : l.scale[k][i] << 16));
         }
         f32x4 sum[kTiles];
 #pragma unroll
@@ -323,8 +337,17 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
 #pragma unroll
             for (uint32_t j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const f16x8*>(x_at[j] + st * 256);
 #pragma unroll
+            for (int i = 0; i < kTiles; ++i) *reinterpret_cast<u32x4*>(swap_to + i * S::kSwapBytes) = l.w[st][i];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            u32x4 chunk[kTiles];
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) chunk[i] = *reinterpret_cast<const u32x4*>(swap_from + i * S::kSwapBytes);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
             for (int i = 0; i < kTiles; ++i) {
-                const u32x4 w = transpose_rows(l.w[st][i]);
+                const u32x4 w = transpose_rows(chunk[i]);
 #pragma unroll
                 for (uint32_t b = 0; b < 4 / kBlock; ++b) {
                     const uint32_t block = st * (4 / kBlock) + b, word = words[block / 4][i][block % 4];
@@ -373,7 +396,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
     __syncthreads();
     float* const sums = reinterpret_cast<float*>(lds);   // [wave][kVecs][16 kTiles]
     constexpr uint32_t kOut = kVecs * 16 * kTiles;
-    static_assert(kOut * 4 <= S::kWaveBytes, "the sums fit where x was");
+    static_assert(kOut * 4 <= S::kWaveBytes + kTiles * S::kSwapBytes, "the sums fit where x was");
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
@@ -397,7 +420,7 @@ void launch(Q4Params& p, uint32_t waves, hipStream_t s) {
     p.slabs_per_wave = (slabs + waves - 1) / waves;
     waves = (slabs + p.slabs_per_wave - 1) / p.slabs_per_wave;
     const dim3 grid((p.rows + 16 * kTiles - 1) / (16 * kTiles)), block(64 * waves);
-    const uint32_t bytes = waves * S::kWaveBytes + S::kNoneBytes;
+    const uint32_t bytes = waves * (S::kWaveBytes + kTiles * S::kSwapBytes) + S::kNoneBytes;
     const auto go = [&](auto* kernel) { hipLaunchKernelGGL(kernel, grid, block, bytes, s, p); };
     if (p.cols % 32 != 0) return go(gemv_q4_kernel<kVecs, kTiles, 1, false, false, true>);
     const bool zeros = p.zeros;
@@ -417,18 +440,25 @@ void launch(Q4Params& p, uint32_t waves, hipStream_t s) {
               : go(gemv_q4_kernel<kVecs, kTiles, 1, false, true, false>);
 }
 
-// Rows and waves per workgroup.  From 8192 rows on there are workgroups of 16
-// rows enough for 4 waves each to fill the card (14336 x 4096, one vector: 9.4
-// us, with 8 waves 10.9); below, 8 waves split the columns further (4096 x
-// 14336: 8.7 us, with 4 waves 9.2).  32 rows share the work on x, where there
-// are vectors enough for that to count (8192 x 28672, 8 vectors: 43.5 us, with
-// 16 rows 51).
+// Rows and waves per workgroup.  From 8192 rows on there are workgroups enough
+// of 16 rows and 4 waves, or of 32 rows, which share the work on x, where
+// vectors make that count, and then of 8 waves from 8 vectors on; below, 16 rows
+// and 8 waves, which split the columns further.  Measured, us:
+//                                        16 rows        32 rows
+//                                   4 waves 8 waves 4 waves 8 waves
+//   14336 x 4096, one vector            9.5    10.4    10.1    11.5
+//   4096 x 14336, one vector            9.9     9.0    14.0    13.5
+//   14336 x 4096, 4 vectors            10.9    11.8    10.6    10.7
+//   14336 x 4096, 16 vectors           18.0    18.8    15.1    14.5
+//   8192 x 28672, 8 vectors            47.0    46.1    44.2    41.3
+//   1003 x 2088, 5 vectors              6.6     5.7     8.9     7.6
 template <int kVecs>
 void launch_rows(Q4Params& p, hipStream_t s) {
-    const bool many = p.rows >= 8192;
-    if constexpr (kVecs >= 8)
-        if (many) return launch<kVecs, 2>(p, 4, s);
-    launch<kVecs, 1>(p, many ? 4 : 8, s);
+    if (p.rows < 8192) return launch<kVecs, 1>(p, 8, s);
+    if constexpr (kVecs >= 4)
+        launch<kVecs, 2>(p, kVecs >= 8 ? 8 : 4, s);
+    else
+        launch<kVecs, 1>(p, 4, s);
 }
 
 }  // namespace
