@@ -321,6 +321,7 @@ __device__ __forceinline__ void store_rows(uint16_t* lds, uint16_t* out, uint64_
 // gets a contiguous run of tiles (its L2 is its own), and within a run 4 tiles
 // of m go with each tile of n, so that the tiles in work at one time share
 // operands both ways.
+constexpr uint32_t kDies = 8;
 __device__ __forceinline__ bool tile_of(uint32_t id, uint32_t ms, uint32_t ns, uint32_t& m, uint32_t& n) {
     const uint32_t total = ms * ns, per = (total + 7) / 8, t = id % 8 * per + id / 8;
     if (id / 8 >= per || t >= total) return false;
@@ -415,9 +416,9 @@ __global__ __launch_bounds__(T::kThreads) void ce_loss_kernel(CeParams p) {
     }
 }
 
-constexpr uint32_t kJoinTokens = 16, kJoinLanes = 16;   // tokens per workgroup, threads per token
+constexpr uint32_t kJoinTokens = 4, kJoinLanes = 64;   // tokens per workgroup, threads per token
 
-// Joins a token's tiles: 16 threads take the tiles in turn, then a butterfly.
+// Joins a token's tiles: 64 threads take the tiles in turn, then their results in order.
 __global__ __launch_bounds__(kJoinTokens* kJoinLanes) void ce_join_kernel(CeParams p, uint32_t tiles) {
     const uint32_t t = blockIdx.x * kJoinTokens + threadIdx.x % kJoinTokens, lane = threadIdx.x / kJoinTokens;
     __shared__ float2 seen[kJoinLanes][kJoinTokens];
@@ -485,15 +486,24 @@ __global__ __launch_bounds__(T::kThreads) void ce_d_kernel(CeParams p) {
 template <class T>
 __global__ __launch_bounds__(T::kThreads) void ce_dh_kernel(CeParams p) {
     __shared__ __align__(16) uint16_t lds[T::kLdsElems];
-    uint32_t mt, nt;
-    if (!tile_of(blockIdx.x, (p.dim + T::kBm - 1) / T::kBm, (p.tokens + T::kBn - 1) / T::kBn, mt, nt)) return;
+    // Eight splits (or a multiple) go to the dies, one die all tiles of a split: W and d come into one L2 each, once.
+    const uint32_t ms = (p.dim + T::kBm - 1) / T::kBm, ns = (p.tokens + T::kBn - 1) / T::kBn;
+    uint32_t mt, nt, split = 0;
+    if (p.splits % kDies == 0) {
+        const uint32_t i = blockIdx.x / kDies, tile = i % (ms * ns);
+        split = blockIdx.x % kDies + i / (ms * ns) * kDies;
+        mt = tile % ms, nt = tile / ms;
+    } else {
+        split = blockIdx.y;
+        if (!tile_of(blockIdx.x, ms, ns, mt, nt)) return;
+    }
     const uint32_t m0 = mt * T::kBm, n0 = nt * T::kBn;
     const uint32_t len = p.piece_end - p.piece_begin;
     const Operand A{p.W + (uint64_t)p.piece_begin * p.dim, p.dim, p.dim, len}, B{p.d, p.ldd, p.tokens, p.ldd};
-    const uint32_t k_begin = blockIdx.y * p.split_k, k_end = min(k_begin + p.split_k, len);
+    const uint32_t k_begin = split * p.split_k, k_end = min(k_begin + p.split_k, len);
     f32x16 acc[T::kMi][T::kNi];
     T::product(lds, A, B, m0, n0, k_begin, k_end, acc);
-    float* const out = p.dh_part + (uint64_t)blockIdx.y * p.tokens * p.dim;
+    float* const out = p.dh_part + (uint64_t)split * p.tokens * p.dim;
 #pragma unroll
     for (uint32_t j = 0; j < T::kNi; ++j) {
         const uint32_t t = n0 + T::n(j);
@@ -621,9 +631,11 @@ CeLayout layout(uint64_t tokens, uint32_t vocab, uint32_t dim) {
     const uint32_t edge = tokens > kThinTokens && !dh_takes_big(tokens, dim) ? 128 : 256;
     const uint64_t out_tiles = (uint64_t)cdiv(dim, edge) * cdiv(tokens, tokens <= kThinTokens ? kThinTokens : edge);
     uint64_t splits = kCus * (edge == 128 ? 2 : 1) / out_tiles;
-    splits = splits < 1 ? 1 : splits > piece / 1024 ? (piece < 1024 ? 1 : piece / 1024) : splits;
+    if (splits > kDies) splits = splits / kDies * kDies;
+    const uint64_t most = piece < 1024 ? 1 : piece / 1024;
+    splits = splits < 1 ? 1 : splits > most ? most : splits;
     l.split_k = (uint32_t)up((piece + splits - 1) / splits, kUnit);
-    l.splits = (uint32_t)((piece + l.split_k - 1) / l.split_k);
+    l.splits = (uint32_t)splits;   // the last ones may be empty: they leave zeros
     l.d = own_bytes;
     l.dh_part = l.d + up(tokens * l.ldd * 2, kAlign);
     l.grad_bytes = l.dh_part + up((uint64_t)l.splits * tokens * dim * 4, kAlign);
@@ -651,8 +663,9 @@ void run_d(CeParams& p, hipStream_t s) {
 }
 template <class T>
 void run_dh(CeParams& p, hipStream_t s) {
-    hipLaunchKernelGGL(ce_dh_kernel<T>, dim3(tile_grid(cdiv(p.dim, T::kBm), cdiv(p.tokens, T::kBn)), p.splits),
-                       dim3(T::kThreads), 0, s, p);
+    const uint32_t ms = cdiv(p.dim, T::kBm), ns = cdiv(p.tokens, T::kBn);
+    const dim3 grid = p.splits % kDies == 0 ? dim3(ms * ns * p.splits) : dim3(tile_grid(ms, ns), p.splits);
+    hipLaunchKernelGGL(ce_dh_kernel<T>, grid, dim3(T::kThreads), 0, s, p);
 }
 template <class T>
 void run_dw(CeParams& p, hipStream_t s) {
