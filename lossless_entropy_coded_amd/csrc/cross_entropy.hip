@@ -16,7 +16,10 @@
 // input type: a relative rounding of at most 2^-8 per value, as dh and dW
 // themselves are rounded) for the two products that read it.  The rounding of
 // the target's own value, by far the largest of a row, is kept per token in
-// fp32 and its product with W[target] is added to dh.
+// fp32 and its product with W[target] is added to dh.  A row of dW sums few
+// tokens where there are few, and their roundings do not average out: up to
+// 128 tokens, what the values of d lose is kept as a second bf16 matrix and
+// multiplied too (with more, it would cost a product as large as dW's).
 //
 // The three products run on one tile routine, out[n][m] = sum_k A(m, k) B(n, k),
 // m being the contiguous index of the output: a 32 x 32 accumulator block holds
@@ -176,7 +179,14 @@ struct Tile {
     using LoadA = Loader<kAx, kBm, kBk, kThreads>;
     using LoadB = Loader<kBx, kBn, kBk, kThreads>;
 
-    // acc = sum over k in [k_begin, k_end) of A(m0 + ., k) B(n0 + ., k); k_begin
+    __device__ static __forceinline__ void clear(f32x16 (&acc)[kMi][kNi]) {
+#pragma unroll
+        for (uint32_t i = 0; i < kMi; ++i)
+#pragma unroll
+            for (uint32_t j = 0; j < kNi; ++j) acc[i][j] = (f32x16)(0.0f);
+    }
+
+    // acc += sum over k in [k_begin, k_end) of A(m0 + ., k) B(n0 + ., k); k_begin
     // is a multiple of kUnit, k_end one too or the operands' end.
     __device__ static __forceinline__ void product(uint16_t* lds, const Operand& A, const Operand& B, uint32_t m0,
                                                    uint32_t n0, uint32_t k_begin, uint32_t k_end,
@@ -185,10 +195,6 @@ struct Tile {
         const uint32_t wm = wave % kWavesM * (kBm / kWavesM), wn = wave / kWavesM * (kBn / kWavesN);
         const LoadA la(A, m0);
         const LoadB lb(B, n0);
-#pragma unroll
-        for (uint32_t i = 0; i < kMi; ++i)
-#pragma unroll
-            for (uint32_t j = 0; j < kNi; ++j) acc[i][j] = (f32x16)(0.0f);
         uint32_t next = k_begin;   // the stage to start next (past k_end: its products are not taken)
 #pragma unroll
         for (uint32_t s = 0; s + 1 < kStages; ++s, next += kBk) {
@@ -351,6 +357,7 @@ struct CeParams {
     uint16_t* d;               // gradient: d of one piece, [token][ldd]
     float* dh_part;            // gradient: dh in fp32, [split][token][dim]
     uint32_t ldd;
+    uint32_t rests;            // d is followed by what its values lost to rounding, laid out the same
     uint32_t piece_begin, piece_end;   // the piece's vocabulary
     uint32_t split_k;          // vocabulary per split of dh's product, a multiple of kUnit
     uint32_t splits;
@@ -372,6 +379,7 @@ __global__ __launch_bounds__(T::kThreads) void ce_loss_kernel(CeParams p) {
     const uint32_t m0 = tile * T::kBm, n0 = nt * T::kBn;
     const Operand A{p.W, p.dim, p.vocab, p.dim}, B{p.h, p.dim, p.tokens, p.dim};
     f32x16 acc[T::kMi][T::kNi];
+    T::clear(acc);
     T::product(lds, A, B, m0, n0, 0, p.dim, acc);
 
     float2* const seen = reinterpret_cast<float2*>(lds);   // [kWavesM][kBn]
@@ -455,6 +463,7 @@ __global__ __launch_bounds__(T::kThreads) void ce_d_kernel(CeParams p) {
     const uint32_t m0 = p.piece_begin + mt * T::kBm, n0 = nt * T::kBn;
     const Operand A{p.W, p.dim, p.vocab, p.dim}, B{p.h, p.dim, p.tokens, p.dim};
     f32x16 acc[T::kMi][T::kNi];
+    T::clear(acc);
     T::product(lds, A, B, m0, n0, 0, p.dim, acc);
     // per column of the lane: its token's target, upstream gradient and lse
     uint32_t own[T::kNi];
@@ -466,20 +475,25 @@ __global__ __launch_bounds__(T::kThreads) void ce_d_kernel(CeParams p) {
         g[j] = own[j] < p.vocab ? p.dloss[t] : 0.0f;
         lse[j] = t < p.tokens ? p.lse[t] : 0.0f;
     }
-    store_rows<T>(lds, p.d + (uint64_t)n0 * p.ldd + mt * T::kBm, p.ldd, T::kBm, p.tokens - n0,
-                  [&](uint32_t i, uint32_t j, uint32_t r) {
-                      uint16_t b[4];
+    for (uint32_t rest = 0; rest <= p.rests; ++rest) {
+        if (rest) __syncthreads();
+        store_rows<T>(lds, p.d + ((uint64_t)rest * p.tokens + n0) * p.ldd + mt * T::kBm, p.ldd, T::kBm, p.tokens - n0,
+                      [&](uint32_t i, uint32_t j, uint32_t r) {
+                          uint16_t b[4];
 #pragma unroll
-                      for (uint32_t e = 0; e < 4; ++e) {
-                          const uint32_t v = m0 + T::m(i, r + e);
-                          float x = __expf(acc[i][j][r + e] - lse[j]);
-                          if (v == own[j]) x -= 1.0f;
-                          x = v < p.piece_end && own[j] < p.vocab ? x * g[j] : 0.0f;
-                          b[e] = f32_bf16(x);
-                          if (v == own[j] && v < p.piece_end) p.own[n0 + T::n(j)] = x - bf16_f32(b[e]);
-                      }
-                      return u32x2{b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16};
-                  });
+                          for (uint32_t e = 0; e < 4; ++e) {
+                              const uint32_t v = m0 + T::m(i, r + e);
+                              float x = __expf(acc[i][j][r + e] - lse[j]);
+                              if (v == own[j]) x -= 1.0f;
+                              x = v < p.piece_end && own[j] < p.vocab ? x * g[j] : 0.0f;
+                              b[e] = f32_bf16(x);
+                              const float lost = x - bf16_f32(b[e]);
+                              if (v == own[j] && v < p.piece_end) p.own[n0 + T::n(j)] = lost;
+                              if (rest) b[e] = f32_bf16(lost);
+                          }
+                          return u32x2{b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16};
+                      });
+    }
 }
 
 // dh += d W over the piece, in fp32, the vocabulary split over blockIdx.y.
@@ -502,6 +516,7 @@ __global__ __launch_bounds__(T::kThreads) void ce_dh_kernel(CeParams p) {
     const Operand A{p.W + (uint64_t)p.piece_begin * p.dim, p.dim, p.dim, len}, B{p.d, p.ldd, p.tokens, p.ldd};
     const uint32_t k_begin = split * p.split_k, k_end = min(k_begin + p.split_k, len);
     f32x16 acc[T::kMi][T::kNi];
+    T::clear(acc);
     T::product(lds, A, B, m0, n0, k_begin, k_end, acc);
     float* const out = p.dh_part + (uint64_t)split * p.tokens * p.dim;
 #pragma unroll
@@ -532,7 +547,12 @@ __global__ __launch_bounds__(T::kThreads) void ce_dw_kernel(CeParams p) {
     const uint32_t m0 = mt * T::kBm, n0 = nt * T::kBn;
     const Operand A{p.h, p.dim, p.dim, p.tokens}, B{p.d, p.ldd, p.ldd, p.tokens};
     f32x16 acc[T::kMi][T::kNi];
+    T::clear(acc);
     T::product(lds, A, B, m0, n0, 0, p.tokens, acc);
+    if (p.rests) {
+        const Operand R{p.d + (uint64_t)p.tokens * p.ldd, p.ldd, p.ldd, p.tokens};
+        T::product(lds, A, R, m0, n0, 0, p.tokens, acc);
+    }
     store_rows<T>(lds, p.dW + (uint64_t)(p.piece_begin + n0) * p.dim + m0, p.dim, p.dim - m0, len - n0,
                   [&](uint32_t i, uint32_t j, uint32_t r) {
                       return u32x2{f32_bf16(acc[i][j][r]) | (uint32_t)f32_bf16(acc[i][j][r + 1]) << 16,
@@ -608,11 +628,13 @@ bool dw_takes_big(uint64_t tokens, uint32_t len, uint32_t dim) { return tokens >
 constexpr uint64_t kAlign = 256;
 uint64_t up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
 
+constexpr uint32_t kRestTokens = 128;
+
 // Workspace: the loss's tile results and target logits; the gradient's d, fp32
 // dh and target roundings.  A piece of the vocabulary is what keeps d within
 // 256 MiB, at least 1024 entries, whole tiles.
 struct CeLayout {
-    uint32_t piece, ldd, splits, split_k;
+    uint32_t piece, ldd, rests, splits, split_k;
     uint64_t own, part, d, dh_part, loss_bytes, grad_bytes;
 };
 
@@ -623,7 +645,9 @@ CeLayout layout(uint64_t tokens, uint32_t vocab, uint32_t dim) {
     const uint64_t own_bytes = up(tokens * 4, kAlign);
     l.part = own_bytes;
     l.loss_bytes = l.part + up(tiles * tokens * 8, kAlign);
-    uint64_t piece = (256ull << 20) / (2 * tokens) / 1024 * 1024;
+    l.rests = tokens <= kRestTokens;
+    const uint64_t rows = tokens << l.rests;
+    uint64_t piece = (256ull << 20) / (2 * rows) / 1024 * 1024;
     piece = piece < 1024 ? 1024 : piece;
     piece = piece < up(vocab, 256) ? piece : up(vocab, 256);
     l.piece = (uint32_t)piece;
@@ -637,7 +661,7 @@ CeLayout layout(uint64_t tokens, uint32_t vocab, uint32_t dim) {
     l.split_k = (uint32_t)up((piece + splits - 1) / splits, kUnit);
     l.splits = (uint32_t)splits;   // the last ones may be empty: they leave zeros
     l.d = own_bytes;
-    l.dh_part = l.d + up(tokens * l.ldd * 2, kAlign);
+    l.dh_part = l.d + up(rows * l.ldd * 2, kAlign);
     l.grad_bytes = l.dh_part + up((uint64_t)l.splits * tokens * dim * 4, kAlign);
     return l;
 }
@@ -737,7 +761,7 @@ extern "C" int wc_ce_grad_async(const uint16_t* h, const uint16_t* W, const void
     p.own = reinterpret_cast<float*>(w + l.own);
     p.d = reinterpret_cast<uint16_t*>(w + l.d);
     p.dh_part = reinterpret_cast<float*>(w + l.dh_part);
-    p.ldd = l.ldd, p.split_k = l.split_k, p.splits = l.splits;
+    p.ldd = l.ldd, p.rests = l.rests, p.split_k = l.split_k, p.splits = l.splits;
     for (uint64_t v0 = 0; v0 < vocab; v0 += l.piece) {
         p.piece_begin = (uint32_t)v0;
         p.piece_end = (uint32_t)(v0 + l.piece < vocab ? v0 + l.piece : vocab);
