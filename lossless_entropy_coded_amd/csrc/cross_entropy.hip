@@ -475,24 +475,30 @@ __global__ __launch_bounds__(T::kThreads) void ce_d_kernel(CeParams p) {
         g[j] = own[j] < p.vocab ? p.dloss[t] : 0.0f;
         lse[j] = t < p.tokens ? p.lse[t] : 0.0f;
     }
-    for (uint32_t rest = 0; rest <= p.rests; ++rest) {
-        if (rest) __syncthreads();
-        store_rows<T>(lds, p.d + ((uint64_t)rest * p.tokens + n0) * p.ldd + mt * T::kBm, p.ldd, T::kBm, p.tokens - n0,
-                      [&](uint32_t i, uint32_t j, uint32_t r) {
-                          uint16_t b[4];
+    const auto values = [&](uint32_t i, uint32_t j, uint32_t r, bool rest) {
+        uint16_t b[4];
 #pragma unroll
-                          for (uint32_t e = 0; e < 4; ++e) {
-                              const uint32_t v = m0 + T::m(i, r + e);
-                              float x = __expf(acc[i][j][r + e] - lse[j]);
-                              if (v == own[j]) x -= 1.0f;
-                              x = v < p.piece_end && own[j] < p.vocab ? x * g[j] : 0.0f;
-                              b[e] = f32_bf16(x);
-                              const float lost = x - bf16_f32(b[e]);
-                              if (v == own[j] && v < p.piece_end) p.own[n0 + T::n(j)] = lost;
-                              if (rest) b[e] = f32_bf16(lost);
-                          }
-                          return u32x2{b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16};
-                      });
+        for (uint32_t e = 0; e < 4; ++e) {
+            const uint32_t v = m0 + T::m(i, r + e);
+            float x = __expf(acc[i][j][r + e] - lse[j]);
+            if (v == own[j]) x -= 1.0f;
+            x = v < p.piece_end && own[j] < p.vocab ? x * g[j] : 0.0f;
+            b[e] = f32_bf16(x);
+            const float lost = x - bf16_f32(b[e]);
+            if (v == own[j] && v < p.piece_end) p.own[n0 + T::n(j)] = lost;
+            if (rest) b[e] = f32_bf16(lost);
+        }
+        return u32x2{b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16};
+    };
+    uint16_t* const to = p.d + (uint64_t)n0 * p.ldd + mt * T::kBm;
+    store_rows<T>(lds, to, p.ldd, T::kBm, p.tokens - n0,
+                  [&](uint32_t i, uint32_t j, uint32_t r) { return values(i, j, r, false); });
+    if constexpr (!T::kAlternate) {   // few tokens never take big tiles
+        if (p.rests) {
+            __syncthreads();
+            store_rows<T>(lds, to + (uint64_t)p.tokens * p.ldd, p.ldd, T::kBm, p.tokens - n0,
+                          [&](uint32_t i, uint32_t j, uint32_t r) { return values(i, j, r, true); });
+        }
     }
 }
 
@@ -566,13 +572,27 @@ __global__ __launch_bounds__(256) void ce_zero_kernel(uint16_t* dW, uint64_t chu
         reinterpret_cast<f32x4*>(dW)[i] = (f32x4)(0.0f);
 }
 
-// dh in bf16: the splits in order, plus what d's target value lost to its rounding times W[target].
+constexpr uint32_t kRoundSlices = 8;                      // of the splits
+constexpr uint32_t kRoundCols = 256 / kRoundSlices * 4;   // columns per workgroup
+
+// dh in bf16: the splits, in order within each of 8 slices of them, then the
+// slices in order, plus what d's target value lost to its rounding times
+// W[target].
 __global__ __launch_bounds__(256) void ce_dh_round_kernel(CeParams p) {
-    const uint32_t t = blockIdx.x, at = (blockIdx.y * 256 + threadIdx.x) * 4;
-    if (at >= p.dim) return;
+    const uint32_t t = blockIdx.x, slice = threadIdx.x / (256 / kRoundSlices), lane = threadIdx.x % (256 / kRoundSlices);
+    const uint32_t at = blockIdx.y * kRoundCols + lane * 4;
+    __shared__ f32x4 shared[256];
+    const uint32_t per = (p.splits + kRoundSlices - 1) / kRoundSlices;
+    const uint32_t begin = slice * per, end = min(begin + per, p.splits);
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (uint32_t s = 0; s < p.splits; ++s)
-        v += *reinterpret_cast<const f32x4*>(p.dh_part + ((uint64_t)s * p.tokens + t) * p.dim + at);
+    if (at < p.dim)
+        for (uint32_t s = begin; s < end; ++s)
+            v += *reinterpret_cast<const f32x4*>(p.dh_part + ((uint64_t)s * p.tokens + t) * p.dim + at);
+    shared[threadIdx.x] = v;
+    __syncthreads();
+    if (slice != 0 || at >= p.dim) return;
+#pragma unroll
+    for (uint32_t k = 1; k < kRoundSlices; ++k) v += shared[threadIdx.x + k * (256 / kRoundSlices)];
     const uint32_t own = target_of(p, t);
     if (own < p.vocab) {
         const u32x2 w = *reinterpret_cast<const u32x2*>(p.W + (uint64_t)own * p.dim + at);
@@ -599,6 +619,7 @@ template <bool kAx, bool kBx>
 using Thin = Tile<kAx, kBx, 256, 64, 4, 1, 3, 64>;     // few tokens: bound by reading W, two stages ahead
 constexpr uint32_t kThinTokens = 64;
 constexpr uint32_t kCus = 256;
+constexpr uint32_t kRestTokens = 128;   // up to these, what d loses is kept (see above)
 
 uint32_t cdiv(uint64_t a, uint32_t b) { return (uint32_t)((a + b - 1) / b); }
 
@@ -613,13 +634,43 @@ bool takes_thin(uint64_t tokens, uint32_t vocab) { return tokens <= kThinTokens 
 // 1000 x 20000 x 2048 112 and 100; 200 x 100000 x 1024 81 and 90; 3000 x 4000 x
 // 704 33 and 33; 4096 x 131072 x 4096 3520 and 6400.
 bool takes_big(uint64_t m, uint64_t n) {
+    if (m <= kRestTokens || n <= kRestTokens) return false;
     const uint64_t big = (uint64_t)cdiv(m, 256) * cdiv(n, 256), mid = (uint64_t)cdiv(m, 128) * cdiv(n, 128);
     return 3 * cdiv(big, kCus) < 2 * cdiv(mid, 2 * kCus);
 }
-// dh has few outputs and a long sum, which is split: big tiles unless they are
-// very few (dh, big and mid, us: 515 x 32003 x 1160, 15 tiles, 111 and 96; 200 x
-// 100000 x 1024, 4 tiles, 160 and 91; 1000 x 20000 x 2048, 32 tiles, 95 and 116).
-bool dh_takes_big(uint64_t tokens, uint32_t dim) { return (uint64_t)cdiv(dim, 256) * cdiv(tokens, 256) >= 24; }
+// dh has few outputs and a long sum, which is split.  Tiles and splits are those
+// that a model of the time likes best: rounds of workgroups, each with a fixed
+// part and one per 64 of its sum (measured: 1.1 us in big tiles, 0.8 in mid and
+// thin ones), and the partial sums written and read once, at 4 TB/s.  One split
+// per sum, or a multiple of the dies (see ce_dh_kernel).  Measured (dh, us):
+// 4 tokens x 66561 x 488 40 with 65 splits of 1024 as of now; 515 x 32003 x
+// 1160 94 with 10 splits, 57 with 8.
+enum DhTile { kDhBig, kDhMid, kDhThin };
+struct DhPlan {
+    DhTile tile;
+    uint32_t splits;
+};
+DhPlan dh_plan(uint64_t tokens, uint32_t dim, uint64_t piece) {
+    DhPlan best{};
+    double best_us = 1e30;
+    const struct {
+        DhTile tile;
+        uint32_t m, n, slots;
+        double us;
+    } kinds[] = {{kDhBig, 256, 256, kCus, 1.1}, {kDhMid, 128, 128, 2 * kCus, 0.8}, {kDhThin, 256, 64, kCus, 0.8}};
+    for (const auto& k : kinds) {
+        if (k.tile == kDhThin && tokens > kThinTokens) continue;
+        const uint64_t tiles = (uint64_t)cdiv(dim, k.m) * cdiv(tokens, k.n);
+        for (uint32_t s = 1; s <= 16 * kDies; s = s == 1 ? kDies : s + kDies) {
+            if (s > 1 && (piece < s * kUnit || tiles * s > 4ull * k.slots)) break;
+            const double units = (double)((piece + s - 1) / s) / kUnit;
+            const double us = (double)((tiles * s + k.slots - 1) / k.slots) * (6.0 + units * k.us) +
+                              (double)s * (double)tokens * dim * 8 / 4e6;
+            if (us < best_us) best_us = us, best = {k.tile, s};
+        }
+    }
+    return best;
+}
 // dW: a short sum leaves the stores the most of the time, which two workgroups
 // per CU overlap with products (dW, big and mid, us: 515 x 32003 x 1160 74 and
 // 62; 200 x 100000 x 1024 142 and 120).
@@ -628,13 +679,12 @@ bool dw_takes_big(uint64_t tokens, uint32_t len, uint32_t dim) { return tokens >
 constexpr uint64_t kAlign = 256;
 uint64_t up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
 
-constexpr uint32_t kRestTokens = 128;
-
 // Workspace: the loss's tile results and target logits; the gradient's d, fp32
 // dh and target roundings.  A piece of the vocabulary is what keeps d within
 // 256 MiB, at least 1024 entries, whole tiles.
 struct CeLayout {
     uint32_t piece, ldd, rests, splits, split_k;
+    DhTile dh_tile;
     uint64_t own, part, d, dh_part, loss_bytes, grad_bytes;
 };
 
@@ -652,14 +702,11 @@ CeLayout layout(uint64_t tokens, uint32_t vocab, uint32_t dim) {
     piece = piece < up(vocab, 256) ? piece : up(vocab, 256);
     l.piece = (uint32_t)piece;
     l.ldd = (uint32_t)(piece + 128);   // an odd number of 256-byte lines: neighbouring rows in different memory channels
-    const uint32_t edge = tokens > kThinTokens && !dh_takes_big(tokens, dim) ? 128 : 256;
-    const uint64_t out_tiles = (uint64_t)cdiv(dim, edge) * cdiv(tokens, tokens <= kThinTokens ? kThinTokens : edge);
-    uint64_t splits = kCus * (edge == 128 ? 2 : 1) / out_tiles;
-    if (splits > kDies) splits = splits / kDies * kDies;
-    const uint64_t most = piece < 1024 ? 1 : piece / 1024;
-    splits = splits < 1 ? 1 : splits > most ? most : splits;
+    const DhPlan plan = dh_plan(tokens, dim, piece);
+    const uint32_t splits = plan.splits;
+    l.dh_tile = plan.tile;
     l.split_k = (uint32_t)up((piece + splits - 1) / splits, kUnit);
-    l.splits = (uint32_t)splits;   // the last ones may be empty: they leave zeros
+    l.splits = splits;   // the last ones may be empty: they leave zeros
     l.d = own_bytes;
     l.dh_part = l.d + up(rows * l.ldd * 2, kAlign);
     l.grad_bytes = l.dh_part + up((uint64_t)l.splits * tokens * dim * 4, kAlign);
@@ -771,8 +818,8 @@ extern "C" int wc_ce_grad_async(const uint16_t* h, const uint16_t* W, const void
         else if (takes_big(len, tokens)) run_d<Big<false, false>>(p, s);
         else run_d<Mid<false, false>>(p, s);
         if (dh) {
-            if (tokens <= kThinTokens) run_dh<Thin<true, false>>(p, s);
-            else if (dh_takes_big(tokens, dim)) run_dh<Big<true, false>>(p, s);
+            if (l.dh_tile == kDhThin) run_dh<Thin<true, false>>(p, s);
+            else if (l.dh_tile == kDhBig) run_dh<Big<true, false>>(p, s);
             else run_dh<Mid<true, false>>(p, s);
         }
         if (dW) {
@@ -781,6 +828,6 @@ extern "C" int wc_ce_grad_async(const uint16_t* h, const uint16_t* W, const void
         }
     }
     if (dh)
-        hipLaunchKernelGGL(ce_dh_round_kernel, dim3(p.tokens, cdiv(dim, 1024)), dim3(256), 0, s, p);
+        hipLaunchKernelGGL(ce_dh_round_kernel, dim3(p.tokens, cdiv(dim, kRoundCols)), dim3(256), 0, s, p);
     return hipGetLastError() == hipSuccess ? WC_OK : WC_ERR_HIP;
 }
