@@ -220,7 +220,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
         x_from[round] = v < p.vecs ? (v * p.cols + job % S::kSlab * kStepCols + r * 8) * 2 : kNoChunk;
     }
 
-    // Start the loads of a slab.
+    // Start the loads of a slab.  The uniform part of an offset stays within the buffer: past its end (in the last
+    // slab, or the one after it) the range check of a lane's part, which subtracts it, could wrap.
     const auto load = [&](uint32_t slab) {
         Loads l;
         const uint32_t c0 = slab * S::kSlab * kStepCols;
@@ -228,22 +229,22 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
         for (uint32_t round = 0; round < S::kRounds; ++round) {
             const uint32_t c = c0 + (round * 4 + q) % S::kSlab * kStepCols + r * 8;
             l.x[round] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                x_buf, c < p.cols ? x_from[round] : kNoChunk, c0 * 2, 0));
+                x_buf, c < p.cols ? x_from[round] : kNoChunk, min(c0, p.cols) * 2, 0));
         }
 #pragma unroll
         for (uint32_t st = 0; st < S::kSlab; ++st) {
-            const uint32_t cs = c0 + st * kStepCols, c = cs + lq * 32;
+            const uint32_t cs = c0 + st * kStepCols, c = cs + lq * 32, uniform = min(cs, p.cols) / 2;
             const bool inside = c < p.cols;
 #pragma unroll
             for (int i = 0; i < kTiles; ++i) {
                 if (kWhole) {
                     l.w[st][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                        codes_buf, inside ? code_at[i] : kNoChunk, cs / 2, 0));
+                        codes_buf, inside ? code_at[i] : kNoChunk, uniform, 0));
                 } else {
 #pragma unroll
                     for (uint32_t d = 0; d < 4; ++d)
                         l.w[st][i][d] = __builtin_amdgcn_raw_buffer_load_b32(
-                            codes_buf, c + d * 8 < p.cols ? code_at[i] + d * 4 : kNoChunk, cs / 2, 0);
+                            codes_buf, c + d * 8 < p.cols ? code_at[i] + d * 4 : kNoChunk, uniform, 0);
                 }
             }
         }

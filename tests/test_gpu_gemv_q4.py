@@ -193,3 +193,15 @@ def test_scales_off_their_alignment(wc, cols, vecs):
     assert within(y, x.double() @ w.t(), q4_tolerance(w, x.double()))
     y2 = _run(wc, wc.Q4Matrix(codes, shifted, rows, cols, group, zeros=shifted_z), x.cuda())
     assert torch.equal(y.view(torch.int32), y2.view(torch.int32))
+
+
+@pytest.mark.parametrize("vecs", [1, 2, 5, 16])
+@pytest.mark.parametrize("cols", [8, 104, 112, 120, 1144, 2024, 4088])
+def test_columns_end_just_before_a_step(wc, cols, vecs):
+    """The last workgroup has one row, so that its codes end where a step's uniform offset may already be past them."""
+    rows, group = 17, 64
+    codes, scales, z, w = q4_case(rows, cols, group, True, cols)
+    x = torch.randn(vecs, cols, generator=torch.Generator().manual_seed(vecs)).to(torch.bfloat16)
+    log(f"case: gemv_q4 {rows}x{cols}, {vecs} vectors, the last step a few columns short")
+    y = _run(wc, wc.Q4Matrix(codes, scales, rows, cols, group, zeros=z), x.cuda())
+    assert within(y, x.double() @ w.t(), q4_tolerance(w, x.double()))
