@@ -491,7 +491,7 @@ extern "C" int wc_embed_q4_async(const wc_q4_matrix* W, const void* ids, uint32_
     p.ids = ids, p.id_bytes = id_bytes, p.n = n, p.out = out;
     p.codes = reinterpret_cast<const uint32_t*>(W->codes), p.scales = W->scales, p.zeros = W->zeros;
     p.vocab = W->rows, p.chunks = W->cols / 8, p.scale = scale;
-    p.group = W->group, p.groups = (W->cols + W->group - 1) / W->group;
+    p.group = W->group, p.groups = W->group < W->cols ? (W->cols + W->group - 1) / W->group : 1;
     return launch_lookup(p, true, static_cast<hipStream_t>(stream));
 }
 

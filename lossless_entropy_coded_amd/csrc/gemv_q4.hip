@@ -488,7 +488,7 @@ extern "C" int wc_gemv_q4_async(const wc_q4_matrix* W, const uint16_t* x, uint32
     Q4Params p{};
     p.codes = W->codes, p.scales = W->scales, p.zeros = W->zeros, p.x = x, p.y = y;
     p.rows = W->rows, p.cols = W->cols, p.group = W->group, p.vecs = n_vecs;
-    p.groups = (W->cols + W->group - 1) / W->group;
+    p.groups = W->group < W->cols ? (W->cols + W->group - 1) / W->group : 1;
     // ceil(2^32 / m), m chunks per group: exact for fewer than 2^16 chunks of m < 2^16 (there are 2^11 at most)
     const uint32_t m = W->group < W->cols ? W->group / 32 : 1u << 15;
     p.group_magic = m == 1 ? 0 : (uint32_t)((0x100000000ull + m - 1) / m);

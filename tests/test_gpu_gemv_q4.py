@@ -205,3 +205,17 @@ def test_columns_end_just_before_a_step(wc, cols, vecs):
     log(f"case: gemv_q4 {rows}x{cols}, {vecs} vectors, the last step a few columns short")
     y = _run(wc, wc.Q4Matrix(codes, scales, rows, cols, group, zeros=z), x.cuda())
     assert within(y, x.double() @ w.t(), q4_tolerance(w, x.double()))
+
+
+@pytest.mark.parametrize("group", [4096, 1 << 20, 0xFFFFFFE0])
+def test_one_scale_per_row_whatever_the_group(wc, group):
+    rows, cols = 40, 1152
+    codes, scales, z, w = q4_case(rows, cols, group, True, 3)
+    x = torch.randn(2, cols, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16)
+    log(f"case: gemv_q4 and lookup, group {group}")
+    matrix = wc.Q4Matrix(codes, scales, rows, cols, group, zeros=z)
+    assert within(_run(wc, matrix, x.cuda()), x.double() @ w.t(), q4_tolerance(w, x.double()))
+    out = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    wc.embed_q4_async(matrix, torch.arange(rows, device="cuda"), rows, out)
+    # scale (8 bits) times code less zero point (5 bits) is exact in fp32, so out is w rounded once
+    assert torch.equal(out.cpu(), w.to(torch.bfloat16))
