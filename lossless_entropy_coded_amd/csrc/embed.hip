@@ -530,10 +530,11 @@ extern "C" int wc_embed_grad_async(const uint16_t* dout, const void* ids, uint32
     // Rows without tokens: where tokens are at most half as many as rows, the whole table is set to zero beside the
     // sort, whose few workgroups leave the memory idle, and rows with tokens are written again; else the summing
     // launch writes only the rows that have none.
-    const bool ahead = !p.accumulate && n && n <= vocab / 2;
+    // (A launch holds fewer than 2^32 threads of 16 bytes each, so tables from 32 GiB on are left to the second way.)
+    const uint64_t table_bytes = (uint64_t)vocab * dim * (p.bf16 ? 2 : 4);
+    const bool ahead = !p.accumulate && n && n <= vocab / 2 && table_bytes < (32ull << 30);
     p.row_blocks = p.accumulate || ahead ? 0 : (vocab + kFillRows - 1) / kFillRows;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    const uint64_t table_bytes = (uint64_t)vocab * dim * (p.bf16 ? 2 : 4);
     if (n) launch_sort_ids(ids, id_bytes, p.n, vocab, p.sorted, scratch, s, ahead ? dtable : nullptr, table_bytes);
     hipLaunchKernelGGL(embed_sum_kernel, dim3((p.runs + p.row_blocks) * p.col_blocks), dim3(kSumThreads), 0, s, p);
     if (p.runs > 1) {

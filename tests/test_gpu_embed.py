@@ -200,3 +200,30 @@ def test_side_stream_and_graph(wc):
         wc.embed_async(table, vocab, dim, ids, n, rows, scale=2.0, stream=side)
         side.synchronize()
         assert torch.equal(out, rows) and torch.equal(grad, want)
+
+
+def test_gradient_of_a_table_beyond_a_launch(wc):
+    """More 16-byte pieces than a launch has threads: every row is written all the same."""
+    vocab, dim, n = 1 << 22, 8256, 100
+    if torch.cuda.mem_get_info()[0] < (vocab * dim * 2) * 5 // 4:
+        pytest.skip("needs 87 GB of device memory")
+    g = torch.Generator().manual_seed(8)
+    ids = torch.randint(0, vocab, (n,), generator=g)
+    ids[0], ids[1] = 0, vocab - 1
+    dout = torch.randn(n, dim, generator=g).to(torch.bfloat16)
+    log(f"case: embed_grad {vocab}x{dim} bf16, {n} tokens")
+    table = torch.full((vocab, dim), 1.0, dtype=torch.bfloat16, device="cuda")
+    work = torch.empty(wc.embed_grad_work_bytes(n, dim), dtype=torch.uint8, device="cuda")
+    wc.embed_grad_async(dout.cuda(), ids.cuda(), n, table, vocab, dim, work, work.numel(), out="bf16")
+    torch.cuda.synchronize()
+    rows, where = ids.unique(return_inverse=True)
+    want = torch.zeros(len(rows), dim, dtype=torch.float64).index_add_(0, where, dout.double())
+    mag = torch.zeros(len(rows), dim, dtype=torch.float64).index_add_(0, where, dout.double().abs())
+    got = table[rows.cuda()]
+    # fewer than n sums within 2^-24 each, then one rounding to bf16
+    assert bool(((got.cpu().double() - want).abs() <= mag * n * 2.0 ** -24 + want.abs() * 2.0 ** -8).all())
+    table[rows.cuda()] = 0
+    for part in table.view(torch.int16).split(1 << 17):
+        assert int(part.count_nonzero()) == 0, "a row without tokens was not written"
+    del table, part
+    torch.cuda.empty_cache()
