@@ -314,6 +314,7 @@ int wc_gemv_bf16_async(const uint16_t* W, uint32_t rows, uint32_t cols, const ui
 #define WC_MAX_VOCAB  (1u << 22)
 #define WC_MAX_DIM    (1u << 16)
 #define WC_MAX_TOKENS (1u << 20)
+#define WC_MAX_LOGITS (1ull << 38)   /* tokens times vocabulary of one cross entropy call */
 
 /*
  * A matrix of 4-bit codes with group scales in device memory, the integer
@@ -341,9 +342,8 @@ int wc_q4_check(const wc_q4_matrix* W);
  * that are verified at once (LazyWeights review: prompt lookup).  One launch.
  *   x   device, n_vecs x cols bf16, 16-byte aligned;
  *   y   device, n_vecs x rows float32 (written), 4-byte aligned.
- * n_vecs is at most WC_GEMV_Q4_MAX_VECS.  Sums are held in fp32 or exact
- * integers and taken in a fixed order: y is a deterministic function of the
- * bits of W and x.  rows == 0 or n_vecs == 0 is a no-op.  WC_ERR_INVALID_ARG
+ * n_vecs is at most WC_GEMV_Q4_MAX_VECS.  Sums are held in fp32 and taken in
+ * a fixed order: y is a deterministic function of the bits of W and x.  rows == 0 or n_vecs == 0 is a no-op.  WC_ERR_INVALID_ARG
  * for bad sizes or alignment, WC_ERR_HIP if the launch fails.
  */
 #define WC_GEMV_Q4_MAX_VECS 16u
@@ -407,6 +407,7 @@ int wc_embed_grad_async(const uint16_t* dout, const void* ids, uint32_t id_bytes
  *            wc_ce_work_bytes(tokens, vocab, dim, grad) bytes (grad 0: enough
  *            for the loss; else for both calls), overwritten; calls that may
  *            overlap need one each.
+ * tokens * vocab is at most WC_MAX_LOGITS (larger batches: call by call).
  * z is accumulated in fp32; the gradient keeps a piece of the vocabulary's d
  * at a time, in bf16.  Results are the same bits on every run.  tokens == 0
  * is a no-op, but for dW, which is then zero.  The gradient takes the lse

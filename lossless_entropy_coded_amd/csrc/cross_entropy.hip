@@ -715,7 +715,7 @@ CeLayout layout(uint64_t tokens, uint32_t vocab, uint32_t dim) {
 
 bool sizes_fit(uint64_t tokens, uint32_t vocab, uint32_t dim) {
     return tokens <= WC_MAX_TOKENS && vocab != 0 && vocab <= WC_MAX_VOCAB && dim != 0 && dim % 8 == 0 &&
-           dim <= WC_MAX_DIM;
+           dim <= WC_MAX_DIM && tokens * vocab <= WC_MAX_LOGITS;   // (a launch holds fewer than 2^32 threads)
 }
 
 bool aligned(const void* p, uintptr_t a) { return p && (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

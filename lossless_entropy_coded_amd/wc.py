@@ -492,6 +492,7 @@ def decode_gemv_noalloc_async(plan: Plan, blob_dev, ops, stream=None) -> None:
 MAX_VOCAB = 1 << 22
 MAX_DIM = 1 << 16
 MAX_TOKENS = 1 << 20
+MAX_LOGITS = 1 << 38   # tokens times vocabulary of one cross entropy call
 GEMV_Q4_MAX_VECS = 16
 OUT_KINDS = {"f32": 0, "bf16": 1}
 

@@ -128,6 +128,19 @@ def test_cross_entropy_refusals(wc):
             wc.ce_work_bytes(*bad)
 
 
+def test_cross_entropy_calls_hold_in_a_launch(wc):
+    """A tile of z is a workgroup: a call has tiles for fewer than 2^32 threads, or is refused."""
+    most = wc.MAX_LOGITS
+    for tokens, vocab, more in ((1 << 20, most >> 20, (0, 1)), (most >> 22, 1 << 22, (1, 0))):
+        assert wc.ce_work_bytes(tokens, vocab, 64) > 0
+        tokens, vocab = tokens + more[0], vocab + more[1]
+        with pytest.raises(wc.WCError):
+            wc.ce_work_bytes(tokens, vocab, 64)
+        args, work = (P, P, P, 8, tokens, vocab, 64), 1 << 60
+        assert wc._lib.wc_ce_loss_async(*args, P, P, P, work, None) == INV
+        assert wc._lib.wc_ce_grad_async(*args, P, P, P, P, P, work, None) == INV
+
+
 # ---- the binding's checks of tensors -----------------------------------------------
 
 
