@@ -398,7 +398,7 @@ int wc_embed_grad_async(const uint16_t* dout, const void* ids, uint32_t id_bytes
  *            16-byte aligned, dim a multiple of 8;
  *   targets  device, tokens ids of target_bytes (4: int32, 8: int64); one
  *            outside [0, vocab) marks a token without a loss (loss 0, no
- *            gradient whatever dloss holds there; its lse is still written);
+ *            gradient whatever dloss and its row of h hold; its lse is still written);
  *   loss, lse  device, tokens float32 (written);
  *   dloss    device, tokens float32: the gradient of each token's loss;
  *   dh, dW   device, bf16 as h and W (written), or NULL where not wanted

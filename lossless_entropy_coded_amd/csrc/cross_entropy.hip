@@ -6,7 +6,8 @@
 //   d[t][v] = (exp(z[t][v] - lse[t]) - [v = target[t]]) dloss[t],
 //   dh = d W,   dW = d^T h.
 // A target outside [0, vocab) marks a token without a loss: its loss, and its
-// rows of d, are zero.
+// rows of d, are zero.  dW takes h with such rows zero too (copied beside the
+// first piece's d), as what stands there may be no number.
 //
 // The loss takes one matrix product whose tiles never leave the chip: each
 // workgroup computes a tile of z in fp32 accumulators and leaves, per token,
@@ -355,6 +356,7 @@ struct CeParams {
     float2* part;              // loss: per vocabulary tile and token, {maximum, sum of exp(z - maximum)}
     float* own;                // loss: the target's logit; gradient: the rounding of the target's d
     uint16_t* d;               // gradient: d of one piece, [token][ldd]
+    uint16_t* h_own;           // gradient: h of the tokens with a loss, zeros for others
     float* dh_part;            // gradient: dh in fp32, [split][token][dim]
     uint32_t ldd;
     uint32_t rests;            // d is followed by what its values lost to rounding, laid out the same
@@ -461,6 +463,16 @@ __global__ __launch_bounds__(T::kThreads) void ce_d_kernel(CeParams p) {
                  nt))
         return;
     const uint32_t m0 = p.piece_begin + mt * T::kBm, n0 = nt * T::kBn;
+    if (p.first && p.dW) {   // the tile's share of h_own
+        const uint32_t chunks = p.dim / 8, count = min(T::kBn, p.tokens - n0) * chunks;
+        const uint32_t step = (p.piece_end - p.piece_begin + T::kBm - 1) / T::kBm * T::kThreads;
+        for (uint32_t i = mt * T::kThreads + threadIdx.x; i < count; i += step) {
+            const uint64_t at = (uint64_t)n0 * chunks + i;
+            u32x4 v = {0, 0, 0, 0};
+            if (target_of(p, n0 + i / chunks) < p.vocab) v = reinterpret_cast<const u32x4*>(p.h)[at];
+            reinterpret_cast<u32x4*>(p.h_own)[at] = v;
+        }
+    }
     const Operand A{p.W, p.dim, p.vocab, p.dim}, B{p.h, p.dim, p.tokens, p.dim};
     f32x16 acc[T::kMi][T::kNi];
     T::clear(acc);
@@ -502,7 +514,7 @@ __global__ __launch_bounds__(T::kThreads) void ce_d_kernel(CeParams p) {
     }
 }
 
-// dh += d W over the piece, in fp32, the vocabulary split over blockIdx.y.
+// dh += d W over the piece, in fp32, the vocabulary in one split or a multiple of the dies.
 template <class T>
 __global__ __launch_bounds__(T::kThreads) void ce_dh_kernel(CeParams p) {
     __shared__ __align__(16) uint16_t lds[T::kLdsElems];
@@ -513,9 +525,8 @@ __global__ __launch_bounds__(T::kThreads) void ce_dh_kernel(CeParams p) {
         const uint32_t i = blockIdx.x / kDies, tile = i % (ms * ns);
         split = blockIdx.x % kDies + i / (ms * ns) * kDies;
         mt = tile % ms, nt = tile / ms;
-    } else {
-        split = blockIdx.y;
-        if (!tile_of(blockIdx.x, ms, ns, mt, nt)) return;
+    } else if (!tile_of(blockIdx.x, ms, ns, mt, nt)) {
+        return;
     }
     const uint32_t m0 = mt * T::kBm, n0 = nt * T::kBn;
     const uint32_t len = p.piece_end - p.piece_begin;
@@ -551,7 +562,7 @@ __global__ __launch_bounds__(T::kThreads) void ce_dw_kernel(CeParams p) {
     uint32_t mt, nt;
     if (!tile_of(blockIdx.x, (p.dim + T::kBm - 1) / T::kBm, (len + T::kBn - 1) / T::kBn, mt, nt)) return;
     const uint32_t m0 = mt * T::kBm, n0 = nt * T::kBn;
-    const Operand A{p.h, p.dim, p.dim, p.tokens}, B{p.d, p.ldd, p.ldd, p.tokens};
+    const Operand A{p.h_own, p.dim, p.dim, p.tokens}, B{p.d, p.ldd, p.ldd, p.tokens};
     f32x16 acc[T::kMi][T::kNi];
     T::clear(acc);
     T::product(lds, A, B, m0, n0, 0, p.tokens, acc);
@@ -680,12 +691,12 @@ constexpr uint64_t kAlign = 256;
 uint64_t up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
 
 // Workspace: the loss's tile results and target logits; the gradient's d, fp32
-// dh and target roundings.  A piece of the vocabulary is what keeps d within
+// dh, target roundings and h of the tokens with a loss.  A piece of the vocabulary is what keeps d within
 // 256 MiB, at least 1024 entries, whole tiles.
 struct CeLayout {
     uint32_t piece, ldd, rests, splits, split_k;
     DhTile dh_tile;
-    uint64_t own, part, d, dh_part, loss_bytes, grad_bytes;
+    uint64_t own, part, d, dh_part, h_own, loss_bytes, grad_bytes;
 };
 
 CeLayout layout(uint64_t tokens, uint32_t vocab, uint32_t dim) {
@@ -709,7 +720,8 @@ CeLayout layout(uint64_t tokens, uint32_t vocab, uint32_t dim) {
     l.splits = splits;   // the last ones may be empty: they leave zeros
     l.d = own_bytes;
     l.dh_part = l.d + up(rows * l.ldd * 2, kAlign);
-    l.grad_bytes = l.dh_part + up((uint64_t)l.splits * tokens * dim * 4, kAlign);
+    l.h_own = l.dh_part + up((uint64_t)l.splits * tokens * dim * 4, kAlign);
+    l.grad_bytes = l.h_own + up(tokens * dim * 2, kAlign);
     return l;
 }
 
@@ -735,7 +747,7 @@ void run_d(CeParams& p, hipStream_t s) {
 template <class T>
 void run_dh(CeParams& p, hipStream_t s) {
     const uint32_t ms = cdiv(p.dim, T::kBm), ns = cdiv(p.tokens, T::kBn);
-    const dim3 grid = p.splits % kDies == 0 ? dim3(ms * ns * p.splits) : dim3(tile_grid(ms, ns), p.splits);
+    const dim3 grid = p.splits % kDies == 0 ? dim3(ms * ns * p.splits) : dim3(tile_grid(ms, ns));
     hipLaunchKernelGGL(ce_dh_kernel<T>, grid, dim3(T::kThreads), 0, s, p);
 }
 template <class T>
@@ -808,6 +820,7 @@ extern "C" int wc_ce_grad_async(const uint16_t* h, const uint16_t* W, const void
     p.own = reinterpret_cast<float*>(w + l.own);
     p.d = reinterpret_cast<uint16_t*>(w + l.d);
     p.dh_part = reinterpret_cast<float*>(w + l.dh_part);
+    p.h_own = reinterpret_cast<uint16_t*>(w + l.h_own);
     p.ldd = l.ldd, p.rests = l.rests, p.split_k = l.split_k, p.splits = l.splits;
     for (uint64_t v0 = 0; v0 < vocab; v0 += l.piece) {
         p.piece_begin = (uint32_t)v0;

@@ -167,6 +167,25 @@ def test_non_finite_logits(wc):
     assert torch.equal(loss2[rest.cuda()], loss[rest.cuda()])
 
 
+@pytest.mark.parametrize("tokens,vocab,dim", [(9, 300, 72), (150, 2000, 264), (700, 2300, 128)])
+def test_tokens_without_a_loss_hold_anything(wc, tokens, vocab, dim):
+    """Infinities and NaNs in h, lse and dloss of tokens without a target leave every gradient's bits as they were."""
+    h, W, t, dloss = _inputs(tokens, vocab, dim, 11)
+    Wd, td = W.cuda(), t.cuda()
+    off = (t < 0) | (t >= vocab)
+    log(f"case: ce {tokens}x{vocab}x{dim}, tokens without a target not finite")
+    loss, lse = _loss(wc, h.cuda(), Wd, td)
+    dh, dW = _grad(wc, h.cuda(), Wd, td, lse, dloss.cuda())
+    where = off.nonzero().flatten()
+    h[where] = float("nan")
+    h[where[0], ::2] = float("inf")
+    dloss[where] = float("nan")
+    loss2, lse2 = _loss(wc, h.cuda(), Wd, td)
+    assert torch.equal(loss2, loss) and torch.equal(lse2[~off.cuda()], lse[~off.cuda()])
+    dh2, dW2 = _grad(wc, h.cuda(), Wd, td, lse2, dloss.cuda())
+    assert torch.equal(dh2, dh) and torch.equal(dW2, dW)
+
+
 def test_no_tokens(wc):
     """No tokens: nothing but a zero dW."""
     W = torch.randn(50, 16).to(BF16).cuda()
