@@ -367,7 +367,7 @@ int wc_embed_q4_async(const wc_q4_matrix* W, const void* ids, uint32_t id_bytes,
 
 /*
  * wc_embed_grad_async -- the table's gradient: dtable[v] = scale * (sum over
- * the t with id[t] = v of dout[t]), summed in fp32 in token order, the same
+ * the t with id[t] = v of dout[t]), summed in fp32 in a fixed order, the same
  * bits on every run.
  *   dout      device, n x dim bf16, 16-byte aligned;
  *   dtable    device, vocab x dim, 16-byte aligned: float32 (out_kind

@@ -10,21 +10,22 @@
 // The lookup moves bytes only: a thread reads and writes 8 columns (16 bytes
 // of bf16, 4 of codes), the tokens of a workgroup as many as fill it.
 //
-// The gradient sums each row's tokens in token order, so it is the same bits
-// on every run.  Tokens are sorted by row: blocks of 4096 by a bitonic network
+// The gradient sums each row's tokens in a fixed order (token order within a
+// run), so it is the same bits on every run.  Tokens are sorted by row: blocks of 4096 by a bitonic network
 // whose keys (row, place in the block) fit 32 bits and stay in registers, four
-// per lane, with all but the ten widest of its 78 exchanges inside a wave
-// (about 10 us; 38 with every exchange through LDS and 64-bit keys).  Then
-// every token's place is its place in its block plus, for each other block,
-// the number of smaller keys there: binary searches over the blocks' sorted
-// rows, in LDS.  The sorted tokens
-// are cut into runs of kRun; a workgroup walks a run, eight rows of the
-// gradient on their way at a time, and sums each row's tokens in fp32.  A row
-// whose tokens lie in one run is finished there; one that crosses runs leaves
-// a partial sum per run, joined in run order by the last kernel.  Rows without
-// tokens are zero (unless the call accumulates): with a large table writing
-// them is most of the bytes, and the memory's rate for writes bounds the call,
-// so the table is set to zero beside the sort where that costs little.
+// per lane, with all but the ten widest of its 78 exchanges inside a wave (17
+// us; 38 with every exchange through LDS and 64-bit keys.  It is a chain of
+// dependent steps: exchanges by lane swaps in place of __shfl_xor, and one
+// v_med3 per key and step, take it to 16 to 19).  Then every token's place is
+// its place in its block plus, for each other block, the number of smaller
+// keys there: binary searches over the blocks' sorted rows, in LDS.  The sorted
+// tokens are cut into runs of up to kRun; a workgroup walks a run, eight rows
+// of the gradient on their way at a time, and sums each row's tokens in fp32.
+// A row whose tokens lie in one run is finished there; one that crosses runs
+// leaves a partial sum per run, joined in a fixed order by the last kernel.
+// Rows without tokens are zero (unless the call accumulates): with a large table
+// writing them is most of the bytes, and the memory's rate for writes bounds the
+// call, so the table is set to zero beside the sort where that costs little.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

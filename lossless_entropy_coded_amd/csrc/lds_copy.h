@@ -27,15 +27,11 @@ __device__ __forceinline__ u32x4 buffer_words(const void* p, uint32_t bytes) {
 // in order with other loads; the caller does the waiting that is needed before
 // LDS is read.  In assembly because the compiler, for the builtin, waits for
 // every such copy before each transposing LDS read; but then it does not count
-// the copy when it waits for other loads, so kernels without such reads take
-// copy_to_lds_counted.
+// the copy when it waits for other loads, so a kernel keeps no loads into
+// registers on their way beside it.
 __device__ __forceinline__ void copy_to_lds(uint32_t to, const u32x4& rsrc, uint32_t offset) {
     asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(offset), "s"(rsrc)
                  : "memory", "m0");
-}
-
-__device__ __forceinline__ void copy_to_lds_counted(void* to, const __amdgpu_buffer_rsrc_t& rsrc, uint32_t offset) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)to, 16, offset, 0, 0, 0);
 }
 
 }  // namespace wc

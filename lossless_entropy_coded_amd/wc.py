@@ -605,7 +605,7 @@ def embed_grad_work_bytes(n: int, dim: int) -> int:
 
 def embed_grad_async(dout_dev, ids_dev, n: int, dtable_dev, vocab: int, dim: int, work_dev, work_bytes: int,
                      out: str = "f32", scale: float = 1.0, accumulate: bool = False, stream=None) -> None:
-    """wc_embed_grad_async: dtable[v] = scale * sum of dout[t] over the t with ids[t] = v, in fp32 and token order.
+    """wc_embed_grad_async: dtable[v] = scale * sum of dout[t] over the t with ids[t] = v, in fp32 and a fixed order.
 
     out: "f32" or "bf16", dtable's type.  accumulate: add to dtable instead of writing every row."""
     call = "wc_embed_grad_async"

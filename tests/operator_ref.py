@@ -25,8 +25,9 @@ def q4_tolerance(w, x):
     group's, is exact or rounded within 24 sequential fp32 operations of the
     products' magnitudes (8 products, the group's scale, the join of lanes and
     waves); groups follow each other, one step per 128 columns at most.  x may
-    be held in fixed point relative to the largest |x| of 128 columns, within
-    2^-31 of it.  w: rows x cols, x: vecs x cols, both 64-bit."""
+    be held relative to a larger |x| near it: in f16, scaled for the largest of
+    at most 512 columns, it is off by less than 2^-39 of that one, for which
+    2^-30 of the largest of its own 128 columns stands.  w: rows x cols, x: vecs x cols, both 64-bit."""
     cols = w.shape[1]
     pad = -cols % 128
     xm = torch.nn.functional.pad(x.abs(), (0, pad)).reshape(x.shape[0], -1, 128).amax(dim=2)
