@@ -25,7 +25,7 @@
 // leaves a partial sum per run, joined in a fixed order by the last kernel.
 // Rows without tokens are zero (unless the call accumulates): with a large table
 // writing them is most of the bytes, and the memory's rate for writes bounds the
-// call, so the table is set to zero beside the sort where that costs little.
+// call, so they are written beside the launches that leave the memory idle.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -119,6 +119,7 @@ struct GradParams {
     uint32_t id_bytes, n, vocab, dim, runs, run_log2;
     uint32_t bf16, accumulate;
     uint32_t col_blocks, row_blocks;
+    uint32_t filled;      // rows that are set to zero before this launch
     float scale;
 };
 
@@ -131,11 +132,13 @@ struct SortParams {
     uint32_t* rows;        // per block, in order (several blocks)
     uint32_t* tokens;
     uint32_t blocks;
+    uint32_t rank_blocks;  // workgroups that rank
     u32x4* fill;           // memory that further workgroups of the launch set to zero
     uint64_t fill_chunks;  // 16 bytes each
 };
 
-// Per thread, not kept in caches: 154 us at 16384 tokens, 32768 x 4096 (2 chunks: 160, 8: 168; kept: 172).
+// Per thread, not kept in caches: with the whole table set here, 154 us at 16384 tokens, 32768 x 4096 (2 chunks: 160,
+// 8: 168; kept: 172).
 constexpr uint32_t kFillChunks = 1;
 
 // The keys of a block in order: four per thread, keys 4 t .. 4 t + 3.
@@ -207,10 +210,17 @@ __global__ __launch_bounds__(kSortThreads) void sort_block_kernel(SortParams p) 
 
 constexpr uint32_t kRankThreads = 1024;
 constexpr uint32_t kRankKeys = 32768;   // rows of other blocks in LDS at a time (128 KB)
+constexpr uint32_t kRankFillers = 240;  // filling workgroups at most: about one per CU, as the LDS allows (480 are no faster)
 
 // Every token's place: its place in its block, and the smaller keys of the
 // other blocks, whose sorted rows come through LDS.
 __global__ __launch_bounds__(kRankThreads) void sort_rank_kernel(SortParams p) {
+    if (blockIdx.x >= p.rank_blocks) {
+        const uint64_t step = (uint64_t)(gridDim.x - p.rank_blocks) * kRankThreads;
+        for (uint64_t at = (uint64_t)(blockIdx.x - p.rank_blocks) * kRankThreads + threadIdx.x; at < p.fill_chunks; at += step)
+            __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, p.fill + at);
+        return;
+    }
     __shared__ uint32_t rows[kRankKeys];
     const uint32_t i = blockIdx.x * kRankThreads + threadIdx.x, log2 = p.block_log2, block = 1u << log2;
     const bool there = i < p.n;
@@ -277,7 +287,7 @@ __global__ __launch_bounds__(kSumThreads) void embed_sum_kernel(GradParams p) {
     const uint32_t col = cb * kSumCols + threadIdx.x * 8;
     if (job >= p.runs) {   // rows without tokens
         __shared__ uint32_t empty[kFillRows];
-        const uint32_t row0 = (job - p.runs) * kFillRows;
+        const uint32_t row0 = p.filled + (job - p.runs) * kFillRows;
         if (threadIdx.x < kFillRows) {
             const uint32_t row = row0 + threadIdx.x;
             uint32_t lo = 0, hi = p.n;   // the first key of a row >= this one
@@ -289,16 +299,14 @@ __global__ __launch_bounds__(kSumThreads) void embed_sum_kernel(GradParams p) {
             empty[threadIdx.x] = row < p.vocab && (lo == p.n || row_of(p.sorted[lo]) != row);
         }
         __syncthreads();
-        if (col >= p.dim) return;
+        // 16 bytes per lane and store, side by side: whole lines, not kept in caches
+        const uint32_t row_chunks = p.dim / 8 << !p.bf16, chunk0 = cb * kSumThreads << !p.bf16;
+        const uint32_t end = min(row_chunks, chunk0 + (kSumThreads << !p.bf16));
         for (uint32_t r = 0; r < kFillRows; ++r) {
             if (!empty[r]) continue;
-            const uint64_t at = (uint64_t)(row0 + r) * p.dim + col;
-            if (p.bf16) {
-                *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.dtable) + at) = u32x4{0, 0, 0, 0};
-            } else {
-                f32x4* const d = reinterpret_cast<f32x4*>(static_cast<float*>(p.dtable) + at);
-                d[0] = d[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            }
+            u32x4* const row = static_cast<u32x4*>(p.dtable) + (uint64_t)(row0 + r) * row_chunks;
+            for (uint32_t c = chunk0 + threadIdx.x; c < end; c += kSumThreads)
+                __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, row + c);
         }
         return;
     }
@@ -441,12 +449,17 @@ int launch_lookup(LookupParams& p, bool q4, hipStream_t s) {
 
 }  // namespace
 
+uint32_t sort_block_log2(uint32_t vocab) {
+    uint32_t log2 = 12;
+    while (((uint64_t)(vocab + 1) << log2) > 0x100000000ull) --log2;
+    return log2;
+}
+
 void launch_sort_ids(const void* ids, uint32_t id_bytes, uint32_t n, uint32_t vocab, uint64_t* sorted,
-                     uint32_t* scratch, hipStream_t stream, void* fill, uint64_t fill_bytes) {
+                     uint32_t* scratch, hipStream_t stream, void* fill, uint64_t fill_bytes, uint64_t more_bytes) {
     SortParams p{};
     p.ids = ids, p.id_bytes = id_bytes, p.n = n, p.vocab = vocab, p.sorted = sorted;
-    p.block_log2 = 12;
-    while (((uint64_t)(vocab + 1) << p.block_log2) > 0x100000000ull) --p.block_log2;
+    p.block_log2 = sort_block_log2(vocab);
     const uint32_t block = 1u << p.block_log2;
     p.blocks = (n + block - 1) / block;
     p.limit = 4;
@@ -454,15 +467,18 @@ void launch_sort_ids(const void* ids, uint32_t id_bytes, uint32_t n, uint32_t vo
     if (p.blocks > 1) p.rows = scratch, p.tokens = scratch + n;
     uint32_t threads = p.limit / 4 < 64 ? 64 : p.limit / 4;
     uint64_t fillers = 0;
-    if (fill) {
+    if (fill_bytes) {
         threads = threads < 256 ? 256 : threads;
         p.fill = static_cast<u32x4*>(fill), p.fill_chunks = fill_bytes / 16;
         fillers = (p.fill_chunks + threads * kFillChunks - 1) / (threads * kFillChunks);
     }
     hipLaunchKernelGGL(sort_block_kernel, dim3((uint32_t)(p.blocks + fillers)), dim3(threads), 0, stream, p);
-    if (p.blocks > 1)
-        hipLaunchKernelGGL(sort_rank_kernel, dim3((n + kRankThreads - 1) / kRankThreads), dim3(kRankThreads), 0, stream,
-                           p);
+    if (p.blocks == 1) return;
+    p.rank_blocks = (n + kRankThreads - 1) / kRankThreads;
+    p.fill = static_cast<u32x4*>(fill) + fill_bytes / 16, p.fill_chunks = more_bytes / 16;
+    const uint64_t groups = (p.fill_chunks + kRankThreads - 1) / kRankThreads;
+    hipLaunchKernelGGL(sort_rank_kernel, dim3(p.rank_blocks + (uint32_t)(groups < kRankFillers ? groups : kRankFillers)),
+                       dim3(kRankThreads), 0, stream, p);
 }
 
 }  // namespace wc
@@ -528,15 +544,32 @@ extern "C" int wc_embed_grad_async(const uint16_t* dout, const void* ids, uint32
     p.n = (uint32_t)n, p.vocab = vocab, p.dim = dim, p.runs = l.runs, p.run_log2 = l.run_log2;
     p.bf16 = out_kind == WC_OUT_BF16, p.accumulate = accumulate != 0, p.scale = scale;
     p.col_blocks = (dim + kSumCols - 1) / kSumCols;
-    // Rows without tokens: where tokens are at most half as many as rows, the whole table is set to zero beside the
-    // sort, whose few workgroups leave the memory idle, and rows with tokens are written again; else the summing
-    // launch writes only the rows that have none.
-    // (A launch holds fewer than 2^32 threads of 16 bytes each, so tables from 32 GiB on are left to the second way.)
-    const uint64_t table_bytes = (uint64_t)vocab * dim * (p.bf16 ? 2 : 4);
-    const bool ahead = !p.accumulate && n && n <= vocab / 2 && table_bytes < (32ull << 30);
-    p.row_blocks = p.accumulate || ahead ? 0 : (vocab + kFillRows - 1) / kFillRows;
+    // Rows without tokens.  What the sort's few workgroups leave idle sets the table's first rows to zero, those with
+    // tokens too, which are written again: as many bytes as take about as long as the sorting launch, and the ranking
+    // one.  The others are written by the summing launch, whose reads leave some of the memory idle, row by row where
+    // there are no tokens; a single block of tokens has no ranking and a short summing launch, so there all rows are
+    // set beside the sort.  Measured, us (nothing ahead; 128 MiB beside the sort; that and 6 KiB per token beside the
+    // ranking, as here; the same, and the rest beside the sort):
+    //   32768 x 4096 fp32, 16384 tokens    148  140  131  143
+    //   131072 x 512 fp32, 16384 tokens     84   67   59   64
+    //   131072 x 4096 bf16, 65536 tokens   390  380  351  350
+    //   32000 x 4096 bf16, 32768 tokens    152  135  128  127
+    //   32000 x 4096 fp32, 2048 tokens     119  110    -  103
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    if (n) launch_sort_ids(ids, id_bytes, p.n, vocab, p.sorted, scratch, s, ahead ? dtable : nullptr, table_bytes);
+    uint64_t sort_bytes = 0, rank_bytes = 0;
+    if (n && !p.accumulate) {
+        const uint64_t row_bytes = (uint64_t)dim * (p.bf16 ? 2 : 4), table_bytes = vocab * row_bytes;
+        const bool one = n <= 1u << sort_block_log2(vocab);
+        const uint64_t first = one ? 32ull << 30 : 128ull << 20;   // (a launch holds fewer than 2^32 threads of 16 bytes)
+        const uint64_t second = one ? 0 : n * 6144;
+        const uint64_t rows = (first + second) / row_bytes;
+        p.filled = rows < vocab ? (uint32_t)rows : vocab;
+        const uint64_t bytes = p.filled * row_bytes;
+        sort_bytes = bytes < first ? bytes : first;
+        rank_bytes = bytes - sort_bytes;
+    }
+    p.row_blocks = p.accumulate ? 0 : (vocab - p.filled + kFillRows - 1) / kFillRows;
+    if (n) launch_sort_ids(ids, id_bytes, p.n, vocab, p.sorted, scratch, s, dtable, sort_bytes, rank_bytes);
     hipLaunchKernelGGL(embed_sum_kernel, dim3((p.runs + p.row_blocks) * p.col_blocks), dim3(kSumThreads), 0, s, p);
     if (p.runs > 1) {
         const uint32_t blocks = (dim + kJoinCols - 1) / kJoinCols, join_blocks = blocks < kJoinBlocks ? blocks : kJoinBlocks;

@@ -202,28 +202,40 @@ def test_side_stream_and_graph(wc):
         assert torch.equal(out, rows) and torch.equal(grad, want)
 
 
-def test_gradient_of_a_table_beyond_a_launch(wc):
-    """More 16-byte pieces than a launch has threads: every row is written all the same."""
-    vocab, dim, n = 1 << 22, 8256, 100
-    if torch.cuda.mem_get_info()[0] < (vocab * dim * 2) * 5 // 4:
-        pytest.skip("needs 87 GB of device memory")
+def _large_table(wc, vocab, dim, n, out):
+    if torch.cuda.mem_get_info()[0] < vocab * dim * (4 if out == "f32" else 2) * 5 // 4:
+        pytest.skip("needs more device memory")
     g = torch.Generator().manual_seed(8)
     ids = torch.randint(0, vocab, (n,), generator=g)
-    ids[0], ids[1] = 0, vocab - 1
-    dout = torch.randn(n, dim, generator=g).to(torch.bfloat16)
-    log(f"case: embed_grad {vocab}x{dim} bf16, {n} tokens")
-    table = torch.full((vocab, dim), 1.0, dtype=torch.bfloat16, device="cuda")
+    ids[0], ids[1], ids[2] = 0, vocab - 1, -1
+    dout = torch.randn(n, dim, generator=g).to(BF16)
+    log(f"case: embed_grad {vocab}x{dim} {out}, {n} tokens")
+    table = torch.full((vocab, dim), 1.0, dtype=torch.float32 if out == "f32" else BF16, device="cuda")
     work = torch.empty(wc.embed_grad_work_bytes(n, dim), dtype=torch.uint8, device="cuda")
-    wc.embed_grad_async(dout.cuda(), ids.cuda(), n, table, vocab, dim, work, work.numel(), out="bf16")
+    wc.embed_grad_async(dout.cuda(), ids.cuda(), n, table, vocab, dim, work, work.numel(), out=out)
     torch.cuda.synchronize()
-    rows, where = ids.unique(return_inverse=True)
-    want = torch.zeros(len(rows), dim, dtype=torch.float64).index_add_(0, where, dout.double())
-    mag = torch.zeros(len(rows), dim, dtype=torch.float64).index_add_(0, where, dout.double().abs())
+    rows, where = ids[ids >= 0].unique(return_inverse=True)
+    d = dout[ids >= 0].double()
+    want = torch.zeros(len(rows), dim, dtype=torch.float64).index_add_(0, where, d)
+    mag = torch.zeros(len(rows), dim, dtype=torch.float64).index_add_(0, where, d.abs())
     got = table[rows.cuda()]
-    # fewer than n sums within 2^-24 each, then one rounding to bf16
-    assert bool(((got.cpu().double() - want).abs() <= mag * n * 2.0 ** -24 + want.abs() * 2.0 ** -8).all())
+    # fewer than n sums within 2^-24 each, then one rounding to the output's type
+    tol = mag * n * 2.0 ** -24 + (want.abs() * 2.0 ** -8 if out == "bf16" else 0)
+    assert bool(((got.cpu().double() - want).abs() <= tol).all())
     table[rows.cuda()] = 0
     for part in table.view(torch.int16).split(1 << 17):
         assert int(part.count_nonzero()) == 0, "a row without tokens was not written"
-    del table, part
+
+
+def test_gradient_of_a_table_beyond_a_launch(wc):
+    """More 16-byte pieces than a launch has threads: every row is written all the same."""
+    _large_table(wc, 1 << 22, 8256, 100, "bf16")
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("vocab,dim,n,out", [(70000, 1024, 5000, "f32"), (70001, 1032, 4097, "bf16"),
+                                             (40000, 2056, 12000, "f32"), (300000, 392, 9000, "bf16"),
+                                             (9000, 8200, 6000, "f32"), (1 << 21, 64, 700, "f32")])
+def test_gradient_of_tables_written_by_several_launches(wc, vocab, dim, n, out):
+    """Tables whose rows are set beside the sort, beside the ranking and by the summing launch."""
+    _large_table(wc, vocab, dim, n, out)
