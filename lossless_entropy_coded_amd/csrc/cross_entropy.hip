@@ -583,18 +583,19 @@ __global__ __launch_bounds__(256) void ce_zero_kernel(uint16_t* dW, uint64_t chu
         reinterpret_cast<f32x4*>(dW)[i] = (f32x4)(0.0f);
 }
 
-constexpr uint32_t kRoundSlices = 8;                      // of the splits
-constexpr uint32_t kRoundCols = 256 / kRoundSlices * 4;   // columns per workgroup
+constexpr uint32_t kRoundCols = 256 * 4;   // columns per workgroup and slice of the splits
 
-// dh in bf16: the splits, in order within each of 8 slices of them, then the
-// slices in order, plus what d's target value lost to its rounding times
-// W[target].
+// dh in bf16: the splits (one, or a multiple of 8), in order within each of
+// kSlices of them, then the slices in order, plus what d's target value lost to
+// its rounding times W[target].  One split in 8 slices left most threads idle
+// (4096 x 4096: 81 us, 32 so).
+template <uint32_t kSlices>
 __global__ __launch_bounds__(256) void ce_dh_round_kernel(CeParams p) {
-    const uint32_t t = blockIdx.x, slice = threadIdx.x / (256 / kRoundSlices), lane = threadIdx.x % (256 / kRoundSlices);
-    const uint32_t at = blockIdx.y * kRoundCols + lane * 4;
+    constexpr uint32_t kLanes = 256 / kSlices;
+    const uint32_t t = blockIdx.x, slice = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+    const uint32_t at = blockIdx.y * (kRoundCols / kSlices) + lane * 4;
     __shared__ f32x4 shared[256];
-    const uint32_t per = (p.splits + kRoundSlices - 1) / kRoundSlices;
-    const uint32_t begin = slice * per, end = min(begin + per, p.splits);
+    const uint32_t per = p.splits / kSlices, begin = slice * per, end = begin + per;
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
     if (at < p.dim)
         for (uint32_t s = begin; s < end; ++s)
@@ -603,7 +604,7 @@ __global__ __launch_bounds__(256) void ce_dh_round_kernel(CeParams p) {
     __syncthreads();
     if (slice != 0 || at >= p.dim) return;
 #pragma unroll
-    for (uint32_t k = 1; k < kRoundSlices; ++k) v += shared[threadIdx.x + k * (256 / kRoundSlices)];
+    for (uint32_t k = 1; k < kSlices; ++k) v += shared[threadIdx.x + k * kLanes];
     const uint32_t own = target_of(p, t);
     if (own < p.vocab) {
         const u32x2 w = *reinterpret_cast<const u32x2*>(p.W + (uint64_t)own * p.dim + at);
@@ -840,7 +841,9 @@ extern "C" int wc_ce_grad_async(const uint16_t* h, const uint16_t* W, const void
             else run_dw<MidDw<true, true>>(p, s);
         }
     }
-    if (dh)
-        hipLaunchKernelGGL(ce_dh_round_kernel, dim3(p.tokens, cdiv(dim, kRoundCols)), dim3(256), 0, s, p);
+    if (dh && p.splits == 1)
+        hipLaunchKernelGGL(ce_dh_round_kernel<1>, dim3(p.tokens, cdiv(dim, kRoundCols)), dim3(256), 0, s, p);
+    else if (dh)
+        hipLaunchKernelGGL(ce_dh_round_kernel<kDies>, dim3(p.tokens, cdiv(dim, kRoundCols / kDies)), dim3(256), 0, s, p);
     return hipGetLastError() == hipSuccess ? WC_OK : WC_ERR_HIP;
 }
