@@ -11,15 +11,16 @@
 // of bf16, 4 of codes), the tokens of a workgroup as many as fill it.
 //
 // The gradient sums each row's tokens in a fixed order (token order within a
-// run), so it is the same bits on every run.  Tokens are sorted by row: blocks of 4096 by a bitonic network
-// whose keys (row, place in the block) fit 32 bits and stay in registers, four
-// per lane, with all but the ten widest of its 78 exchanges inside a wave (17
-// us; 38 with every exchange through LDS and 64-bit keys.  It is a chain of
-// dependent steps: exchanges by lane swaps in place of __shfl_xor, and one
-// v_med3 per key and step, take it to 16 to 19).  Then every token's place is
-// its place in its block plus, for each other block, the number of smaller
-// keys there: binary searches over the blocks' sorted rows, in LDS.  The sorted
-// tokens are cut into runs of up to kRun; a workgroup walks a run, eight rows
+// run), so it is the same bits on every run.  Tokens are sorted by row: up to
+// 8192 of them by counting for each the tokens before it, more in blocks of
+// 4096 by a bitonic network whose keys (row, place in the block) fit 32 bits
+// and stay in registers, four per lane, with all but the ten widest of its 78
+// exchanges inside a wave (17 us; 38 with every exchange through LDS and 64-bit
+// keys.  It is a chain of dependent steps: exchanges by lane swaps in place of
+// __shfl_xor, and one v_med3 per key and step, take it to 16 to 19).  Then
+// every token's place is its place in its block plus, for each other block, the
+// number of smaller keys there: binary searches over the blocks' sorted rows,
+// in LDS.  The sorted tokens are cut into runs of up to kRun; a workgroup walks a run, eight rows
 // of the gradient on their way at a time, and sums each row's tokens in fp32.
 // A row whose tokens lie in one run is finished there; one that crosses runs
 // leaves a partial sum per run, joined in a fixed order by the last kernel.
@@ -127,9 +128,8 @@ struct SortParams {
     const void* ids;
     uint32_t id_bytes, n, vocab;
     uint32_t block_log2;   // keys per block: with a block's index beside it, a row fits 32 bits
-    uint32_t limit;        // the network's size: a power of two, >= 4
     uint64_t* sorted;
-    uint32_t* rows;        // per block, in order (several blocks)
+    uint32_t* rows;        // per block, in order
     uint32_t* tokens;
     uint32_t blocks;
     uint32_t rank_blocks;  // workgroups that rank
@@ -141,16 +141,64 @@ struct SortParams {
 // 8: 168; kept: 172).
 constexpr uint32_t kFillChunks = 1;
 
+// The work of a filling workgroup, of the sorting launch's p.blocks and more.
+__device__ __forceinline__ void fill_zeros(const SortParams& p) {
+    uint64_t i = (uint64_t)(blockIdx.x - p.blocks) * blockDim.x * kFillChunks + threadIdx.x;
+#pragma unroll
+    for (uint32_t k = 0; k < kFillChunks; ++k, i += blockDim.x)
+        if (i < p.fill_chunks) __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, p.fill + i);
+}
+
+__device__ __forceinline__ uint32_t row_at(const SortParams& p, uint32_t t) {
+    const int64_t id = id_at(p.ids, p.id_bytes, t);
+    return id >= 0 && id < (int64_t)p.vocab ? (uint32_t)id : p.vocab;
+}
+
+constexpr uint32_t kDirectTokens = 8192;
+constexpr uint32_t kDirectThreads = 512;   // at most
+
+// Few tokens: a token's place is the number of smaller keys (row, token), so
+// each lane counts those of one token, a workgroup 64 tokens, each of its waves
+// a part of the keys: 64 keys come into the lanes of a wave and go round as
+// scalars, 3 operations per key and 64 tokens.  Against sorting and ranking, the
+// whole gradient, us (5000 x 256 bf16): 512 tokens 13.5 and 15.7, 2048 17.1 and
+// 20.1, 4096 20.4 and 26.4, 8192 29.6 and 35.4, 12000 37.2 and 38.0; 16384
+// (32768 x 512) 49.9 and 45.1.
+__global__ __launch_bounds__(kDirectThreads) void sort_direct_kernel(SortParams p) {
+    if (blockIdx.x >= p.blocks) return fill_zeros(p);
+    __shared__ uint32_t shared[kDirectThreads / 64][64];
+    const uint32_t waves = blockDim.x >> 6;
+    const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t tile = blockIdx.x * 64, token = tile + lane;
+    const uint32_t row = row_at(p, min(token, p.n - 1));
+    const uint32_t per = ((p.n + 63) / 64 + waves - 1) / waves * 64;
+    const uint32_t begin = min(wave * per, p.n), end = min(begin + per, p.n);
+    uint32_t place = 0;
+    uint32_t next = begin + lane < end ? row_at(p, begin + lane) : ~0u;   // (smaller than no key)
+    for (uint32_t from = begin; from < end; from += 64) {
+        const uint32_t keys = next;
+        next = from + 64 + lane < end ? row_at(p, from + 64 + lane) : ~0u;
+        if (from != tile) {
+            const uint32_t less = row + (from < tile);   // earlier tokens of the same row come before
+#pragma unroll
+            for (uint32_t k = 0; k < 64; ++k) place += (uint32_t)__builtin_amdgcn_readlane((int)keys, k) < less;
+        } else {
+#pragma unroll
+            for (uint32_t k = 0; k < 64; ++k)
+                place += (uint32_t)__builtin_amdgcn_readlane((int)keys, k) < row + (k < lane);
+        }
+    }
+    shared[wave][lane] = place;
+    __syncthreads();
+    if (wave != 0 || token >= p.n) return;
+    for (uint32_t w = 1; w < waves; ++w) place += shared[w][lane];
+    p.sorted[place] = (uint64_t)row << 32 | token;
+}
+
 // The keys of a block in order: four per thread, keys 4 t .. 4 t + 3.
 __global__ __launch_bounds__(kSortThreads) void sort_block_kernel(SortParams p) {
     __shared__ u32x4 shared[kSortThreads];
-    if (blockIdx.x >= p.blocks) {
-        uint64_t i = (uint64_t)(blockIdx.x - p.blocks) * blockDim.x * kFillChunks + threadIdx.x;
-#pragma unroll
-        for (uint32_t k = 0; k < kFillChunks; ++k, i += blockDim.x)
-            if (i < p.fill_chunks) __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, p.fill + i);
-        return;
-    }
+    if (blockIdx.x >= p.blocks) return fill_zeros(p);
     const uint32_t tid = threadIdx.x, base = blockIdx.x << p.block_log2;
     const uint32_t count = min(p.n - base, 1u << p.block_log2);
     u32x4 key;
@@ -158,10 +206,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_block_kernel(SortParams p) 
     for (uint32_t e = 0; e < 4; ++e) {
         const uint32_t i = tid * 4 + e;
         uint32_t k = ~0u;
-        if (i < count) {
-            const int64_t id = id_at(p.ids, p.id_bytes, base + i);
-            k = (id >= 0 && id < (int64_t)p.vocab ? (uint32_t)id : p.vocab) << p.block_log2 | i;
-        }
+        if (i < count) k = row_at(p, base + i) << p.block_log2 | i;
         key[e] = k;
     }
     const auto order = [&](uint32_t a, uint32_t b, bool up) {   // key[a] before key[b], or after it
@@ -171,7 +216,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_block_kernel(SortParams p) 
     };
     order(0, 1, true);
     order(2, 3, false);
-    for (uint32_t size = 4; size <= p.limit; size <<= 1) {
+    for (uint32_t size = 4; size <= 1u << p.block_log2; size <<= 1) {
         const bool up = (tid * 4 & size) == 0;
         for (uint32_t stride = size >> 1; stride >= 4; stride >>= 1) {
             const uint32_t far = stride / 4;
@@ -199,12 +244,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_block_kernel(SortParams p) 
         const uint32_t i = tid * 4 + e;
         if (i >= count) continue;
         const uint32_t row = key[e] >> p.block_log2, token = base + (key[e] & ((1u << p.block_log2) - 1));
-        if (p.rows) {
-            p.rows[base + i] = row;
-            p.tokens[base + i] = token;
-        } else {
-            p.sorted[i] = (uint64_t)row << 32 | token;
-        }
+        p.rows[base + i] = row;
+        p.tokens[base + i] = token;
     }
 }
 
@@ -449,33 +490,28 @@ int launch_lookup(LookupParams& p, bool q4, hipStream_t s) {
 
 }  // namespace
 
-uint32_t sort_block_log2(uint32_t vocab) {
-    uint32_t log2 = 12;
-    while (((uint64_t)(vocab + 1) << log2) > 0x100000000ull) --log2;
-    return log2;
-}
-
 void launch_sort_ids(const void* ids, uint32_t id_bytes, uint32_t n, uint32_t vocab, uint64_t* sorted,
                      uint32_t* scratch, hipStream_t stream, void* fill, uint64_t fill_bytes, uint64_t more_bytes) {
     SortParams p{};
     p.ids = ids, p.id_bytes = id_bytes, p.n = n, p.vocab = vocab, p.sorted = sorted;
-    p.block_log2 = sort_block_log2(vocab);
+    p.fill = static_cast<u32x4*>(fill), p.fill_chunks = fill_bytes / 16;
+    const auto blocks = [&](uint32_t threads) {   // of the first launch, those that fill among them
+        return dim3((uint32_t)(p.blocks + (p.fill_chunks + threads * kFillChunks - 1) / (threads * kFillChunks)));
+    };
+    if (n <= kDirectTokens) {
+        p.blocks = (n + 63) / 64;
+        const uint32_t threads = n <= 1024 ? kDirectThreads / 2 : kDirectThreads;   // small workgroups fill faster
+        hipLaunchKernelGGL(sort_direct_kernel, blocks(threads), dim3(threads), 0, stream, p);
+        return;
+    }
+    p.block_log2 = 12;
+    while (((uint64_t)(vocab + 1) << p.block_log2) > 0x100000000ull) --p.block_log2;
     const uint32_t block = 1u << p.block_log2;
     p.blocks = (n + block - 1) / block;
-    p.limit = 4;
-    while (p.limit < n && p.limit < block) p.limit <<= 1;
-    if (p.blocks > 1) p.rows = scratch, p.tokens = scratch + n;
-    uint32_t threads = p.limit / 4 < 64 ? 64 : p.limit / 4;
-    uint64_t fillers = 0;
-    if (fill_bytes) {
-        threads = threads < 256 ? 256 : threads;
-        p.fill = static_cast<u32x4*>(fill), p.fill_chunks = fill_bytes / 16;
-        fillers = (p.fill_chunks + threads * kFillChunks - 1) / (threads * kFillChunks);
-    }
-    hipLaunchKernelGGL(sort_block_kernel, dim3((uint32_t)(p.blocks + fillers)), dim3(threads), 0, stream, p);
-    if (p.blocks == 1) return;
+    p.rows = scratch, p.tokens = scratch + n;
+    hipLaunchKernelGGL(sort_block_kernel, blocks(block / 4), dim3(block / 4), 0, stream, p);
     p.rank_blocks = (n + kRankThreads - 1) / kRankThreads;
-    p.fill = static_cast<u32x4*>(fill) + fill_bytes / 16, p.fill_chunks = more_bytes / 16;
+    p.fill += p.fill_chunks, p.fill_chunks = more_bytes / 16;
     const uint64_t groups = (p.fill_chunks + kRankThreads - 1) / kRankThreads;
     hipLaunchKernelGGL(sort_rank_kernel, dim3(p.rank_blocks + (uint32_t)(groups < kRankFillers ? groups : kRankFillers)),
                        dim3(kRankThreads), 0, stream, p);
@@ -547,19 +583,20 @@ extern "C" int wc_embed_grad_async(const uint16_t* dout, const void* ids, uint32
     // Rows without tokens.  What the sort's few workgroups leave idle sets the table's first rows to zero, those with
     // tokens too, which are written again: as many bytes as take about as long as the sorting launch, and the ranking
     // one.  The others are written by the summing launch, whose reads leave some of the memory idle, row by row where
-    // there are no tokens; a single block of tokens has no ranking and a short summing launch, so there all rows are
-    // set beside the sort.  Measured, us (nothing ahead; 128 MiB beside the sort; that and 6 KiB per token beside the
+    // there are no tokens; few tokens have no ranking and a short summing launch, so there all rows are set beside the
+    // sort.  Measured, us (nothing ahead; 128 MiB beside the sort; that and 6 KiB per token beside the
     // ranking, as here; the same, and the rest beside the sort):
     //   32768 x 4096 fp32, 16384 tokens    148  140  131  143
     //   131072 x 512 fp32, 16384 tokens     84   67   59   64
     //   131072 x 4096 bf16, 65536 tokens   390  380  351  350
     //   32000 x 4096 bf16, 32768 tokens    152  135  128  127
-    //   32000 x 4096 fp32, 2048 tokens     119  110    -  103
+    //   32768 x 4096 fp32, 8192 tokens       -  121    -  115
+    //   32000 x 4096 fp32, 2048 tokens     119  110    -  101
     const hipStream_t s = static_cast<hipStream_t>(stream);
     uint64_t sort_bytes = 0, rank_bytes = 0;
     if (n && !p.accumulate) {
         const uint64_t row_bytes = (uint64_t)dim * (p.bf16 ? 2 : 4), table_bytes = vocab * row_bytes;
-        const bool one = n <= 1u << sort_block_log2(vocab);
+        const bool one = n <= kDirectTokens;
         const uint64_t first = one ? 32ull << 30 : 128ull << 20;   // (a launch holds fewer than 2^32 threads of 16 bytes)
         const uint64_t second = one ? 0 : n * 6144;
         const uint64_t rows = (first + second) / row_bytes;

@@ -191,14 +191,11 @@ hipError_t launch_decode_lanes(const DecodeParams& p, uint32_t decode_bits, uint
 
 // Tokens sorted by id, then by token: sorted[i] = row << 32 | token, row = vocab
 // for ids (id_bytes 4 or 8 each) outside [0, vocab).  scratch: 2 n words.  1 <=
-// n <= 2^20, vocab <= 2^22.  One launch up to 4096 tokens (for vocabularies
-// below 2^20), else two.  The first one also sets fill_bytes at `fill` to zero,
-// the second one, if there is one, more_bytes behind them (multiples of 16).
+// n <= 2^20, vocab <= 2^22.  One launch up to 8192 tokens, else two.  The first
+// one also sets fill_bytes at `fill` to zero, the second one more_bytes behind
+// them (multiples of 16; 0 if there is one launch).
 void launch_sort_ids(const void* ids, uint32_t id_bytes, uint32_t n, uint32_t vocab, uint64_t* sorted,
                      uint32_t* scratch, hipStream_t stream, void* fill, uint64_t fill_bytes, uint64_t more_bytes);
-// Tokens that one launch sorts: 2^log2.
-uint32_t sort_block_log2(uint32_t vocab);
-
 // The HIP device a plan was made for.
 int plan_device(const wc_plan_s* plan);
 

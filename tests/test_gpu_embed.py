@@ -235,7 +235,11 @@ def test_gradient_of_a_table_beyond_a_launch(wc):
 
 @pytest.mark.parametrize("vocab,dim,n,out", [(70000, 1024, 5000, "f32"), (70001, 1032, 4097, "bf16"),
                                              (40000, 2056, 12000, "f32"), (300000, 392, 9000, "bf16"),
-                                             (9000, 8200, 6000, "f32"), (1 << 21, 64, 700, "f32")])
+                                             (9000, 8200, 6000, "f32"), (1 << 21, 64, 700, "f32"),
+                                             (50, 72, 1024, "f32"), (50, 72, 1025, "f32"), (1, 8, 8192, "f32"),
+                                             (7000, 64, 8191, "bf16"), (7000, 64, 8193, "bf16"), (1, 8, 8193, "f32"),
+                                             (1 << 22, 8, 9001, "f32"), (1 << 20, 64, 12345, "bf16")])
 def test_gradient_of_tables_written_by_several_launches(wc, vocab, dim, n, out):
-    """Tables whose rows are set beside the sort, beside the ranking and by the summing launch."""
+    """Tables whose rows are set beside the sort, beside the ranking and by the summing launch; sizes where the way of
+    sorting changes."""
     _large_table(wc, vocab, dim, n, out)
