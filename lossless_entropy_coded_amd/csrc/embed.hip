@@ -160,7 +160,8 @@ constexpr uint32_t kDirectThreads = 512;   // at most
 // Few tokens: a token's place is the number of smaller keys (row, token), so
 // each lane counts those of one token, a workgroup 64 tokens, each of its waves
 // a part of the keys: 64 keys come into the lanes of a wave and go round as
-// scalars, 3 operations per key and 64 tokens.  Against sorting and ranking, the
+// scalars, 3 operations per key and 64 tokens, which bound it: 4.2 us at 512
+// tokens, 6.8 at 2048, 11 at 4096, 18 at 8192.  Against sorting and ranking, the
 // whole gradient, us (5000 x 256 bf16): 512 tokens 13.5 and 15.7, 2048 17.1 and
 // 20.1, 4096 20.4 and 26.4, 8192 29.6 and 35.4, 12000 37.2 and 38.0; 16384
 // (32768 x 512) 49.9 and 45.1.
