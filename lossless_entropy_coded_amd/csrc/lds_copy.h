@@ -28,9 +28,12 @@ __device__ __forceinline__ u32x4 buffer_words(const void* p, uint32_t bytes) {
 // LDS is read.  In assembly because the compiler, for the builtin, waits for
 // every such copy before each transposing LDS read; but then it does not count
 // the copy when it waits for other loads, so a kernel keeps no loads into
-// registers on their way beside it.
+// registers on their way beside it.  Nor does it add the wait state that a
+// memory instruction with LDS needs behind a write of m0: the s_nop is that one
+// (without it the copy may go to the place of the copy before).
 __device__ __forceinline__ void copy_to_lds(uint32_t to, const u32x4& rsrc, uint32_t offset) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(offset), "s"(rsrc)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(offset),
+                 "s"(rsrc)
                  : "memory", "m0");
 }
 
