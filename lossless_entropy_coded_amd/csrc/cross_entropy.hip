@@ -15,12 +15,14 @@
 // token's tiles in tile order.  The gradient computes z again, a piece of the
 // vocabulary at a time, and keeps that piece's d in bf16 (the matrix cores'
 // input type: a relative rounding of at most 2^-8 per value, as dh and dW
-// themselves are rounded) for the two products that read it.  The rounding of
-// the target's own value, by far the largest of a row, is kept per token in
-// fp32 and its product with W[target] is added to dh.  A row of dW sums few
-// tokens where there are few, and their roundings do not average out: up to
-// 128 tokens, what the values of d lose is kept as a second bf16 matrix and
-// multiplied too (with more, it would cost a product as large as dW's).
+// themselves are rounded) for the two products that read it.  What the target's
+// own value, as a rule by far the largest of a token's d, loses to that is kept
+// per token in fp32, and goes into both: its product with W[target] is added to
+// dh, its product with h[t] to dW[target], whose row often has that one token
+// only.  Up to 128 tokens, what all values of d lose is kept as a second bf16
+// matrix and multiplied for dW (with more, it would cost a product as large as
+// dW's): then a row of dW has so few tokens that the roundings of the others'
+// values do not average out either.
 //
 // The three products run on one tile routine, out[n][m] = sum_k A(m, k) B(n, k),
 // m being the contiguous index of the output: a 32 x 32 accumulator block holds
@@ -167,10 +169,11 @@ __device__ __forceinline__ bf16x8 fragment(const uint16_t* lds, uint32_t x, uint
 // 4 waves of 128 x 128 each, which read a third less LDS, reach 885: a lone
 // wave per SIMD cannot cover its own LDS reads.
 template <bool kAx, bool kBx, uint32_t kBm_, uint32_t kBn_, uint32_t kWavesM_, uint32_t kWavesN_, uint32_t kStages_,
-          uint32_t kBk>
+          uint32_t kBk_>
 struct Tile {
-    static_assert(kUnit % kBk == 0, "splits are whole stages");
     static constexpr uint32_t kBm = kBm_, kBn = kBn_, kWavesM = kWavesM_, kWavesN = kWavesN_, kStages = kStages_;
+    static constexpr uint32_t kBk = kBk_;
+    static_assert(kUnit % kBk == 0, "splits are whole stages");
     static constexpr uint32_t kThreads = 64 * kWavesM * kWavesN;
     static constexpr uint32_t kMi = kBm / kWavesM / 32, kNi = kBn / kWavesN / 32;
     static constexpr uint32_t kStageElems = (kBm + kBn) * kBk;
@@ -354,7 +357,7 @@ struct CeParams {
     uint16_t* dW;
     // workspace
     float2* part;              // loss: per vocabulary tile and token, {maximum, sum of exp(z - maximum)}
-    float* own;                // loss: the target's logit; gradient: the rounding of the target's d
+    float* own;                // loss: the target's logit; gradient: what the target's d loses to rounding
     uint16_t* d;               // gradient: d of one piece, [token][ldd]
     uint16_t* h_own;           // gradient: h of the tokens with a loss, zeros for others
     float* dh_part;            // gradient: dh in fp32, [split][token][dim]
@@ -554,9 +557,116 @@ __global__ __launch_bounds__(T::kThreads) void ce_dh_kernel(CeParams p) {
     }
 }
 
-// dW of the piece = d^T h.
+// acc += what the values of the targets lost in d to rounding, times h: of the
+// piece's entries n0 .. n0 + kBn - 1, a product as dW's own whose k runs over
+// the tokens with a target among them, in token order.  There are few (every
+// token has one target, so all tiles of n together take each once), and they are
+// looked for in the targets of all tokens, kScan per thread at a time: no list
+// has to be made by a launch before.  The lost value is rounded to bf16 like d,
+// which leaves 2^-16 of a value of d.  It takes 8 us of 270 (loss and gradients)
+// at 515 tokens x 32003 x 1160, 0.17 ms of 14.0 at 4096 x 131072 x 4096.  LDS is
+// free when it begins and when it ends.
 template <class T>
-__global__ __launch_bounds__(T::kThreads) void ce_dw_kernel(CeParams p) {
+__device__ __forceinline__ void add_lost(uint16_t* lds, const CeParams& p, uint32_t m0, uint32_t n0,
+                                         f32x16 (&acc)[T::kMi][T::kNi]) {
+    constexpr uint32_t kScan = 8, kWaves = T::kThreads / 64, kCounts = kScan * kWaves;
+    constexpr uint32_t kChunksA = T::kBm / 8, kChunksB = T::kBn / 8;
+    static_assert(kCounts <= 64, "a wave's lanes hold all counts");
+    static_assert(T::kStageElems * 2 + T::kThreads * kScan * 8 + kCounts * 4 <= T::kLdsElems * 2,
+                  "the list fits behind one stage");
+    uint16_t* const sa = lds;
+    uint16_t* const sb = lds + T::kBm * T::kBk;
+    uint2* const list = reinterpret_cast<uint2*>(lds + T::kStageElems);   // {token, n | lost value << 16}
+    uint32_t* const counts = reinterpret_cast<uint32_t*>(list + T::kThreads * kScan);
+    const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t wm = wave % T::kWavesM * (T::kBm / T::kWavesM), wn = wave / T::kWavesM * (T::kBn / T::kWavesN);
+    const uint32_t from = p.piece_begin + n0, width = min(p.piece_end - from, T::kBn);
+    const uint32_t* const targets = static_cast<const uint32_t*>(p.targets);
+    const uint32_t words = p.target_bytes / 4;
+    uint32_t t0 = 0;
+    do {   // (a loop that might not be entered would keep the tile's sums in registers twice)
+        uint32_t at[kScan], high[kScan];   // low and high words of targets
+        float lost[kScan];                 // (of tokens with a target in the piece; all loads are on their way at once)
+#pragma unroll
+        for (uint32_t k = 0; k < kScan; ++k) {
+            const uint32_t t = min(t0 + k * T::kThreads + threadIdx.x, p.tokens - 1);
+            at[k] = targets[(uint64_t)t * words];
+            high[k] = targets[(uint64_t)t * words + words - 1];
+            lost[k] = p.own[t];
+        }
+        uint64_t has[kScan];
+#pragma unroll
+        for (uint32_t k = 0; k < kScan; ++k) {
+            const bool fits = t0 + k * T::kThreads + threadIdx.x < p.tokens && (words == 1 || high[k] == 0);
+            at[k] = fits && at[k] - from < width ? at[k] - from : ~0u;   // n, if the tile has it
+            has[k] = __ballot(at[k] != ~0u);
+            if (lane == 0) counts[k * kWaves + wave] = (uint32_t)__popcll(has[k]);
+        }
+        __syncthreads();
+        uint32_t before = lane < kCounts ? counts[lane] : 0;   // of this and the counts before it
+#pragma unroll
+        for (uint32_t step = 1; step < 64; step *= 2) {
+            const uint32_t other = (uint32_t)__shfl_up((int)before, step);
+            if (lane >= step) before += other;
+        }
+        const uint32_t total = (uint32_t)__builtin_amdgcn_readlane((int)before, 63);
+#pragma unroll
+        for (uint32_t k = 0; k < kScan; ++k) {
+            const uint32_t c = k * kWaves + wave;
+            const uint32_t first = c ? (uint32_t)__builtin_amdgcn_readlane((int)before, c - 1) : 0;
+            if (at[k] == ~0u) continue;
+            const uint32_t t = t0 + k * T::kThreads + threadIdx.x;
+            list[first + (uint32_t)__popcll(has[k] & ((1ull << lane) - 1))] =
+                make_uint2(t, at[k] | (uint32_t)f32_bf16(lost[k]) << 16);
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (uint32_t k0 = 0; k0 < total; k0 += T::kBk) {
+            for (uint32_t i = threadIdx.x; i < T::kBk * kChunksA; i += T::kThreads) {
+                const uint32_t row = i / kChunksA, c = i % kChunksA;
+                u32x4 v = {0, 0, 0, 0};
+                if (k0 + row < total && m0 + c * 8 < p.dim)
+                    v = *reinterpret_cast<const u32x4*>(p.h + (uint64_t)list[k0 + row].x * p.dim + m0 + c * 8);
+                *reinterpret_cast<u32x4*>(sa + row * T::kBm + (c ^ ((row & 3u) << 2)) * 8) = v;
+            }
+#pragma unroll 1
+            for (uint32_t i = threadIdx.x; i < T::kBk * kChunksB; i += T::kThreads) {
+                const uint32_t row = i / kChunksB, c = i % kChunksB;
+                u32x4 v = {0, 0, 0, 0};
+                const uint32_t entry = k0 + row < total ? list[k0 + row].y : 0xFFFFu;
+                if ((entry & 0xFFFFu) / 8 == c) {
+                    const uint32_t word = (entry >> 16) << (entry & 1u) * 16;
+#pragma unroll
+                    for (uint32_t e = 0; e < 4; ++e) v[e] = (entry & 7u) / 2 == e ? word : 0;
+                }
+                *reinterpret_cast<u32x4*>(sb + row * T::kBn + (c ^ ((row & 3u) << 2)) * 8) = v;
+            }
+            __syncthreads();
+#pragma unroll
+            for (uint32_t kk = 0; kk < T::kBk; kk += 16) {
+                bf16x8 a[T::kMi], b[T::kNi];
+#pragma unroll
+                for (uint32_t i = 0; i < T::kMi; ++i) a[i] = fragment<true, T::kBm, T::kBk>(sa, wm + i * 32, kk);
+#pragma unroll
+                for (uint32_t j = 0; j < T::kNi; ++j) b[j] = fragment<true, T::kBn, T::kBk>(sb, wn + j * 32, kk);
+#pragma unroll
+                for (uint32_t i = 0; i < T::kMi; ++i)
+#pragma unroll
+                    for (uint32_t j = 0; j < T::kNi; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            __syncthreads();
+        }
+        t0 += T::kThreads * kScan;
+    } while (t0 < p.tokens);
+}
+
+// dW of the piece = d^T h.  (Three workgroups of mid tiles per CU: with more
+// registers, and so two, loss and gradients at 515 tokens x 32003 x 1160 take 297
+// us in place of 279.)
+template <class T>
+__global__ __launch_bounds__(T::kThreads, T::kAlternate ? 2 : 3) void ce_dw_kernel(CeParams p) {
     __shared__ __align__(16) uint16_t lds[T::kLdsElems];
     const uint32_t len = p.piece_end - p.piece_begin;
     uint32_t mt, nt;
@@ -566,9 +676,13 @@ __global__ __launch_bounds__(T::kThreads) void ce_dw_kernel(CeParams p) {
     f32x16 acc[T::kMi][T::kNi];
     T::clear(acc);
     T::product(lds, A, B, m0, n0, 0, p.tokens, acc);
-    if (p.rests) {
+    if constexpr (T::kAlternate) {   // few tokens never take big tiles
+        add_lost<T>(lds, p, m0, n0, acc);
+    } else if (p.rests) {
         const Operand R{p.d + (uint64_t)p.tokens * p.ldd, p.ldd, p.ldd, p.tokens};
         T::product(lds, A, R, m0, n0, 0, p.tokens, acc);
+    } else {
+        add_lost<T>(lds, p, m0, n0, acc);
     }
     store_rows<T>(lds, p.dW + (uint64_t)(p.piece_begin + n0) * p.dim + m0, p.dim, p.dim - m0, len - n0,
                   [&](uint32_t i, uint32_t j, uint32_t r) {
