@@ -515,6 +515,14 @@ def _sizes(call: str, **sizes) -> None:
             raise WCError(WC_ERR_INVALID_ARG, call, f"{what} is {v}")
 
 
+def _workspace(work_dev, work_bytes: int, device, call: str):
+    """The pointer and the size of a workspace; a size that C's 64 bits do not hold would arrive there as another."""
+    size = int(work_bytes)
+    if not 0 <= size < 1 << 64:
+        raise WCError(WC_ERR_INVALID_ARG, call, f"work_bytes is {size}")
+    return _bytes_ok(work_dev, size, device, "work", call), size
+
+
 _INDEX_BYTES = {}   # dtype -> bytes, of the id types seen
 
 
@@ -618,9 +626,9 @@ def embed_grad_async(dout_dev, ids_dev, n: int, dtable_dev, vocab: int, dim: int
     dout = _bytes_ok(dout_dev, 2 * n * dim, dev, "dout", call)
     ids = _bytes_ok(ids_dev, width * n, dev, "ids", call)
     dtable = _bytes_ok(dtable_dev, (4 if out == "f32" else 2) * vocab * dim, dev, "dtable", call)
-    work = _bytes_ok(work_dev, int(work_bytes), dev, "work", call)
+    work, work_bytes = _workspace(work_dev, work_bytes, dev, call)
     _check(_lib.wc_embed_grad_async(dout, ids, width, n, scale, dtable, OUT_KINDS[out], vocab, dim, bool(accumulate),
-                                    work, int(work_bytes), _stream_handle(stream)), call)
+                                    work, work_bytes, _stream_handle(stream)), call)
 
 
 def ce_work_bytes(tokens: int, vocab: int, dim: int, grad: bool = True) -> int:
@@ -644,8 +652,8 @@ def ce_loss_async(h_dev, W_dev, targets_dev, tokens: int, vocab: int, dim: int, 
     targets = _bytes_ok(targets_dev, width * tokens, dev, "targets", call)
     loss = _bytes_ok(loss_dev, 4 * tokens, dev, "loss", call)
     lse = _bytes_ok(lse_dev, 4 * tokens, dev, "lse", call)
-    work = _bytes_ok(work_dev, int(work_bytes), dev, "work", call)
-    _check(_lib.wc_ce_loss_async(h, W, targets, width, tokens, vocab, dim, loss, lse, work, int(work_bytes),
+    work, work_bytes = _workspace(work_dev, work_bytes, dev, call)
+    _check(_lib.wc_ce_loss_async(h, W, targets, width, tokens, vocab, dim, loss, lse, work, work_bytes,
                                  _stream_handle(stream)), call)
 
 
@@ -664,8 +672,8 @@ def ce_grad_async(h_dev, W_dev, targets_dev, tokens: int, vocab: int, dim: int, 
     dloss = _bytes_ok(dloss_dev, 4 * tokens, dev, "dloss", call)
     dh = _bytes_ok(dh_dev, 2 * tokens * dim, dev, "dh", call) if dh_dev is not None else 0
     dW = _bytes_ok(dW_dev, 2 * vocab * dim, dev, "dW", call) if dW_dev is not None else 0
-    work = _bytes_ok(work_dev, int(work_bytes), dev, "work", call)
-    _check(_lib.wc_ce_grad_async(h, W, targets, width, tokens, vocab, dim, lse, dloss, dh, dW, work, int(work_bytes),
+    work, work_bytes = _workspace(work_dev, work_bytes, dev, call)
+    _check(_lib.wc_ce_grad_async(h, W, targets, width, tokens, vocab, dim, lse, dloss, dh, dW, work, work_bytes,
                                  _stream_handle(stream)), call)
 
 
