@@ -24,8 +24,12 @@
 //     significant bits), and off by less than 2^-39 of it below; an infinity
 //     or NaN stays one;
 //   - the products are exact in fp32 and sums are held in fp32: a group's sum
-//     times its scale is added to the slab's, the slab's times its power of
-//     two to the row's.
+//     times its scale is added to the slab's, the slab's to the row's.  The
+//     slab's power of two goes back in before the scale where it is below one,
+//     after it where it is above: so nothing on the way leaves fp32's range that
+//     the plain products would not (a sum is up to 2^31 before it, scales are
+//     any finite bf16).  Neither loses bits: sums below 2^-126 are multiples of
+//     x's smallest steps, which fp32 holds.
 // (Subtracting zero * sum(x) from sum(code x) instead would lose small products
 // next to a large x that its zero point cancels.  bf16 in place of f16, code
 // by code through v_cvt_off_f32_i4, needs no scaling of x but 1.75 operations
@@ -329,6 +333,11 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
                     words[k][i] =
                         spread_rows(exchanged(kGiven ? l.scale[k][i] << 16 | l.zero[k][i] : l.scale[k][i] << 16));
         }
+        const u32x4 unit = *reinterpret_cast<const u32x4*>(units + q * 4);   // of vectors 4 q .., the bits
+        f32x4 below, above;   // the part of it below one, and that above
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e)
+            below[e] = __uint_as_float(min(unit[e], 0x3F800000u)), above[e] = __uint_as_float(max(unit[e], 0x3F800000u));
         f32x4 sum[kTiles];
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) sum[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -361,15 +370,14 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemv_q4_kernel(Q4Params p) {
                     for (uint32_t j = b * kBlock; j < (b + 1) * kBlock; ++j)
                         D = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[j], weights(w[j], by1, by16, consts), D, 0, 0, 0);
 #pragma unroll
-                    for (uint32_t e = 0; e < 4; ++e) sum[i][e] = __builtin_fmaf(D[e], scale, sum[i][e]);
+                    for (uint32_t e = 0; e < 4; ++e) sum[i][e] = __builtin_fmaf(D[e] * below[e], scale, sum[i][e]);
                 }
             }
         }
-        const f32x4 unit = *reinterpret_cast<const f32x4*>(units + q * 4);   // of vectors 4 q ..
 #pragma unroll
         for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-            for (uint32_t e = 0; e < 4; ++e) acc[i][e] = __builtin_fmaf(sum[i][e], unit[e], acc[i][e]);
+            for (uint32_t e = 0; e < 4; ++e) acc[i][e] = __builtin_fmaf(sum[i][e], above[e], acc[i][e]);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
     };
