@@ -74,3 +74,50 @@ def test_scales_of_different_size(wc, vecs):
         assert bool(((y - ref).abs() <= tol)[fits].all()), size
         gone = (ref.abs() > 2.0 ** 129)
         assert not bool(torch.isfinite(y[gone]).any()), size
+
+
+# From 8192 rows on, 1 and 2 vectors take 4 waves per workgroup (8 below), and 3 and more 32 rows (16 below), of 8 waves
+# from 5 on (they are rounded up to 4, 8 or 16 vectors).  The last workgroup has 1, 17, 31 or all of its rows.
+TALL = [(8192, 128, 128, False), (8193, 1152, 32, True), (8209, 1152, 32, False), (8193, 1000, 64, True),
+        (8209, 1160, 96, False), (8209, 1024, 64, True), (8223, 512, 65536, True), (8193, 2048, 128, False),
+        (8192, 104, 32, True), (8209, 640, 128, True), (8193, 576, 96, True), (8209, 512, 64, False)]
+
+
+@pytest.mark.parametrize("rows,cols,group,zeros", TALL)
+def test_tall_matrices(wc, rows, cols, group, zeros):
+    codes, scales, z, w = q4_case(rows, cols, group, zeros, rows + cols)
+    matrix = wc.Q4Matrix(codes, scales, rows, cols, group, zeros=z)
+    for vecs in (1, 2, 3, 4, 5, 8, 9, 16):
+        x = torch.randn(vecs, cols, generator=torch.Generator().manual_seed(cols + vecs)).to(BF16)
+        log(f"case: gemv_q4 {rows}x{cols} group {group} zeros {zeros} vecs {vecs}")
+        y = _run(wc, matrix, x.cuda())
+        assert within(y, x.double() @ w.t(), q4_tolerance(w, x.double())), vecs
+        again = _run(wc, matrix, x.cuda())
+        assert torch.equal(y.view(torch.int32), again.view(torch.int32)), "two runs differ"
+        if group == 32 and cols % 128 == 0:     # scales and zero points off their alignment: another kernel, the same bits
+            groups = cols // group
+            shifted = torch.empty(rows * groups + 1, dtype=BF16, device="cuda")[1:].reshape(rows, groups)
+            shifted.copy_(scales)
+            other = wc.Q4Matrix(codes, shifted, rows, cols, group, zeros=z)
+            assert torch.equal(_run(wc, other, x.cuda()).view(torch.int32), y.view(torch.int32)), vecs
+
+
+@pytest.mark.parametrize("vecs", [1, 3, 8, 16])
+def test_tall_matrices_with_values_that_are_not_finite(wc, vecs):
+    """An infinity in one vector and a NaN in another reach no other vector, and no row that has a zero weight there
+    gets anything but NaN for it."""
+    rows, cols, group = 8209, 384, 64
+    codes, scales, z, w = q4_case(rows, cols, group, True, 1)
+    matrix = wc.Q4Matrix(codes, scales, rows, cols, group, zeros=z)
+    x = torch.randn(vecs, cols, generator=torch.Generator().manual_seed(9)).to(BF16)
+    x[0, 70] = float("inf")
+    if vecs > 2:
+        x[2, 383] = float("nan")
+    log(f"case: gemv_q4 {rows}x{cols} vecs {vecs}, not finite")
+    y = _run(wc, matrix, x.cuda()).cpu().double()
+    ref = torch.stack([(w * v).sum(dim=1) for v in x.double()])
+    fin = torch.isfinite(ref)
+    assert torch.equal(torch.isnan(y), torch.isnan(ref))
+    assert torch.equal(y[~fin & ~torch.isnan(ref)], ref[~fin & ~torch.isnan(ref)])
+    tol = q4_tolerance(w, torch.nan_to_num(x.double(), 0.0, 0.0, 0.0))
+    assert bool(((y - ref).abs()[fin] <= tol[fin]).all())
