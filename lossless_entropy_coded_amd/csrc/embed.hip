@@ -32,7 +32,6 @@
 #include <cstdint>
 
 #include "../../include/wc.h"
-#include "kernels.h"
 
 namespace wc {
 namespace {
@@ -489,8 +488,11 @@ int launch_lookup(LookupParams& p, bool q4, hipStream_t s) {
     return hipGetLastError() == hipSuccess ? WC_OK : WC_ERR_HIP;
 }
 
-}  // namespace
-
+// Tokens sorted by id, then by token: sorted[i] = row << 32 | token, row = vocab
+// for ids (id_bytes 4 or 8 each) outside [0, vocab).  scratch: 2 n words.  1 <=
+// n <= 2^20, vocab <= 2^22.  One launch up to 8192 tokens, else two.  The first
+// one also sets fill_bytes at `fill` to zero, the second one more_bytes behind
+// them (multiples of 16; 0 if there is one launch).
 void launch_sort_ids(const void* ids, uint32_t id_bytes, uint32_t n, uint32_t vocab, uint64_t* sorted,
                      uint32_t* scratch, hipStream_t stream, void* fill, uint64_t fill_bytes, uint64_t more_bytes) {
     SortParams p{};
@@ -518,6 +520,7 @@ void launch_sort_ids(const void* ids, uint32_t id_bytes, uint32_t n, uint32_t vo
                        dim3(kRankThreads), 0, stream, p);
 }
 
+}  // namespace
 }  // namespace wc
 
 using namespace wc;

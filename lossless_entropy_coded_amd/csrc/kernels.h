@@ -189,13 +189,6 @@ int decode_lanes_blocks_per_cu(uint32_t decode_bits, uint32_t waves, uint32_t l2
 hipError_t launch_decode_lanes(const DecodeParams& p, uint32_t decode_bits, uint32_t waves, uint32_t grid,
                                LanesOut mode, bool rans, hipStream_t stream);
 
-// Tokens sorted by id, then by token: sorted[i] = row << 32 | token, row = vocab
-// for ids (id_bytes 4 or 8 each) outside [0, vocab).  scratch: 2 n words.  1 <=
-// n <= 2^20, vocab <= 2^22.  One launch up to 8192 tokens, else two.  The first
-// one also sets fill_bytes at `fill` to zero, the second one more_bytes behind
-// them (multiples of 16; 0 if there is one launch).
-void launch_sort_ids(const void* ids, uint32_t id_bytes, uint32_t n, uint32_t vocab, uint64_t* sorted,
-                     uint32_t* scratch, hipStream_t stream, void* fill, uint64_t fill_bytes, uint64_t more_bytes);
 // The HIP device a plan was made for.
 int plan_device(const wc_plan_s* plan);
 
