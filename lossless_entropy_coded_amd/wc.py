@@ -497,8 +497,26 @@ GEMV_Q4_MAX_VECS = 16
 OUT_KINDS = {"f32": 0, "bf16": 1}
 
 
-def _bytes_ok(t, nbytes: int, device, what: str, call: str) -> int:
-    """The device pointer of a tensor that _require accepts (or of a raw integer pointer)."""
+_KINDS = {}   # dtype -> "bf16", "f32", "words" (whole numbers) or its own name, of the types seen
+
+
+def _kind_of(dtype) -> str:
+    kind = _KINDS.get(dtype)
+    if kind is None:
+        name = str(dtype).rsplit(".", 1)[-1]
+        kind = _KINDS[dtype] = {"bfloat16": "bf16", "float32": "f32"}.get(
+            name, "words" if name.startswith(("int", "uint", "bool")) else name)
+    return kind
+
+
+def _bytes_ok(t, nbytes: int, device, what: str, call: str, kind: str = "") -> int:
+    """The device pointer of a tensor that _require accepts (or of a raw integer pointer).  kind: the floating type
+    that the call reads or writes ("bf16", "f32"), or "words" for whole numbers alone; a tensor of whole numbers is
+    taken as the words that it holds in any case.  Empty: any type."""
+    if kind and hasattr(t, "dtype"):
+        found = _KINDS.get(t.dtype) or _kind_of(t.dtype)
+        if found != kind and found != "words":
+            raise WCError(WC_ERR_INVALID_ARG, call, f"{what} is {t.dtype}, where {kind} is read or written")
     try:
         if t.is_cuda and t.get_device() == device and t.nbytes >= nbytes and t.is_contiguous():
             return t.data_ptr()
@@ -550,9 +568,9 @@ class Q4Matrix:
         self._tensors = (codes, scales, zeros)
         self.device = _current_device()
         n = self.rows * -(-self.cols // max(self.group, 1))
-        c = _bytes_ok(codes, self.rows * self.cols // 2, self.device, "codes", "wc_q4_check")
-        s = _bytes_ok(scales, 2 * n, self.device, "scales", "wc_q4_check")
-        z = _bytes_ok(zeros, n, self.device, "zeros", "wc_q4_check") if zeros is not None else 0
+        c = _bytes_ok(codes, self.rows * self.cols // 2, self.device, "codes", "wc_q4_check", "words")
+        s = _bytes_ok(scales, 2 * n, self.device, "scales", "wc_q4_check", "bf16")
+        z = _bytes_ok(zeros, n, self.device, "zeros", "wc_q4_check", "words") if zeros is not None else 0
         self._struct = _Q4(c, s, z, self.rows, self.cols, self.group)
         self._ref = ctypes.addressof(self._struct)
         _check(_lib.wc_q4_check(self._ref), "wc_q4_check")
@@ -573,8 +591,8 @@ def gemv_q4_async(W: Q4Matrix, x_dev, n_vecs: int, y_dev, stream=None) -> None:
     dev = _on_device(W, call)
     if n_vecs >> 32:
         _sizes(call, n_vecs=n_vecs)
-    x = _bytes_ok(x_dev, 2 * n_vecs * W.cols, dev, "x", call)
-    y = _bytes_ok(y_dev, 4 * n_vecs * W.rows, dev, "y", call)
+    x = _bytes_ok(x_dev, 2 * n_vecs * W.cols, dev, "x", call, "bf16")
+    y = _bytes_ok(y_dev, 4 * n_vecs * W.rows, dev, "y", call, "f32")
     _check(_lib.wc_gemv_q4_async(W._ref, x, n_vecs, y, _stream_handle(stream)), call)
 
 
@@ -585,9 +603,9 @@ def embed_async(table_dev, vocab: int, dim: int, ids_dev, n: int, out_dev, scale
     if (vocab | dim | n) >> 32:
         _sizes(call, vocab=vocab, dim=dim, n=n)
     width = _index_bytes(ids_dev, "ids", call)
-    table = _bytes_ok(table_dev, 2 * vocab * dim, dev, "table", call)
+    table = _bytes_ok(table_dev, 2 * vocab * dim, dev, "table", call, "bf16")
     ids = _bytes_ok(ids_dev, width * n, dev, "ids", call)
-    out = _bytes_ok(out_dev, 2 * n * dim, dev, "out", call)
+    out = _bytes_ok(out_dev, 2 * n * dim, dev, "out", call, "bf16")
     _check(_lib.wc_embed_async(table, vocab, dim, ids, width, n, scale, out, _stream_handle(stream)), call)
 
 
@@ -599,7 +617,7 @@ def embed_q4_async(W: Q4Matrix, ids_dev, n: int, out_dev, scale: float = 1.0, st
         _sizes(call, n=n)
     width = _index_bytes(ids_dev, "ids", call)
     ids = _bytes_ok(ids_dev, width * n, dev, "ids", call)
-    out = _bytes_ok(out_dev, 2 * n * W.cols, dev, "out", call)
+    out = _bytes_ok(out_dev, 2 * n * W.cols, dev, "out", call, "bf16")
     _check(_lib.wc_embed_q4_async(W._ref, ids, width, n, scale, out, _stream_handle(stream)), call)
 
 
@@ -623,9 +641,9 @@ def embed_grad_async(dout_dev, ids_dev, n: int, dtable_dev, vocab: int, dim: int
     if out not in OUT_KINDS:
         raise WCError(WC_ERR_INVALID_ARG, call, f"out is {out!r}, not one of {sorted(OUT_KINDS)}")
     width = _index_bytes(ids_dev, "ids", call)
-    dout = _bytes_ok(dout_dev, 2 * n * dim, dev, "dout", call)
+    dout = _bytes_ok(dout_dev, 2 * n * dim, dev, "dout", call, "bf16")
     ids = _bytes_ok(ids_dev, width * n, dev, "ids", call)
-    dtable = _bytes_ok(dtable_dev, (4 if out == "f32" else 2) * vocab * dim, dev, "dtable", call)
+    dtable = _bytes_ok(dtable_dev, (4 if out == "f32" else 2) * vocab * dim, dev, "dtable", call, out)
     work, work_bytes = _workspace(work_dev, work_bytes, dev, call)
     _check(_lib.wc_embed_grad_async(dout, ids, width, n, scale, dtable, OUT_KINDS[out], vocab, dim, bool(accumulate),
                                     work, work_bytes, _stream_handle(stream)), call)
@@ -647,11 +665,11 @@ def ce_loss_async(h_dev, W_dev, targets_dev, tokens: int, vocab: int, dim: int, 
     if (tokens | vocab | dim) >> 32:
         _sizes(call, tokens=tokens, vocab=vocab, dim=dim)
     width = _index_bytes(targets_dev, "targets", call)
-    h = _bytes_ok(h_dev, 2 * tokens * dim, dev, "h", call)
-    W = _bytes_ok(W_dev, 2 * vocab * dim, dev, "W", call)
+    h = _bytes_ok(h_dev, 2 * tokens * dim, dev, "h", call, "bf16")
+    W = _bytes_ok(W_dev, 2 * vocab * dim, dev, "W", call, "bf16")
     targets = _bytes_ok(targets_dev, width * tokens, dev, "targets", call)
-    loss = _bytes_ok(loss_dev, 4 * tokens, dev, "loss", call)
-    lse = _bytes_ok(lse_dev, 4 * tokens, dev, "lse", call)
+    loss = _bytes_ok(loss_dev, 4 * tokens, dev, "loss", call, "f32")
+    lse = _bytes_ok(lse_dev, 4 * tokens, dev, "lse", call, "f32")
     work, work_bytes = _workspace(work_dev, work_bytes, dev, call)
     _check(_lib.wc_ce_loss_async(h, W, targets, width, tokens, vocab, dim, loss, lse, work, work_bytes,
                                  _stream_handle(stream)), call)
@@ -665,13 +683,13 @@ def ce_grad_async(h_dev, W_dev, targets_dev, tokens: int, vocab: int, dim: int, 
     if (tokens | vocab | dim) >> 32:
         _sizes(call, tokens=tokens, vocab=vocab, dim=dim)
     width = _index_bytes(targets_dev, "targets", call)
-    h = _bytes_ok(h_dev, 2 * tokens * dim, dev, "h", call)
-    W = _bytes_ok(W_dev, 2 * vocab * dim, dev, "W", call)
+    h = _bytes_ok(h_dev, 2 * tokens * dim, dev, "h", call, "bf16")
+    W = _bytes_ok(W_dev, 2 * vocab * dim, dev, "W", call, "bf16")
     targets = _bytes_ok(targets_dev, width * tokens, dev, "targets", call)
-    lse = _bytes_ok(lse_dev, 4 * tokens, dev, "lse", call)
-    dloss = _bytes_ok(dloss_dev, 4 * tokens, dev, "dloss", call)
-    dh = _bytes_ok(dh_dev, 2 * tokens * dim, dev, "dh", call) if dh_dev is not None else 0
-    dW = _bytes_ok(dW_dev, 2 * vocab * dim, dev, "dW", call) if dW_dev is not None else 0
+    lse = _bytes_ok(lse_dev, 4 * tokens, dev, "lse", call, "f32")
+    dloss = _bytes_ok(dloss_dev, 4 * tokens, dev, "dloss", call, "f32")
+    dh = _bytes_ok(dh_dev, 2 * tokens * dim, dev, "dh", call, "bf16") if dh_dev is not None else 0
+    dW = _bytes_ok(dW_dev, 2 * vocab * dim, dev, "dW", call, "bf16") if dW_dev is not None else 0
     work, work_bytes = _workspace(work_dev, work_bytes, dev, call)
     _check(_lib.wc_ce_grad_async(h, W, targets, width, tokens, vocab, dim, lse, dloss, dh, dW, work, work_bytes,
                                  _stream_handle(stream)), call)
