@@ -374,26 +374,32 @@ def decode_u8_async(plan: Plan, blob_dev, out_dev, stream=None) -> None:
                                    ctypes.c_void_p(_stream_handle(stream))), "wc_decode_u8_async")
 
 
-_torch = None   # torch, once it is there and holds a device
+_lookups_found = None   # what _lookups returns, once torch has a device in use
 
 
-def _torch_on_device():
-    """torch, if it has a device in use (None before): looked up once, for calls that take a few microseconds."""
-    global _torch
-    if _torch is None:
+def _lookups():
+    """(current device, handle of its current stream), two functions, once torch has a device in use (None before).
+    A Stream object costs 3 us, much of a call of a token, so the handle itself is asked for where torch has it."""
+    global _lookups_found
+    if _lookups_found is None:
         import torch
-        if torch.cuda.is_initialized():
-            _torch = torch
-    return _torch
+        if not torch.cuda.is_initialized():
+            return None
+        device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _lookups_found = device, (lambda: raw_stream(device())) if raw_stream else _current_stream
+    return _lookups_found
+
+
+def _current_stream() -> int:
+    import torch
+    return int(torch.cuda.current_stream().cuda_stream)
 
 
 def _stream_handle(stream) -> int:
     if stream is None:
-        torch = _torch_on_device()
-        if torch is not None:   # the handle itself: a Stream object costs 3 us
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-        import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        found = _lookups_found or _lookups()
+        return found[1]() if found else _current_stream()
     if hasattr(stream, "cuda_stream"):
         return int(stream.cuda_stream)
     return int(stream)
@@ -427,9 +433,9 @@ def stream_reference_async(src_dev, src_bytes: int, dst_dev, dst_bytes: int, str
 
 
 def _current_device():
-    torch = _torch_on_device()
-    if torch is not None:
-        return torch._C._cuda_getDevice()
+    found = _lookups_found or _lookups()
+    if found:
+        return found[0]()
     import torch
     return torch.cuda.current_device() if torch.cuda.is_available() else None
 
