@@ -343,15 +343,22 @@ int wc_q4_check(const wc_q4_matrix* W);
  *   x   device, n_vecs x cols bf16, 16-byte aligned;
  *   y   device, n_vecs x rows float32 (written), 4-byte aligned.
  * n_vecs is at most WC_GEMV_Q4_MAX_VECS.  Sums are held in fp32 and taken in
- * a fixed order: y is a deterministic function of the bits of W and x.  rows == 0 or n_vecs == 0 is a no-op.  WC_ERR_INVALID_ARG
- * for bad sizes or alignment, WC_ERR_HIP if the launch fails.
+ * a fixed order: y is a deterministic function of n_vecs and the bits of W and
+ * x.  (Of n_vecs too, since a vector's x is held relative to the largest value
+ * of the 512 columns that go together for one vector, 256 for 2 to 8, 128 for
+ * more: exact down to 2^-32 of it, off by less than 2^-39 of it below.)
+ * rows == 0 or n_vecs == 0 is a no-op.  WC_ERR_INVALID_ARG for bad sizes or
+ * alignment, WC_ERR_HIP if the launch fails.
  */
 #define WC_GEMV_Q4_MAX_VECS 16u
 int wc_gemv_q4_async(const wc_q4_matrix* W, const uint16_t* x, uint32_t n_vecs, float* y, void* stream);
 
 /*
- * wc_embed_async, wc_embed_q4_async -- out[t] = scale * table[id[t]], rounded
- * once to bf16 (scale 1 on a bf16 table copies the words' bits).  One launch.
+ * wc_embed_async, wc_embed_q4_async -- out[t] = scale * table[id[t]]: a product
+ * in fp32 (with a 4-bit table's entry as fp32 holds it, which is exactly if it
+ * is in fp32's range), rounded to bf16.  The product of a scale that is a power
+ * of two is exact, so that this is the only rounding; scale 1 on a bf16 table
+ * copies the words' bits.  One launch.
  *   table     device, vocab x dim bf16, 16-byte aligned, dim a multiple of 8
  *             (a tensor of wc_decode_async's output qualifies when its element
  *             offset is a multiple of 8); or a 4-bit matrix of vocab rows;
@@ -373,9 +380,9 @@ int wc_embed_q4_async(const wc_q4_matrix* W, const void* ids, uint32_t id_bytes,
  *   dtable    device, vocab x dim, 16-byte aligned: float32 (out_kind
  *             WC_OUT_F32) or bf16 (WC_OUT_BF16);
  *   accumulate  0: every row is written, zeros where no token has it; else the
- *             sums are added to dtable (rounded once) and other rows are left
- *             as they are: the gradient of a table that is also the output
- *             matrix goes on top of wc_ce_grad_async's dW this way;
+ *             sums are added to dtable in fp32, rounded to its type, and other
+ *             rows are left as they are: the gradient of a table that is also the
+ *             output matrix goes on top of wc_ce_grad_async's dW this way;
  *   work_dev  device scratch of at least wc_embed_grad_work_bytes(n, dim)
  *             bytes, 256-byte aligned, overwritten; calls that may overlap
  *             need one each.
@@ -408,8 +415,10 @@ int wc_embed_grad_async(const uint16_t* dout, const void* ids, uint32_t id_bytes
  *            for the loss; else for both calls), overwritten; calls that may
  *            overlap need one each.
  * tokens * vocab is at most WC_MAX_LOGITS (larger batches: call by call).
- * z is accumulated in fp32; the gradient keeps a piece of the vocabulary's d
- * at a time, in bf16.  Results are the same bits on every run.  tokens == 0
+ * z is accumulated in fp32 (a logit of +infinity or NaN gives its token NaN,
+ * one of -infinity leaves that entry out); the gradient keeps a piece of the
+ * vocabulary's d at a time, in bf16, and what the target's value loses to that
+ * beside it (up to 128 tokens, for dW, what every value loses).  Results are the same bits on every run.  tokens == 0
  * is a no-op, but for dW, which is then zero.  The gradient takes the lse
  * that the loss call wrote.
  */

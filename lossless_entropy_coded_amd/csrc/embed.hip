@@ -1,7 +1,7 @@
 // embed.hip -- embedding lookup with scaling, from a bf16 table or from a
 // 4-bit one with group scales, and the table's gradient.
 //
-//   out[t]     = scale * table[id[t]]            (rounded once to bf16)
+//   out[t]     = scale * table[id[t]]            (in fp32, rounded to bf16)
 //   dtable[v]  = scale * sum over t with id[t] = v of dout[t]
 //
 // An id outside [0, vocab) marks a token without a row (padding): its output
