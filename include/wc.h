@@ -416,11 +416,11 @@ int wc_embed_grad_async(const uint16_t* dout, const void* ids, uint32_t id_bytes
  *            overlap need one each.
  * tokens * vocab is at most WC_MAX_LOGITS (larger batches: call by call).
  * z is accumulated in fp32 (a logit of +infinity or NaN gives its token NaN,
- * one of -infinity leaves that entry out); the gradient keeps a piece of the
- * vocabulary's d at a time, in bf16, and what the target's value loses to that
- * beside it (up to 128 tokens, for dW, what every value loses).  Results are the same bits on every run.  tokens == 0
- * is a no-op, but for dW, which is then zero.  The gradient takes the lse
- * that the loss call wrote.
+ * one of -infinity leaves that entry out of the loss); the gradient keeps a
+ * piece of the vocabulary's d at a time, in bf16, and what the target's value
+ * loses to that beside it (up to 128 tokens, for dW, what every value loses).
+ * Results are the same bits on every run.  tokens == 0 is a no-op, but for dW,
+ * which is then zero.  The gradient takes the lse that the loss call wrote.
  */
 int wc_ce_work_bytes(uint64_t tokens, uint32_t vocab, uint32_t dim, int grad, uint64_t* work_bytes);
 int wc_ce_loss_async(const uint16_t* h, const uint16_t* W, const void* targets, uint32_t target_bytes,

@@ -766,33 +766,31 @@ bool takes_big(uint64_t m, uint64_t n) {
 }
 // dh has few outputs and a long sum, which is split.  Tiles and splits are those
 // that a model of the time likes best: rounds of workgroups, each with a fixed
-// part and one per 64 of its sum (measured: 1.1 us in big tiles, 0.8 in mid and
-// thin ones), and the partial sums written and read once, at 4 TB/s.  One split
+// part and one per 64 of its sum (measured: 1.1 us in big tiles, 0.8 in mid
+// ones), and the partial sums written and read once, at 4 TB/s.  One split
 // per sum, or a multiple of the dies (see ce_dh_kernel).  Measured (dh, us):
 // 4 tokens x 66561 x 488 40 with 65 splits of 1024 as of now; 515 x 32003 x
 // 1160 94 with 10 splits, 57 with 8.
-enum DhTile { kDhBig, kDhMid, kDhThin };
 struct DhPlan {
-    DhTile tile;
+    bool big;
     uint32_t splits;
 };
 DhPlan dh_plan(uint64_t tokens, uint32_t dim, uint64_t piece) {
     DhPlan best{};
     double best_us = 1e30;
     const struct {
-        DhTile tile;
-        uint32_t m, n, slots;
+        bool big;
+        uint32_t edge, slots;
         double us;
-    } kinds[] = {{kDhBig, 256, 256, kCus, 1.1}, {kDhMid, 128, 128, 2 * kCus, 0.8}, {kDhThin, 256, 64, kCus, 0.8}};
+    } kinds[] = {{true, 256, kCus, 1.1}, {false, 128, 2 * kCus, 0.8}};
     for (const auto& k : kinds) {
-        if (k.tile == kDhThin && tokens > kThinTokens) continue;
-        const uint64_t tiles = (uint64_t)cdiv(dim, k.m) * cdiv(tokens, k.n);
+        const uint64_t tiles = (uint64_t)cdiv(dim, k.edge) * cdiv(tokens, k.edge);
         for (uint32_t s = 1; s <= 16 * kDies; s = s == 1 ? kDies : s + kDies) {
             if (s > 1 && (piece < s * kUnit || tiles * s > 4ull * k.slots)) break;
             const double units = (double)((piece + s - 1) / s) / kUnit;
             const double us = (double)((tiles * s + k.slots - 1) / k.slots) * (6.0 + units * k.us) +
                               (double)s * (double)tokens * dim * 8 / 4e6;
-            if (us < best_us) best_us = us, best = {k.tile, s};
+            if (us < best_us) best_us = us, best = {k.big, s};
         }
     }
     return best;
@@ -810,7 +808,7 @@ uint64_t up(uint64_t v, uint64_t m) { return (v + m - 1) / m * m; }
 // 256 MiB, at least 1024 entries, whole tiles.
 struct CeLayout {
     uint32_t piece, ldd, rests, splits, split_k;
-    DhTile dh_tile;
+    bool dh_big;
     uint64_t own, part, d, dh_part, h_own, loss_bytes, grad_bytes;
 };
 
@@ -830,7 +828,7 @@ CeLayout layout(uint64_t tokens, uint32_t vocab, uint32_t dim) {
     l.ldd = (uint32_t)(piece + 128);   // an odd number of 256-byte lines: neighbouring rows in different memory channels
     const DhPlan plan = dh_plan(tokens, dim, piece);
     const uint32_t splits = plan.splits;
-    l.dh_tile = plan.tile;
+    l.dh_big = plan.big;
     l.split_k = (uint32_t)up((piece + splits - 1) / splits, kUnit);
     l.splits = splits;   // the last ones may be empty: they leave zeros
     l.d = own_bytes;
@@ -946,8 +944,7 @@ extern "C" int wc_ce_grad_async(const uint16_t* h, const uint16_t* W, const void
         else if (takes_big(len, tokens)) run_d<Big<false, false>>(p, s);
         else run_d<Mid<false, false>>(p, s);
         if (dh) {
-            if (l.dh_tile == kDhThin) run_dh<Thin<true, false>>(p, s);
-            else if (l.dh_tile == kDhBig) run_dh<Big<true, false>>(p, s);
+            if (l.dh_big) run_dh<Big<true, false>>(p, s);
             else run_dh<Mid<true, false>>(p, s);
         }
         if (dW) {
