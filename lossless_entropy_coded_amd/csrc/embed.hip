@@ -136,16 +136,11 @@ struct SortParams {
     uint64_t fill_chunks;  // 16 bytes each
 };
 
-// Per thread, not kept in caches: with the whole table set here, 154 us at 16384 tokens, 32768 x 4096 (2 chunks: 160,
-// 8: 168; kept: 172).
-constexpr uint32_t kFillChunks = 1;
-
-// The work of a filling workgroup, of the sorting launch's p.blocks and more.
+// The work of a filling workgroup, of the sorting launch's p.blocks and more: 16 bytes per thread, not kept in caches
+// (with the whole table set here, 16384 tokens, 32768 x 4096, in a loop: 154 us; 32 bytes 160, 128: 168; kept: 172).
 __device__ __forceinline__ void fill_zeros(const SortParams& p) {
-    uint64_t i = (uint64_t)(blockIdx.x - p.blocks) * blockDim.x * kFillChunks + threadIdx.x;
-#pragma unroll
-    for (uint32_t k = 0; k < kFillChunks; ++k, i += blockDim.x)
-        if (i < p.fill_chunks) __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, p.fill + i);
+    const uint64_t i = (uint64_t)(blockIdx.x - p.blocks) * blockDim.x + threadIdx.x;
+    if (i < p.fill_chunks) __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, p.fill + i);
 }
 
 __device__ __forceinline__ uint32_t row_at(const SortParams& p, uint32_t t) {
@@ -499,7 +494,7 @@ void launch_sort_ids(const void* ids, uint32_t id_bytes, uint32_t n, uint32_t vo
     p.ids = ids, p.id_bytes = id_bytes, p.n = n, p.vocab = vocab, p.sorted = sorted;
     p.fill = static_cast<u32x4*>(fill), p.fill_chunks = fill_bytes / 16;
     const auto blocks = [&](uint32_t threads) {   // of the first launch, those that fill among them
-        return dim3((uint32_t)(p.blocks + (p.fill_chunks + threads * kFillChunks - 1) / (threads * kFillChunks)));
+        return dim3((uint32_t)(p.blocks + (p.fill_chunks + threads - 1) / threads));
     };
     if (n <= kDirectTokens) {
         p.blocks = (n + 63) / 64;
@@ -599,7 +594,7 @@ extern "C" int wc_embed_grad_async(const uint16_t* dout, const void* ids, uint32
     const hipStream_t s = static_cast<hipStream_t>(stream);
     uint64_t sort_bytes = 0, rank_bytes = 0;
     if (n && !p.accumulate) {
-        const uint64_t row_bytes = (uint64_t)dim * (p.bf16 ? 2 : 4), table_bytes = vocab * row_bytes;
+        const uint64_t row_bytes = (uint64_t)dim * (p.bf16 ? 2 : 4);
         const bool one = n <= kDirectTokens;
         const uint64_t first = one ? 32ull << 30 : 128ull << 20;   // (a launch holds fewer than 2^32 threads of 16 bytes)
         const uint64_t second = one ? 0 : n * 6144;

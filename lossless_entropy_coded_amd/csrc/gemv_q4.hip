@@ -49,6 +49,7 @@
 #include <cstdint>
 
 #include "../../include/wc.h"
+#include "buffers.h"
 
 namespace wc {
 namespace {
@@ -62,7 +63,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr uint32_t kStepCols = 128;
 constexpr uint32_t kMaxWaves = 8;
-constexpr uint32_t kNoChunk = 0xFFFFFFF0u;   // a buffer offset beyond every operand: loads zeros
 
 struct Q4Params {
     const uint8_t* codes;
@@ -91,7 +91,7 @@ struct Q4Shape {
 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, uint64_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)(uint32_t)bytes, 0x00027000);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)(uint32_t)bytes, kBufferWord);
 }
 
 // Constants in registers: an operation takes no second literal, and with these

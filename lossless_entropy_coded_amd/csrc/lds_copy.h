@@ -5,11 +5,11 @@
 
 #include <cstdint>
 
+#include "buffers.h"
+
 namespace wc {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
-constexpr uint32_t kNoChunk = 0xFFFFFFF0u;   // a buffer offset beyond every operand: loads zeros
 
 // The byte offset in LDS of a pointer into it.
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
@@ -19,7 +19,7 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // A buffer of `bytes` bytes at p: accesses beyond it load zeros.
 __device__ __forceinline__ u32x4 buffer_words(const void* p, uint32_t bytes) {
     const uint64_t addr = reinterpret_cast<uint64_t>(p);
-    return u32x4{(uint32_t)addr, (uint32_t)(addr >> 32) & 0xFFFFu, bytes, 0x00027000u};
+    return u32x4{(uint32_t)addr, (uint32_t)(addr >> 32) & 0xFFFFu, bytes, kBufferWord};
 }
 
 // Start copying 16 bytes per lane from a buffer to consecutive LDS places from
