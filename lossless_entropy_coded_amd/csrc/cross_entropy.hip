@@ -769,8 +769,8 @@ bool takes_big(uint64_t m, uint64_t n) {
 // part and one per 64 of its sum (measured: 1.1 us in big tiles, 0.8 in mid
 // ones), and the partial sums written and read once, at 4 TB/s.  One split
 // per sum, or a multiple of the dies (see ce_dh_kernel).  Measured (dh, us):
-// 4 tokens x 66561 x 488 40 with 65 splits of 1024 as of now; 515 x 32003 x
-// 1160 94 with 10 splits, 57 with 8.
+// 515 tokens x 32003 x 1160 58 with the 16 splits that it takes, 94 with 10; 4 x
+// 66561 x 488 12 with 128.
 struct DhPlan {
     bool big;
     uint32_t splits;

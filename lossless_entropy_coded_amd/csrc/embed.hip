@@ -583,14 +583,15 @@ extern "C" int wc_embed_grad_async(const uint16_t* dout, const void* ids, uint32
     // tokens too, which are written again: as many bytes as take about as long as the sorting launch, and the ranking
     // one.  The others are written by the summing launch, whose reads leave some of the memory idle, row by row where
     // there are no tokens; few tokens have no ranking and a short summing launch, so there all rows are set beside the
-    // sort.  Measured, us (nothing ahead; 128 MiB beside the sort; that and 6 KiB per token beside the
-    // ranking, as here; the same, and the rest beside the sort):
-    //   32768 x 4096 fp32, 16384 tokens    148  140  131  143
-    //   131072 x 512 fp32, 16384 tokens     84   67   59   64
-    //   131072 x 4096 bf16, 65536 tokens   390  380  351  350
-    //   32000 x 4096 bf16, 32768 tokens    152  135  128  127
-    //   32768 x 4096 fp32, 8192 tokens       -  121    -  115
-    //   32000 x 4096 fp32, 2048 tokens     119  110    -  101
+    // sort.  Measured on inputs that rotate past the caches, us (nothing ahead; 128 MiB beside the sort; that and 6 KiB
+    // per token beside the ranking, as here; the same, and the rest beside the sort; one set of inputs in a loop, whose
+    // gradients stay in the cache, takes up to 11 us less; a table of its own for each call too, up to 14 more):
+    //   32768 x 4096 fp32, 16384 tokens    160  149  140  160
+    //   131072 x 512 fp32, 16384 tokens     84   69   61   76
+    //   131072 x 4096 bf16, 65536 tokens   390  380  352  371
+    //   32000 x 4096 bf16, 32768 tokens    155  144  136  149
+    //   32768 x 4096 fp32, 8192 tokens     140  125    -  120
+    //   32000 x 4096 fp32, 2048 tokens     118  111    -  102
     const hipStream_t s = static_cast<hipStream_t>(stream);
     uint64_t sort_bytes = 0, rank_bytes = 0;
     if (n && !p.accumulate) {

@@ -33,7 +33,8 @@
 // (Subtracting zero * sum(x) from sum(code x) instead would lose small products
 // next to a large x that its zero point cancels.  bf16 in place of f16, code
 // by code through v_cvt_off_f32_i4, needs no scaling of x but 1.75 operations
-// per weight, 2.4 with zero points: 12.2 us at 14336 x 4096, one vector.)
+// per weight, 2.4 with zero points: 12.2 us at 14336 x 4096, one vector, where
+// this takes 9.8.)
 //
 // A wave takes 16 kTiles rows and a part of the columns, 128 columns per step.
 // Lane 4 r + q loads the 16 bytes of row r's q-th chunk of 32 columns, so that
@@ -451,16 +452,27 @@ void launch(Q4Params& p, uint32_t waves, hipStream_t s) {
 
 // Rows and waves per workgroup.  From 8192 rows on there are workgroups enough
 // of 16 rows and 4 waves, or of 32 rows, which share the work on x, where
-// vectors make that count, and then of 8 waves from 8 vectors on; below, 16 rows
-// and 8 waves, which split the columns further.  Measured, us:
+// vectors make that count, and then of 8 waves from 5 vectors on; below, 16 rows
+// and 8 waves, which split the columns further.  Measured on matrices that rotate
+// past the caches, groups of 128 (32 for 2088 columns), us:
 //                                        16 rows        32 rows
 //                                   4 waves 8 waves 4 waves 8 waves
-//   14336 x 4096, one vector            9.5    10.4    10.1    11.5
-//   4096 x 14336, one vector            9.9     9.0    14.0    13.5
-//   14336 x 4096, 4 vectors            10.9    11.8    10.6    10.7
-//   14336 x 4096, 16 vectors           18.0    18.8    15.1    14.5
-//   8192 x 28672, 8 vectors            47.0    46.1    44.2    41.3
-//   1003 x 2088, 5 vectors              6.6     5.7     8.9     7.6
+//   14336 x 4096, one vector           10.9    12.3    11.8    13.0
+//   10240 x 4096, one vector            8.8     9.7    11.3    12.3
+//    8192 x 4096, one vector            7.3     7.5     8.1     7.9
+//    6144 x 4096, one vector            6.9     7.0     7.4     7.3
+//    4096 x 14336, one vector          11.3    10.0    15.4    16.1
+//   14336 x 4096, 4 vectors            12.1    12.9    11.6    11.8
+//    8192 x 4096, 4 vectors             8.1     8.0     8.2     8.1
+//    6144 x 4096, 4 vectors             7.9     7.9     8.0     7.8
+//    4096 x 14336, 4 vectors           16.0    12.1    19.1    16.3
+//   14336 x 4096, 16 vectors           19.7    20.1    16.1    15.7
+//    8192 x 28672, 8 vectors           44.6    43.6    41.7    38.1
+//    8192 x 4096, 8 vectors             9.7    10.0     9.3     9.2
+//    6144 x 4096, 8 vectors             9.6     9.8     9.1     8.8
+//    4096 x 4096, 8 vectors             7.8     6.8     8.9     8.5
+//    1003 x 2088, 4 vectors             6.4     5.5     8.6     7.4
+// (At 6144 rows 32 already gain a tenth for 8 vectors and more.)
 template <int kVecs>
 void launch_rows(Q4Params& p, hipStream_t s) {
     if (p.rows < 8192) return launch<kVecs, 1>(p, 8, s);
