@@ -499,7 +499,7 @@ __global__ __launch_bounds__(T::kThreads) void ce_d_kernel(CeParams p) {
             if (v == own[j]) x -= 1.0f;
             x = v < p.piece_end && own[j] < p.vocab ? x * g[j] : 0.0f;
             b[e] = f32_bf16(x);
-            const float lost = x - bf16_f32(b[e]);
+            const float lost = (b[e] & 0x7F80u) == 0x7F80u ? 0.0f : x - bf16_f32(b[e]);   // (an infinity loses nothing)
             if (v == own[j] && v < p.piece_end) p.own[n0 + T::n(j)] = lost;
             if (rest) b[e] = f32_bf16(lost);
         }

@@ -47,3 +47,21 @@ def test_target_rows(wc, tokens, vocab, dim, hot):
     assert float((dW.double() - ref.dW).norm()) <= 1.1 * ref.dW_off
     again = _gradients(wc, h, W, t, dloss)
     assert torch.equal(dh, again[0]) and torch.equal(dW, again[1])
+
+
+@pytest.mark.parametrize("tokens,vocab,dim", [(20, 300, 72), (200, 300, 72), (1100, 9000, 1032)])
+def test_infinite_upstream_gradient(wc, tokens, vocab, dim):
+    """An infinite dloss makes its token's d infinite and dW with it, of the sign that the formula gives: what an
+    infinity loses to rounding is nothing."""
+    h, W, t, dloss = seeded(tokens, vocab, dim, 8, pads=False)
+    at = tokens // 2
+    h[at] = torch.where(h[at] == 0, 1.0, h[at].float()).to(torch.bfloat16)
+    for value in (float("inf"), float("-inf")):
+        dloss[at] = value
+        log(f"case: ce_grad {tokens}x{vocab}x{dim}, dloss {value}")
+        dh, dW = _gradients(wc, h, W, t, dloss)
+        rows = torch.arange(vocab, device="cuda")
+        sign = torch.where(rows == t[at], -1.0, 1.0)[:, None] * h[at].float().sign()[None] * value
+        assert torch.equal(dW.float(), sign)
+        rest = torch.arange(tokens, device="cuda") != at
+        assert bool(torch.isfinite(dh[rest]).all()) and not bool(torch.isfinite(dh[at]).any())
