@@ -430,6 +430,137 @@ int wc_ce_grad_async(const uint16_t* h, const uint16_t* W, const void* targets, 
                      uint64_t tokens, uint32_t vocab, uint32_t dim, const float* lse, const float* dloss,
                      uint16_t* dh, uint16_t* dW, void* work_dev, uint64_t work_bytes, void* stream);
 
+/*
+ * Codes in 8-bit floating point: e4m3 bytes (OCP: no infinities, 0x7F and 0xFF
+ * NaN, largest value 448), one fp32 scale per block of WC_FP8_BLOCK columns
+ * (the last block of a row may be shorter); a code stands for scale * code.
+ *
+ * wc_quant_fp8_async -- rows of activations to such codes.  With a the largest
+ * magnitude of a row's block,
+ *   scale = max(a, 2^-100) / 448,   code = y / scale, rounded to nearest even;
+ * a block that holds an infinity or a NaN gets the scale NaN.  One launch.
+ *   x       device, 16-byte aligned bf16, dim a multiple of 8; gated 0: n x dim,
+ *           y = x; else n x 2 dim, each row gate and then up:
+ *           y = silu(gate) up = gate / (1 + exp(-gate)) up, in fp32;
+ *   codes   device, n x dim bytes (written), 16-byte aligned;
+ *   scales  device, n x ceil(dim / WC_FP8_BLOCK) float32 (written).
+ * n == 0 is a no-op; n is at most WC_MAX_TOKENS.
+ */
+#define WC_FP8_BLOCK 128u
+int wc_quant_fp8_async(const uint16_t* x, uint64_t n, uint32_t dim, int gated, uint8_t* codes, float* scales,
+                       void* stream);
+
+/*
+ * wc_rms_norm_async -- the norm before a projection, with the residual's
+ * addition.  With h = x + residual rounded to bf16 (without one, h = x),
+ *   r[t] = 1 / sqrt(mean_c h[t][c]^2 + eps),   y[t][c] = h[t][c] r[t] weight[c],
+ * in fp32 from h on.  One launch.
+ *   x         device, n x dim bf16, dim a multiple of 8;
+ *   residual  device, n x dim bf16, or NULL (then sum is NULL too);
+ *   weight    device, dim bf16;
+ *   sum       device, n x dim bf16 (written): h, the residual of the next layer;
+ *   y         device, n x dim bf16 (written), or NULL;
+ *   codes, scales  as wc_quant_fp8_async writes them of y in fp32, or both NULL
+ *             (y or codes must be given);
+ *   rstd      device, n float32 (written): r, for the gradient; or NULL.
+ * bf16 tensors and codes are 16-byte aligned.  sum may be x or residual itself,
+ * y may be x or (without a residual) x; no other outputs may overlap inputs.
+ * eps is at least 0.  n == 0 is a no-op.  Squares are summed in fp32: a row whose
+ * sum of squares leaves its range has r = 0.
+ */
+int wc_rms_norm_async(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, uint64_t n, uint32_t dim,
+                      float eps, uint16_t* sum, uint16_t* y, uint8_t* codes, float* scales, float* rstd, void* stream);
+
+/*
+ * wc_rms_norm_grad_async -- the gradient of y (rounding taken as the identity).
+ * With u = h r and g = weight dy,
+ *   dh[t][c]   = dsum[t][c] + r[t] (g[t][c] - u[t][c] mean_c(g[t][c] u[t][c])),
+ *   dweight[c] = sum_t dy[t][c] u[t][c].
+ * dh is the gradient of x and of the residual alike.  Two launches at most.
+ *   dy       device, n x dim bf16: the gradient of y;
+ *   h, rstd  what wc_rms_norm_async wrote as sum and rstd (h is x without a residual);
+ *   dsum     device, n x dim bf16: the gradient that h has from where else it
+ *            goes, or NULL: none;
+ *   dh       device, n x dim bf16 (written), or NULL; it may be dy, h or dsum itself;
+ *   dweight  device, dim float32, or NULL (not both): written, or, where
+ *            accumulate is not 0, added to;
+ *   work_dev device scratch of at least wc_rms_norm_grad_work_bytes(n, dim)
+ *            bytes, 256-byte aligned, overwritten (not needed without dweight);
+ *            calls that may overlap need one each.
+ * Sums are fp32 in a fixed order, the same bits on every run.  n == 0: dweight
+ * is zero (or left as it is).
+ */
+int wc_rms_norm_grad_work_bytes(uint64_t n, uint32_t dim, uint64_t* work_bytes);
+int wc_rms_norm_grad_async(const uint16_t* dy, const uint16_t* h, const uint16_t* weight, const float* rstd,
+                           const uint16_t* dsum, uint64_t n, uint32_t dim, uint16_t* dh, float* dweight,
+                           int accumulate, void* work_dev, uint64_t work_bytes, void* stream);
+
+/*
+ * A matrix of e4m3 codes with a scale per block of WC_FP8_BLOCK rows by
+ * WC_FP8_BLOCK columns in device memory (a plane of codes as
+ * wc_decode_u8_async leaves it):
+ *   w[r][c] = scales[r / 128][c / 128] * code[r][c].
+ */
+typedef struct {
+    const uint8_t* codes;   /* rows x cols, row-major, 16-byte aligned                   */
+    const float* scales;    /* ceil(rows / 128) x ceil(cols / 128) float32               */
+    uint32_t rows;          /* at most WC_MAX_VOCAB                                      */
+    uint32_t cols;          /* a multiple of 16, at most WC_MAX_DIM                      */
+} wc_fp8_matrix;
+
+/* wc_fp8_check -- WC_OK if sizes and alignment are as above, else
+ * WC_ERR_INVALID_ARG.  rows == 0 is valid (pointers are not looked at). */
+int wc_fp8_check(const wc_fp8_matrix* W);
+
+/*
+ * wc_gemm_fp8_async -- y[t] = W x[t] for one token to many:
+ *   y[t][r] = sum_b (x_scales[t][b] scales[r / 128][b]) sum_{c in block b} x_codes[t][c] codes[r][c].
+ * The product of the scales is taken first, in fp32 (it must be in its range);
+ * sums are fp32 in a fixed order that depends on the sizes alone, so y is the
+ * same bits on every run.  At most two launches.
+ *   x_codes   device, tokens x cols e4m3, 16-byte aligned;
+ *   x_scales  device, tokens x ceil(cols / 128) float32 (both as
+ *             wc_quant_fp8_async or wc_rms_norm_async writes them);
+ *   y         device, tokens x rows (written), 16-byte aligned: float32
+ *             (out_kind WC_OUT_F32) or bf16 (WC_OUT_BF16), rounded once;
+ *   work_dev  device scratch of at least wc_gemm_fp8_work_bytes(W, tokens)
+ *             bytes (0: it may be NULL), 256-byte aligned, overwritten; calls
+ *             that may overlap need one each.
+ * tokens is at most WC_MAX_TOKENS, tokens * rows at most WC_MAX_LOGITS; none of
+ * either is a no-op.
+ */
+int wc_gemm_fp8_work_bytes(const wc_fp8_matrix* W, uint64_t tokens, uint64_t* work_bytes);
+int wc_gemm_fp8_async(const wc_fp8_matrix* W, const uint8_t* x_codes, const float* x_scales, uint64_t tokens, void* y,
+                      uint32_t out_kind, void* work_dev, uint64_t work_bytes, void* stream);
+
+/*
+ * wc_clip_grads_async -- the global norm of a list of gradients, and their
+ * clipping, before an optimizer's step:
+ *   norm = sqrt(sum of g^2 over all elements of all tensors),
+ *   out  = g * (max_norm / norm) where max_norm < norm < infinity, else g
+ * (a norm that is infinite or NaN leaves the gradients as they are, and says
+ * so).  Squares are summed in double precision in a fixed order; the product is
+ * fp32, rounded to the tensor's type.
+ *   grads     host array of n tensors, read before the call returns;
+ *   max_norm  at least 0 (infinity: the norm alone, and copies);
+ *   norm      device, one float32 (written);
+ *   work_dev  device scratch of at least wc_clip_grads_work_bytes(grads, n)
+ *             bytes (0: it may be NULL), 256-byte aligned, overwritten; calls
+ *             that may overlap need one each.
+ * Two launches per 96 tensors.  n is at most WC_MAX_GRADS.
+ */
+#define WC_MAX_GRADS      (1u << 20)
+#define WC_MAX_GRAD_NUMEL (1ull << 38)
+typedef struct {
+    const void* g;    /* device, numel elements, aligned to them (faster: to 16 bytes) */
+    void* out;        /* the same, written: g itself, or no part of any tensor read    */
+    uint64_t numel;   /* at most WC_MAX_GRAD_NUMEL; 0: nothing                         */
+    uint32_t kind;    /* of both: WC_OUT_F32 or WC_OUT_BF16                            */
+} wc_grad;
+int wc_clip_grads_work_bytes(const wc_grad* grads, uint32_t n, uint64_t* work_bytes);
+int wc_clip_grads_async(const wc_grad* grads, uint32_t n, float max_norm, float* norm, void* work_dev,
+                        uint64_t work_bytes, void* stream);
+
 /* ---- debug status ---------------------------------------------------------- */
 /*
  * wc_plan_debug_status -- a plan made with WC_DEBUG=1 in the environment

@@ -10,7 +10,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libwc.so")
 SOURCES = ["decode.hip", "decode_lanes.hip", "gemv.hip", "noalloc.hip", "stream.hip", "gemv_q4.hip", "embed.hip",
-           "cross_entropy.hip", "plan.cpp", "encode.cpp"]
+           "cross_entropy.hip", "quant_fp8.hip", "norm.hip", "gemm_fp8.hip", "clip_grads.hip", "plan.cpp", "encode.cpp"]
 
 HIPCC_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "-shared", "--offload-arch=gfx950",

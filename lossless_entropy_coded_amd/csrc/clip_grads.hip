@@ -1,0 +1,253 @@
+// clip_grads.hip -- the global norm of a list of gradients, and their clipping:
+//
+//   norm = sqrt(sum over all tensors and elements of g^2),
+//   out  = g * (max_norm / norm) where max_norm < norm < infinity, else g.
+//
+// Two passes over the gradients, both bound by memory.  The tensors' addresses
+// and sizes are kernel arguments, kBatch tensors to a launch, so that a call
+// needs no device memory for them and can be captured as it stands.  All tensors
+// of a batch are cut into chunks of one size in bytes; a workgroup of the norm
+// takes chunks block, block + grid, ... and leaves one partial sum, in double
+// precision (no gradient of fp32 or bf16 overflows there, and long sums keep
+// fp32's digits).  Every workgroup of the second pass adds all partial sums
+// itself, in the same order, which is less than a launch in between would cost.
+// The second pass goes through the chunks from the last to the first: those read
+// last by the first pass may still lie in the 256 MB cache.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/wc.h"
+#include "e4m3.h"
+
+namespace wc {
+namespace {
+
+constexpr uint32_t kThreads = 256;
+constexpr uint32_t kBatch = 96;            // tensors per launch: 32 bytes of arguments each
+constexpr uint32_t kGroups = 2048;         // workgroups per launch at most
+constexpr uint32_t kRounds = 4;            // 16-byte loads per thread on their way
+
+struct ClipTensor {
+    const void* g;
+    void* out;
+    uint64_t numel;
+    uint32_t first;     // its first chunk
+    uint32_t kind;
+};
+
+struct ClipParams {
+    ClipTensor tensor[kBatch];
+    double* part;
+    uint32_t tensors, chunks, chunk_bytes;
+    uint32_t part_at;   // the batch's first partial sum
+    uint32_t parts;     // of all batches
+    float max_norm;
+    float* norm;        // written by the first workgroup, where not NULL
+};
+static_assert(sizeof(ClipParams) <= 4096, "kernel arguments");
+
+__device__ __forceinline__ uint32_t tensor_of(const ClipParams& p, uint32_t chunk) {
+    uint32_t lo = 0, hi = p.tensors;   // first[lo] <= chunk < first[hi]
+    while (hi - lo > 1) {
+        const uint32_t mid = (lo + hi) / 2;
+        if (p.tensor[mid].first <= chunk) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// The workgroup's sum of v, in every thread; always in the same order.
+__device__ __forceinline__ double group_sum(double v) {
+    __shared__ double sums[kThreads / 64];
+#pragma unroll
+    for (uint32_t d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+    if ((threadIdx.x & 63u) == 0) sums[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = sums[0];
+#pragma unroll
+    for (uint32_t k = 1; k < kThreads / 64; ++k) v += sums[k];
+    return v;
+}
+
+__device__ __forceinline__ double square(float f) { return (double)f * (double)f; }
+
+// Calls wide(k-th 16 bytes' index within the chunk's tensor) or, for what is not whole 16 bytes (or not aligned to
+// them), one(element).
+template <class Wide, class One>
+__device__ __forceinline__ void for_chunk(const ClipParams& p, const ClipTensor& t, uint32_t chunk, Wide wide, One one) {
+    const uint32_t size = t.kind == WC_OUT_F32 ? 4 : 2;
+    const uint32_t per = p.chunk_bytes / size;
+    const uint64_t begin = (uint64_t)(chunk - t.first) * per;
+    const uint64_t left = t.numel - begin;
+    const uint32_t count = left < per ? (uint32_t)left : per;
+    const bool whole = ((reinterpret_cast<uintptr_t>(t.g) | reinterpret_cast<uintptr_t>(t.out)) & 15u) == 0;
+    const uint32_t lanes = whole ? count / (16 / size) : 0;
+    if (lanes) wide(begin / (16 / size), lanes);
+    for (uint32_t i = lanes * (16 / size) + threadIdx.x; i < count; i += kThreads) one(begin + i);
+}
+
+__device__ __forceinline__ float value(const ClipTensor& t, uint64_t i) {
+    return t.kind == WC_OUT_F32 ? static_cast<const float*>(t.g)[i]
+                                : __uint_as_float((uint32_t) static_cast<const uint16_t*>(t.g)[i] << 16);
+}
+
+__global__ __launch_bounds__(kThreads) void clip_norm_kernel(ClipParams p) {
+    double sum = 0.0;
+    for (uint32_t chunk = blockIdx.x; chunk < p.chunks; chunk += gridDim.x) {
+        const ClipTensor& t = p.tensor[tensor_of(p, chunk)];
+        for_chunk(
+            p, t, chunk,
+            [&](uint64_t from, uint32_t lanes) {
+                const u32x4* const g = static_cast<const u32x4*>(t.g) + from;
+                for (uint32_t i = threadIdx.x; i < lanes; i += kThreads * kRounds) {
+                    u32x4 w[kRounds];
+#pragma unroll
+                    for (uint32_t k = 0; k < kRounds; ++k)
+                        w[k] = i + k * kThreads < lanes ? g[i + k * kThreads] : u32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (uint32_t k = 0; k < kRounds; ++k)
+#pragma unroll
+                        for (uint32_t e = 0; e < 4; ++e) {
+                            if (t.kind == WC_OUT_F32) sum += square(__uint_as_float(w[k][e]));
+                            else sum += square(bf16_lo(w[k][e])) + square(bf16_hi(w[k][e]));
+                        }
+                }
+            },
+            [&](uint64_t i) { sum += square(value(t, i)); });
+    }
+    sum = group_sum(sum);
+    if (threadIdx.x == 0) p.part[p.part_at + blockIdx.x] = sum;
+}
+
+__global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipParams p) {
+    double sum = 0.0;
+    for (uint32_t i = threadIdx.x; i < p.parts; i += kThreads) sum += p.part[i];
+    const double total = sqrt(group_sum(sum));
+    const float norm = (float)total;
+    if (p.norm && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = norm;
+    const bool clips = norm > p.max_norm && norm < INFINITY;
+    const float factor = clips ? (float)((double)p.max_norm / total) : 1.0f;
+    for (uint32_t at = blockIdx.x; at < p.chunks; at += gridDim.x) {
+        const uint32_t chunk = p.chunks - 1 - at;
+        const ClipTensor& t = p.tensor[tensor_of(p, chunk)];
+        if (!clips && t.g == t.out) continue;
+        for_chunk(
+            p, t, chunk,
+            [&](uint64_t from, uint32_t lanes) {
+                const u32x4* const g = static_cast<const u32x4*>(t.g) + from;
+                u32x4* const out = static_cast<u32x4*>(t.out) + from;
+                for (uint32_t i = threadIdx.x; i < lanes; i += kThreads * kRounds) {
+                    u32x4 w[kRounds];
+#pragma unroll
+                    for (uint32_t k = 0; k < kRounds; ++k)
+                        w[k] = i + k * kThreads < lanes ? g[i + k * kThreads] : u32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (uint32_t k = 0; k < kRounds; ++k) {
+                        if (i + k * kThreads >= lanes) break;
+                        if (clips) {
+#pragma unroll
+                            for (uint32_t e = 0; e < 4; ++e)
+                                w[k][e] = t.kind == WC_OUT_F32
+                                              ? __float_as_uint(__uint_as_float(w[k][e]) * factor)
+                                              : pack_bf16(bf16_lo(w[k][e]) * factor, bf16_hi(w[k][e]) * factor);
+                        }
+                        out[i + k * kThreads] = w[k];
+                    }
+                }
+            },
+            [&](uint64_t i) {
+                if (t.kind == WC_OUT_F32) {
+                    const float v = static_cast<const float*>(t.g)[i];
+                    static_cast<float*>(t.out)[i] = clips ? v * factor : v;
+                } else {
+                    const uint16_t v = static_cast<const uint16_t*>(t.g)[i];
+                    static_cast<uint16_t*>(t.out)[i] =
+                        clips ? (uint16_t)pack_bf16(__uint_as_float((uint32_t)v << 16) * factor, 0.0f) : v;
+                }
+            });
+    }
+}
+
+uint32_t size_of(const wc_grad& g) { return g.kind == WC_OUT_F32 ? 4 : 2; }
+
+// A list's chunks: 4 to 64 KiB, so that few gradients still are work for many workgroups and large ones are not cut
+// finer than the memory asks for.
+uint32_t chunk_bytes(const wc_grad* grads, uint32_t n) {
+    uint64_t bytes = 0;
+    for (uint32_t i = 0; i < n; ++i) bytes += grads[i].numel * size_of(grads[i]);
+    uint32_t c = 4096;
+    while (c < 65536 && (uint64_t)c * kGroups < bytes) c *= 2;
+    return c;
+}
+
+// The next batch: as many tensors from `at` on as fit, but those without elements.  Returns where the one after it begins.
+uint32_t next_batch(const wc_grad* grads, uint32_t n, uint32_t at, uint32_t bytes, ClipParams& p) {
+    p.tensors = p.chunks = 0;
+    p.chunk_bytes = bytes;
+    for (; at < n && p.tensors < kBatch; ++at) {
+        const wc_grad& g = grads[at];
+        if (g.numel == 0) continue;
+        const uint64_t chunks = (g.numel * size_of(g) + bytes - 1) / bytes;
+        p.tensor[p.tensors++] = ClipTensor{g.g, g.out, g.numel, p.chunks, g.kind};
+        p.chunks += (uint32_t)chunks;
+    }
+    return at;
+}
+uint32_t groups_of(const ClipParams& p) { return p.chunks < kGroups ? p.chunks : kGroups; }
+
+bool list_fits(const wc_grad* grads, uint32_t n) {
+    if (n > WC_MAX_GRADS || (n && !grads)) return false;
+    for (uint32_t i = 0; i < n; ++i) {
+        const wc_grad& g = grads[i];
+        if (g.kind != WC_OUT_F32 && g.kind != WC_OUT_BF16) return false;
+        if (g.numel > WC_MAX_GRAD_NUMEL) return false;
+        if (g.numel && (!aligned(g.g, size_of(g)) || !aligned(g.out, size_of(g)))) return false;
+    }
+    return true;
+}
+
+}  // namespace
+}  // namespace wc
+
+using namespace wc;
+
+extern "C" int wc_clip_grads_work_bytes(const wc_grad* grads, uint32_t n, uint64_t* work_bytes) {
+    if (!work_bytes || !list_fits(grads, n)) return WC_ERR_INVALID_ARG;
+    const uint32_t bytes = chunk_bytes(grads, n);
+    uint64_t parts = 0;
+    ClipParams p{};
+    for (uint32_t at = 0; at < n;) at = next_batch(grads, n, at, bytes, p), parts += groups_of(p);
+    *work_bytes = parts * sizeof(double);
+    return WC_OK;
+}
+
+extern "C" int wc_clip_grads_async(const wc_grad* grads, uint32_t n, float max_norm, float* norm, void* work_dev,
+                                   uint64_t work_bytes, void* stream) {
+    uint64_t need = 0;
+    const int st = wc_clip_grads_work_bytes(grads, n, &need);
+    if (st != WC_OK) return st;
+    if (!(max_norm >= 0.0f) || !aligned(norm, 4) || (need && (!aligned(work_dev, 256) || work_bytes < need)))
+        return WC_ERR_INVALID_ARG;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const uint32_t bytes = chunk_bytes(grads, n);
+    ClipParams p{};
+    p.part = static_cast<double*>(work_dev);
+    p.max_norm = max_norm;
+    for (uint32_t at = 0; at < n;) {
+        at = next_batch(grads, n, at, bytes, p);
+        if (p.chunks == 0) continue;
+        hipLaunchKernelGGL(clip_norm_kernel, dim3(groups_of(p)), dim3(kThreads), 0, s, p);
+        p.part_at += groups_of(p);
+    }
+    p.parts = p.part_at;
+    p.norm = norm;
+    uint32_t at = 0;
+    do {   // a list without elements: its norm alone, 0
+        at = next_batch(grads, n, at, bytes, p);
+        if (p.chunks == 0 && !p.norm) continue;
+        hipLaunchKernelGGL(clip_scale_kernel, dim3(p.chunks ? groups_of(p) : 1), dim3(kThreads), 0, s, p);
+        p.norm = nullptr;
+    } while (at < n);
+    return hipGetLastError() == hipSuccess ? WC_OK : WC_ERR_HIP;
+}

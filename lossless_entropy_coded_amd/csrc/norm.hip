@@ -1,0 +1,352 @@
+// norm.hip -- root-mean-square norm with the residual's addition, into bf16 or
+// e4m3 codes with scales, and its gradient.
+//
+//   h = bf16(x + residual), or x;   r[t] = 1 / sqrt(mean_c h[t][c]^2 + eps);
+//   y[t][c] = h[t][c] r[t] w[c];
+//   with u = h r (the unit row) and g = w dy:
+//   dh[t][c] = dsum[t][c] + r[t] (g[t][c] - u[t][c] mean_c(g[t][c] u[t][c])),
+//   dw[c]    = sum_t dy[t][c] u[t][c].
+//
+// The norm is taken of the sum as it is stored, in bf16, so that the gradient,
+// which reads it again, is that of what was computed.  y goes to its codes
+// without being rounded to bf16 first.
+//
+// Both kernels read each input once and are bound by memory.  A row is held in
+// registers (8 columns per lane and round), by one wave where rows are short
+// enough (then nothing waits for other waves), else by a workgroup.  The
+// gradient's waves take many rows each, sum dw over them in registers and leave
+// one partial row per workgroup; a second kernel adds those in order, so that
+// results are the same bits on every run.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/wc.h"
+#include "e4m3.h"
+
+namespace wc {
+namespace {
+
+constexpr uint32_t kMaxWaves = 16;
+
+struct NormParams {
+    const uint16_t* x;
+    const uint16_t* residual;
+    const uint16_t* weight;
+    uint16_t* sum;
+    uint16_t* y;
+    uint8_t* codes;
+    float* scales;
+    float* rstd;
+    uint32_t n, dim, blocks;
+    float eps, inv_dim;
+};
+
+// The sum over a row that blockDim.x threads hold: one wave, or a workgroup of
+// one row.  `sums` is LDS of kMaxWaves floats, free for the next call after one
+// more barrier.
+__device__ __forceinline__ float row_sum(float v, float* sums) {
+    v = wave_sum(v);
+    const uint32_t waves = blockDim.x >> 6;
+    if (waves == 1) return v;
+    if ((threadIdx.x & 63u) == 0) sums[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = sums[0];
+    for (uint32_t k = 1; k < waves; ++k) v += sums[k];
+    return v;
+}
+
+__device__ __forceinline__ u32x4 load8(const uint16_t* row, uint32_t c, uint32_t dim) {
+    return c < dim ? *reinterpret_cast<const u32x4*>(row + c) : u32x4{0, 0, 0, 0};
+}
+
+// blockDim.x threads hold a row, 8 columns each in kRounds rounds; blockDim.y rows (one, unless a row is one wave).
+template <uint32_t kRounds, bool kCodes>
+__global__ __launch_bounds__(64 * kMaxWaves) void rms_norm_kernel(NormParams p) {
+    __shared__ float sums[kMaxWaves];
+    const uint32_t row = __builtin_amdgcn_readfirstlane(blockIdx.x * blockDim.y + threadIdx.y);
+    if (row >= p.n) return;   // whole waves, and none where waves wait for each other
+    const uint64_t first = (uint64_t)row * p.dim;
+    u32x4 h[kRounds], w[kRounds];
+#pragma unroll
+    for (uint32_t k = 0; k < kRounds; ++k) {
+        const uint32_t c = (k * blockDim.x + threadIdx.x) * 8;
+        h[k] = load8(p.x + first, c, p.dim);
+    }
+    if (p.residual) {
+        u32x4 r[kRounds];
+#pragma unroll
+        for (uint32_t k = 0; k < kRounds; ++k) {
+            const uint32_t c = (k * blockDim.x + threadIdx.x) * 8;
+            r[k] = load8(p.residual + first, c, p.dim);
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < kRounds; ++k) {
+            const uint32_t c = (k * blockDim.x + threadIdx.x) * 8;
+            float a[8], b[8];
+            unpack_bf16(h[k], a);
+            unpack_bf16(r[k], b);
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i) a[i] += b[i];
+            h[k] = pack_bf16(a);
+            if (c < p.dim) *reinterpret_cast<u32x4*>(p.sum + first + c) = h[k];
+        }
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < kRounds; ++k) w[k] = load8(p.weight, (k * blockDim.x + threadIdx.x) * 8, p.dim);
+    float squares = 0.0f;
+#pragma unroll
+    for (uint32_t k = 0; k < kRounds; ++k) {
+        float a[8];
+        unpack_bf16(h[k], a);
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) squares = __builtin_fmaf(a[i], a[i], squares);
+    }
+    const float rstd = 1.0f / sqrtf(__builtin_fmaf(row_sum(squares, sums), p.inv_dim, p.eps));
+    if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
+#pragma unroll
+    for (uint32_t k = 0; k < kRounds; ++k) {
+        const uint32_t c = (k * blockDim.x + threadIdx.x) * 8;
+        float y[8], g[8];
+        unpack_bf16(h[k], y);
+        unpack_bf16(w[k], g);
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) y[i] = y[i] * rstd * g[i];
+        if (p.y && c < p.dim) *reinterpret_cast<u32x4*>(p.y + first + c) = pack_bf16(y);
+        if (kCodes) {
+            const BlockCodes q = block_codes(y);
+            if (c < p.dim) {
+                *reinterpret_cast<u32x2*>(p.codes + first + c) = q.codes;
+                if (threadIdx.x % kBlockLanes == 0) p.scales[(uint64_t)row * p.blocks + c / kBlockCols] = q.scale;
+            }
+        }
+    }
+}
+
+struct NormGradParams {
+    const uint16_t* dy;
+    const uint16_t* h;
+    const uint16_t* weight;
+    const float* rstd;
+    const uint16_t* dsum;
+    uint16_t* dh;
+    float* part;               // per workgroup, its sum of dy u
+    uint32_t n, dim, teams;    // teams: rows in work at a time
+    float inv_dim;
+};
+
+// A team (the threads that hold a row) takes rows team, team + teams, ...
+template <uint32_t kRounds, uint32_t kMost>
+__global__ __launch_bounds__(64 * kMost) void rms_norm_grad_kernel(NormGradParams p) {
+    extern __shared__ __align__(16) float lds[];   // dw of one team; blockDim.y > 1 only
+    __shared__ float sums[2][kMaxWaves];
+    const uint32_t team = __builtin_amdgcn_readfirstlane(blockIdx.x * blockDim.y + threadIdx.y);
+    u32x4 w[kRounds];
+    float dw[kRounds][8];
+#pragma unroll
+    for (uint32_t k = 0; k < kRounds; ++k) {
+        w[k] = load8(p.weight, (k * blockDim.x + threadIdx.x) * 8, p.dim);
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) dw[k][i] = 0.0f;
+    }
+    uint32_t turn = 0;
+    for (uint32_t row = team; row < p.n; row += p.teams, turn ^= 1) {
+        const uint64_t first = (uint64_t)row * p.dim;
+        u32x4 dy[kRounds], h[kRounds], add[kRounds];
+#pragma unroll
+        for (uint32_t k = 0; k < kRounds; ++k) {
+            const uint32_t c = (k * blockDim.x + threadIdx.x) * 8;
+            dy[k] = load8(p.dy + first, c, p.dim);
+            h[k] = load8(p.h + first, c, p.dim);
+            add[k] = p.dsum ? load8(p.dsum + first, c, p.dim) : u32x4{0, 0, 0, 0};
+        }
+        const float rstd = p.rstd[row];
+        float along = 0.0f;
+#pragma unroll
+        for (uint32_t k = 0; k < kRounds; ++k) {
+            float d[8], u[8], g[8];
+            unpack_bf16(dy[k], d);
+            unpack_bf16(h[k], u);
+            unpack_bf16(w[k], g);
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i) {
+                const float du = d[i] * (u[i] * rstd);
+                dw[k][i] += du;
+                along = __builtin_fmaf(du, g[i], along);
+            }
+        }
+        if (!p.dh) continue;
+        along = row_sum(along, sums[turn]) * p.inv_dim;
+#pragma unroll
+        for (uint32_t k = 0; k < kRounds; ++k) {
+            const uint32_t c = (k * blockDim.x + threadIdx.x) * 8;
+            float d[8], u[8], g[8], out[8];
+            unpack_bf16(dy[k], d);
+            unpack_bf16(h[k], u);
+            unpack_bf16(w[k], g);
+            unpack_bf16(add[k], out);
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i)
+                out[i] = __builtin_fmaf(rstd, __builtin_fmaf(-along, u[i] * rstd, d[i] * g[i]), out[i]);
+            if (c < p.dim) *reinterpret_cast<u32x4*>(p.dh + first + c) = pack_bf16(out);
+        }
+    }
+    if (!p.part) return;
+    for (uint32_t y = 1; y < blockDim.y; ++y) {   // the workgroup's teams in order
+        if (threadIdx.y == y)
+#pragma unroll
+            for (uint32_t k = 0; k < kRounds; ++k)
+#pragma unroll
+                for (uint32_t i = 0; i < 2; ++i)
+                    *reinterpret_cast<f32x4*>(lds + ((k * 2 + i) * 64 + threadIdx.x) * 4) =
+                        f32x4{dw[k][4 * i], dw[k][4 * i + 1], dw[k][4 * i + 2], dw[k][4 * i + 3]};
+        __syncthreads();
+        if (threadIdx.y == 0)
+#pragma unroll
+            for (uint32_t k = 0; k < kRounds; ++k)
+#pragma unroll
+                for (uint32_t i = 0; i < 2; ++i) {
+                    const f32x4 v = *reinterpret_cast<const f32x4*>(lds + ((k * 2 + i) * 64 + threadIdx.x) * 4);
+#pragma unroll
+                    for (uint32_t e = 0; e < 4; ++e) dw[k][4 * i + e] += v[e];
+                }
+        __syncthreads();
+    }
+    if (threadIdx.y != 0) return;
+    float* const part = p.part + (uint64_t)blockIdx.x * p.dim;
+#pragma unroll
+    for (uint32_t k = 0; k < kRounds; ++k) {
+        const uint32_t c = (k * blockDim.x + threadIdx.x) * 8;
+        if (c >= p.dim) continue;
+        *reinterpret_cast<f32x4*>(part + c) = f32x4{dw[k][0], dw[k][1], dw[k][2], dw[k][3]};
+        *reinterpret_cast<f32x4*>(part + c + 4) = f32x4{dw[k][4], dw[k][5], dw[k][6], dw[k][7]};
+    }
+}
+
+constexpr uint32_t kJoinLanes = 8, kJoinSlices = 32;   // 4 columns per lane
+
+// dw: the partial rows of each slice in order, then the slices in order.
+__global__ __launch_bounds__(kJoinLanes * kJoinSlices) void rms_norm_join_kernel(const float* part, uint32_t parts,
+                                                                               uint32_t dim, float* dw,
+                                                                               int accumulate) {
+    __shared__ f32x4 shared[kJoinLanes * kJoinSlices];
+    const uint32_t lane = threadIdx.x % kJoinLanes, slice = threadIdx.x / kJoinLanes;
+    const uint32_t c = (blockIdx.x * kJoinLanes + lane) * 4;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    const uint32_t per = (parts + kJoinSlices - 1) / kJoinSlices, begin = slice * per;
+    const uint32_t end = begin + per < parts ? begin + per : parts;
+    if (c < dim)
+        for (uint32_t k = begin; k < end; ++k) v += *reinterpret_cast<const f32x4*>(part + (uint64_t)k * dim + c);
+    shared[threadIdx.x] = v;
+    __syncthreads();
+    if (slice != 0 || c >= dim) return;
+    for (uint32_t k = 1; k < kJoinSlices; ++k) v += shared[k * kJoinLanes + lane];
+#pragma unroll
+    for (uint32_t e = 0; e < 4; ++e) dw[c + e] = accumulate ? dw[c + e] + v[e] : v[e];
+}
+
+uint32_t cdiv(uint64_t a, uint32_t b) { return (uint32_t)((a + b - 1) / b); }
+
+// How a row is held: by `waves` waves in 1, 2, 4 or 8 rounds.
+struct RowShape {
+    uint32_t waves, rounds, rows;   // rows per workgroup: 4 where a row is one wave
+};
+RowShape row_shape(uint32_t dim) {
+    const uint32_t lanes = cdiv(dim, 8);
+    RowShape s{};
+    s.waves = 1;
+    while (s.waves * 64 * 8 < lanes) s.waves *= 2;
+    s.rounds = 1;
+    while (s.waves * 64 * s.rounds < lanes) s.rounds *= 2;
+    s.rows = s.waves == 1 ? 4 : 1;
+    return s;
+}
+
+constexpr uint32_t kGradGroups = 512;
+uint32_t grad_groups(uint64_t n, const RowShape& s) {
+    const uint32_t groups = cdiv(n, s.rows);
+    return groups < kGradGroups ? groups : kGradGroups;
+}
+
+bool sizes_fit(uint64_t n, uint32_t dim) {
+    return n <= WC_MAX_TOKENS && dim != 0 && dim % 8 == 0 && dim <= WC_MAX_DIM;
+}
+
+template <uint32_t kRounds>
+void launch_norm(const NormParams& p, const RowShape& r, hipStream_t s) {
+    const dim3 grid(cdiv(p.n, r.rows)), block(64 * r.waves, r.rows);
+    if (p.codes) hipLaunchKernelGGL((rms_norm_kernel<kRounds, true>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((rms_norm_kernel<kRounds, false>), grid, block, 0, s, p);
+}
+
+template <uint32_t kRounds>
+void launch_grad(const NormGradParams& p, const RowShape& r, uint32_t groups, hipStream_t s) {
+    const uint32_t bytes = r.rows > 1 ? kRounds * 64 * 8 * 4 : 0;
+    const dim3 grid(groups), block(64 * r.waves, r.rows);
+    if (r.waves <= 4) hipLaunchKernelGGL((rms_norm_grad_kernel<kRounds, 4>), grid, block, bytes, s, p);
+    else hipLaunchKernelGGL((rms_norm_grad_kernel<kRounds, kMaxWaves>), grid, block, bytes, s, p);
+}
+
+}  // namespace
+}  // namespace wc
+
+using namespace wc;
+
+extern "C" int wc_rms_norm_async(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, uint64_t n,
+                                 uint32_t dim, float eps, uint16_t* sum, uint16_t* y, uint8_t* codes, float* scales,
+                                 float* rstd, void* stream) {
+    if (!sizes_fit(n, dim) || !(eps >= 0.0f)) return WC_ERR_INVALID_ARG;
+    if (n == 0) return WC_OK;
+    if ((!y && !codes) || (codes != nullptr) != (scales != nullptr) || (residual != nullptr) != (sum != nullptr))
+        return WC_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(weight, 16) || !aligned_or_null(residual, 16) || !aligned_or_null(sum, 16) ||
+        !aligned_or_null(y, 16) || !aligned_or_null(codes, 16) || !aligned_or_null(scales, 4) ||
+        !aligned_or_null(rstd, 4))
+        return WC_ERR_INVALID_ARG;
+    NormParams p{};
+    p.x = x, p.residual = residual, p.weight = weight, p.sum = sum, p.y = y, p.codes = codes, p.scales = scales;
+    p.rstd = rstd, p.n = (uint32_t)n, p.dim = dim, p.blocks = cdiv(dim, kBlockCols), p.eps = eps;
+    p.inv_dim = 1.0f / (float)dim;
+    const RowShape r = row_shape(dim);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (r.rounds == 1) launch_norm<1>(p, r, s);
+    else if (r.rounds == 2) launch_norm<2>(p, r, s);
+    else if (r.rounds == 4) launch_norm<4>(p, r, s);
+    else launch_norm<8>(p, r, s);
+    return hipGetLastError() == hipSuccess ? WC_OK : WC_ERR_HIP;
+}
+
+extern "C" int wc_rms_norm_grad_work_bytes(uint64_t n, uint32_t dim, uint64_t* work_bytes) {
+    if (!work_bytes || !sizes_fit(n, dim)) return WC_ERR_INVALID_ARG;
+    *work_bytes = (uint64_t)grad_groups(n, row_shape(dim)) * dim * 4;
+    return WC_OK;
+}
+
+extern "C" int wc_rms_norm_grad_async(const uint16_t* dy, const uint16_t* h, const uint16_t* weight,
+                                      const float* rstd, const uint16_t* dsum, uint64_t n, uint32_t dim, uint16_t* dh,
+                                      float* dweight, int accumulate, void* work_dev, uint64_t work_bytes,
+                                      void* stream) {
+    if (!sizes_fit(n, dim) || (n != 0 && !dh && !dweight) || !aligned_or_null(dweight, 4)) return WC_ERR_INVALID_ARG;
+    if (n == 0 && (!dweight || accumulate)) return WC_OK;
+    const RowShape r = row_shape(dim);
+    const uint32_t groups = grad_groups(n, r);
+    if (n != 0 && (!aligned(dy, 16) || !aligned(h, 16) || !aligned(weight, 16) || !aligned(rstd, 4) ||
+                   !aligned_or_null(dsum, 16) || !aligned_or_null(dh, 16) ||
+                   (dweight && (!aligned(work_dev, 256) || work_bytes < (uint64_t)groups * dim * 4))))
+        return WC_ERR_INVALID_ARG;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    NormGradParams p{};
+    if (n != 0) {
+        p.dy = dy, p.h = h, p.weight = weight, p.rstd = rstd, p.dsum = dsum, p.dh = dh;
+        p.part = dweight ? static_cast<float*>(work_dev) : nullptr;
+        p.n = (uint32_t)n, p.dim = dim, p.teams = groups * r.rows, p.inv_dim = 1.0f / (float)dim;
+        if (r.rounds == 1) launch_grad<1>(p, r, groups, s);
+        else if (r.rounds == 2) launch_grad<2>(p, r, groups, s);
+        else if (r.rounds == 4) launch_grad<4>(p, r, groups, s);
+        else launch_grad<8>(p, r, groups, s);
+    }
+    if (dweight)   // of no tokens: zeros
+        hipLaunchKernelGGL(rms_norm_join_kernel, dim3(cdiv(dim, kJoinLanes * 4)), dim3(kJoinLanes * kJoinSlices), 0, s,
+                           p.part, n ? groups : 0, dim, dweight, accumulate);
+    return hipGetLastError() == hipSuccess ? WC_OK : WC_ERR_HIP;
+}

@@ -93,6 +93,16 @@ class _Q4(ctypes.Structure):
                 ("rows", ctypes.c_uint32), ("cols", ctypes.c_uint32), ("group", ctypes.c_uint32)]
 
 
+class _Fp8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_uint32),
+                ("cols", ctypes.c_uint32)]
+
+
+class _Grad(ctypes.Structure):
+    _fields_ = [("g", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_uint64),
+                ("kind", ctypes.c_uint32)]
+
+
 _void_p, _u32, _u64, _int, _float = (ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int, ctypes.c_float)
 for _name, _args in {
         "wc_q4_check": [_void_p],
@@ -106,7 +116,18 @@ for _name, _args in {
         "wc_ce_loss_async": [_void_p, _void_p, _void_p, _u32, _u64, _u32, _u32, _void_p, _void_p, _void_p, _u64,
                              _void_p],
         "wc_ce_grad_async": [_void_p, _void_p, _void_p, _u32, _u64, _u32, _u32, _void_p, _void_p, _void_p, _void_p,
-                             _void_p, _u64, _void_p]}.items():
+                             _void_p, _u64, _void_p],
+        "wc_quant_fp8_async": [_void_p, _u64, _u32, _int, _void_p, _void_p, _void_p],
+        "wc_rms_norm_async": [_void_p, _void_p, _void_p, _u64, _u32, _float, _void_p, _void_p, _void_p, _void_p, _void_p,
+                              _void_p],
+        "wc_rms_norm_grad_work_bytes": [_u64, _u32, _u64p],
+        "wc_rms_norm_grad_async": [_void_p, _void_p, _void_p, _void_p, _void_p, _u64, _u32, _void_p, _void_p, _int,
+                                   _void_p, _u64, _void_p],
+        "wc_fp8_check": [_void_p],
+        "wc_gemm_fp8_work_bytes": [_void_p, _u64, _u64p],
+        "wc_gemm_fp8_async": [_void_p, _void_p, _void_p, _u64, _void_p, _u32, _void_p, _u64, _void_p],
+        "wc_clip_grads_work_bytes": [_void_p, _u32, _u64p],
+        "wc_clip_grads_async": [_void_p, _u32, _float, _void_p, _void_p, _u64, _void_p]}.items():
     getattr(_lib, _name).argtypes = _args
     getattr(_lib, _name).restype = ctypes.c_int
 _lib.wc_stream_reference_async.argtypes = [ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_uint64,
@@ -164,6 +185,9 @@ EXPORTED = ("wc_encode_host", "wc_encode_u8_host", "wc_free_host", "wc_plan", "w
             "wc_decode_gemv_noalloc_async", "wc_stream_reference_async", "wc_plan_debug_status",
             "wc_q4_check", "wc_gemv_q4_async", "wc_embed_async", "wc_embed_q4_async", "wc_embed_grad_work_bytes",
             "wc_embed_grad_async", "wc_ce_work_bytes", "wc_ce_loss_async", "wc_ce_grad_async",
+            "wc_quant_fp8_async", "wc_rms_norm_async", "wc_rms_norm_grad_work_bytes", "wc_rms_norm_grad_async",
+            "wc_fp8_check", "wc_gemm_fp8_work_bytes", "wc_gemm_fp8_async", "wc_clip_grads_work_bytes",
+            "wc_clip_grads_async",
             "wc_plan_destroy", "wc_status_str")
 
 
@@ -699,6 +723,192 @@ def ce_grad_async(h_dev, W_dev, targets_dev, tokens: int, vocab: int, dim: int, 
     work, work_bytes = _workspace(work_dev, work_bytes, dev, call)
     _check(_lib.wc_ce_grad_async(h, W, targets, width, tokens, vocab, dim, lse, dloss, dh, dW, work, work_bytes,
                                  _stream_handle(stream)), call)
+
+
+# ---- 8-bit floating point, norms and gradients -------------------------------------
+
+FP8_BLOCK = 128   # columns (and rows of a matrix) that share a scale
+MAX_GRADS = 1 << 20
+MAX_GRAD_NUMEL = 1 << 38
+_CODE_KIND = "float8_e4m3fn"
+
+
+def quant_fp8_async(x_dev, n: int, dim: int, codes_dev, scales_dev, gated: bool = False, stream=None) -> None:
+    """wc_quant_fp8_async: rows of bf16 activations (gated: silu(gate) * up of rows gate, up) to e4m3 codes with an
+    fp32 scale per FP8_BLOCK columns; one launch.
+
+    x_dev: n x dim bf16 (gated: n x 2 dim); codes_dev: n x dim float8_e4m3fn (or bytes); scales_dev: n x
+    ceil(dim / FP8_BLOCK) float32."""
+    call = "wc_quant_fp8_async"
+    dev = _current_device()
+    if (n | dim) >> 32:
+        _sizes(call, n=n, dim=dim)
+    gated = bool(gated)
+    x = _bytes_ok(x_dev, (4 if gated else 2) * n * dim, dev, "x", call, "bf16")
+    codes = _bytes_ok(codes_dev, n * dim, dev, "codes", call, _CODE_KIND)
+    scales = _bytes_ok(scales_dev, 4 * n * -(-dim // FP8_BLOCK), dev, "scales", call, "f32")
+    _check(_lib.wc_quant_fp8_async(x, n, dim, gated, codes, scales, _stream_handle(stream)), call)
+
+
+def rms_norm_async(x_dev, weight_dev, n: int, dim: int, eps: float, y_dev=None, codes_dev=None, scales_dev=None,
+                   residual_dev=None, sum_dev=None, rstd_dev=None, stream=None) -> None:
+    """wc_rms_norm_async: y = h * rstd * weight, rstd = 1 / sqrt(mean(h^2) + eps), of h = x or h = bf16(x + residual),
+    which goes to sum_dev; one launch.
+
+    y goes to y_dev (bf16), to codes_dev and scales_dev (as quant_fp8_async writes them), or to both; rstd_dev (n
+    float32), if given, keeps rstd for the gradient."""
+    call = "wc_rms_norm_async"
+    dev = _current_device()
+    if (n | dim) >> 32:
+        _sizes(call, n=n, dim=dim)
+    wide = 2 * n * dim
+    x = _bytes_ok(x_dev, wide, dev, "x", call, "bf16")
+    weight = _bytes_ok(weight_dev, 2 * dim, dev, "weight", call, "bf16")
+    residual = _bytes_ok(residual_dev, wide, dev, "residual", call, "bf16") if residual_dev is not None else 0
+    total = _bytes_ok(sum_dev, wide, dev, "sum", call, "bf16") if sum_dev is not None else 0
+    y = _bytes_ok(y_dev, wide, dev, "y", call, "bf16") if y_dev is not None else 0
+    codes = _bytes_ok(codes_dev, n * dim, dev, "codes", call, _CODE_KIND) if codes_dev is not None else 0
+    scales = (_bytes_ok(scales_dev, 4 * n * -(-dim // FP8_BLOCK), dev, "scales", call, "f32")
+              if scales_dev is not None else 0)
+    rstd = _bytes_ok(rstd_dev, 4 * n, dev, "rstd", call, "f32") if rstd_dev is not None else 0
+    _check(_lib.wc_rms_norm_async(x, residual, weight, n, dim, eps, total, y, codes, scales, rstd,
+                                  _stream_handle(stream)), call)
+
+
+def rms_norm_grad_work_bytes(n: int, dim: int) -> int:
+    """wc_rms_norm_grad_work_bytes: device scratch of rms_norm_grad_async for n tokens."""
+    _sizes("wc_rms_norm_grad_work_bytes", n=n, dim=dim)
+    b = ctypes.c_uint64(0)
+    _check(_lib.wc_rms_norm_grad_work_bytes(n, dim, ctypes.byref(b)), "wc_rms_norm_grad_work_bytes")
+    return b.value
+
+
+def rms_norm_grad_async(dy_dev, h_dev, weight_dev, rstd_dev, n: int, dim: int, dh_dev, dweight_dev, work_dev,
+                        work_bytes: int, dsum_dev=None, accumulate: bool = False, stream=None) -> None:
+    """wc_rms_norm_grad_async: dh (bf16, of x and the residual alike) and dweight (float32) of rms_norm_async's y; either
+    may be None.
+
+    h_dev: what rms_norm_async wrote to sum_dev (x without a residual); dsum_dev: the gradient that h has from where
+    else it goes, or None.  accumulate: add to dweight instead of writing it."""
+    call = "wc_rms_norm_grad_async"
+    dev = _current_device()
+    if (n | dim) >> 32:
+        _sizes(call, n=n, dim=dim)
+    wide = 2 * n * dim
+    dy = _bytes_ok(dy_dev, wide, dev, "dy", call, "bf16")
+    h = _bytes_ok(h_dev, wide, dev, "h", call, "bf16")
+    weight = _bytes_ok(weight_dev, 2 * dim, dev, "weight", call, "bf16")
+    rstd = _bytes_ok(rstd_dev, 4 * n, dev, "rstd", call, "f32")
+    dsum = _bytes_ok(dsum_dev, wide, dev, "dsum", call, "bf16") if dsum_dev is not None else 0
+    dh = _bytes_ok(dh_dev, wide, dev, "dh", call, "bf16") if dh_dev is not None else 0
+    dweight = _bytes_ok(dweight_dev, 4 * dim, dev, "dweight", call, "f32") if dweight_dev is not None else 0
+    work, work_bytes = _scratch(work_dev, work_bytes, dev, call)
+    _check(_lib.wc_rms_norm_grad_async(dy, h, weight, rstd, dsum, n, dim, dh, dweight, bool(accumulate), work,
+                                       work_bytes, _stream_handle(stream)), call)
+
+
+def _scratch(work_dev, work_bytes: int, device, call: str):
+    """_workspace of a call that may need none: (0, 0) where none is given."""
+    if work_dev is None:
+        if work_bytes:
+            raise WCError(WC_ERR_INVALID_ARG, call, f"work is None, work_bytes {work_bytes}")
+        return 0, 0
+    return _workspace(work_dev, work_bytes, device, call)
+
+
+class Fp8Matrix:
+    """A wc_fp8_matrix over device tensors (kept alive by this handle): rows x cols e4m3 codes (float8_e4m3fn, or bytes as
+    decode_u8_async leaves a plane of them) and a float32 scale per block of FP8_BLOCK x FP8_BLOCK."""
+
+    def __init__(self, codes, scales, rows: int, cols: int):
+        call = "wc_fp8_check"
+        _sizes(call, rows=rows, cols=cols)
+        self.rows, self.cols = int(rows), int(cols)
+        self._tensors = (codes, scales)
+        self.device = _current_device()
+        c = _bytes_ok(codes, self.rows * self.cols, self.device, "codes", call, _CODE_KIND)
+        s = _bytes_ok(scales, 4 * -(-self.rows // FP8_BLOCK) * -(-self.cols // FP8_BLOCK), self.device, "scales", call,
+                      "f32")
+        self._struct = _Fp8(c, s, self.rows, self.cols)
+        self._ref = ctypes.addressof(self._struct)
+        _check(_lib.wc_fp8_check(self._ref), call)
+
+
+def gemm_fp8_work_bytes(W: Fp8Matrix, tokens: int) -> int:
+    """wc_gemm_fp8_work_bytes: device scratch of gemm_fp8_async for this many tokens."""
+    _sizes("wc_gemm_fp8_work_bytes", tokens=tokens)
+    b = ctypes.c_uint64(0)
+    _check(_lib.wc_gemm_fp8_work_bytes(W._ref, tokens, ctypes.byref(b)), "wc_gemm_fp8_work_bytes")
+    return b.value
+
+
+def gemm_fp8_async(W: Fp8Matrix, x_codes_dev, x_scales_dev, tokens: int, y_dev, work_dev, work_bytes: int,
+                   out: str = "bf16", stream=None) -> None:
+    """wc_gemm_fp8_async: y[t] = W x[t] for e4m3 activations with a float32 scale per token and FP8_BLOCK columns.
+
+    x_codes_dev, x_scales_dev: as quant_fp8_async or rms_norm_async writes them; y_dev: tokens x W.rows of `out` ("f32"
+    or "bf16"); work_dev may be None where gemm_fp8_work_bytes is 0."""
+    call = "wc_gemm_fp8_async"
+    dev = _on_device(W, call)
+    if tokens >> 32:
+        _sizes(call, tokens=tokens)
+    if out not in OUT_KINDS:
+        raise WCError(WC_ERR_INVALID_ARG, call, f"out is {out!r}, not one of {sorted(OUT_KINDS)}")
+    x = _bytes_ok(x_codes_dev, tokens * W.cols, dev, "x_codes", call, _CODE_KIND)
+    xs = _bytes_ok(x_scales_dev, 4 * tokens * -(-W.cols // FP8_BLOCK), dev, "x_scales", call, "f32")
+    y = _bytes_ok(y_dev, (4 if out == "f32" else 2) * tokens * W.rows, dev, "y", call, out)
+    work, work_bytes = _scratch(work_dev, work_bytes, dev, call)
+    _check(_lib.wc_gemm_fp8_async(W._ref, x, xs, tokens, y, OUT_KINDS[out], work, work_bytes, _stream_handle(stream)),
+           call)
+
+
+class GradList:
+    """A list of gradients for clip_grads_async (kept alive by this handle): float32 or bf16 device tensors, and where the
+    clipped ones go (outs: tensors of the same sizes and types; None: in place)."""
+
+    def __init__(self, grads, outs=None):
+        call = "wc_clip_grads_async"
+        grads = list(grads)
+        outs = grads if outs is None else list(outs)
+        if len(outs) != len(grads) or len(grads) > MAX_GRADS:
+            raise WCError(WC_ERR_INVALID_ARG, call, f"{len(grads)} gradients and {len(outs)} outputs")
+        self.device = _current_device()
+        self._tensors = (grads, outs)
+        self._array = (_Grad * max(len(grads), 1))()
+        self._n = len(grads)
+        for i, (g, out) in enumerate(zip(grads, outs)):
+            kind = _kind_of(g.dtype)
+            if kind not in OUT_KINDS or _kind_of(out.dtype) != kind:
+                raise WCError(WC_ERR_INVALID_ARG, call, f"gradient {i} is {g.dtype}, its output {out.dtype}")
+            n = g.numel()
+            if out.numel() != n:
+                raise WCError(WC_ERR_INVALID_ARG, call, f"gradient {i} has {n} elements, its output {out.numel()}")
+            size = (4 if kind == "f32" else 2) * n
+            self._array[i] = _Grad(_bytes_ok(g, size, self.device, f"gradient {i}", call),
+                                   _bytes_ok(out, size, self.device, f"output {i}", call), n, OUT_KINDS[kind])
+
+
+def clip_grads_work_bytes(grads: GradList) -> int:
+    """wc_clip_grads_work_bytes: device scratch of clip_grads_async for this list."""
+    b = ctypes.c_uint64(0)
+    _check(_lib.wc_clip_grads_work_bytes(ctypes.addressof(grads._array), grads._n, ctypes.byref(b)),
+           "wc_clip_grads_work_bytes")
+    return b.value
+
+
+def clip_grads_async(grads: GradList, max_norm: float, norm_dev, work_dev, work_bytes: int, stream=None) -> None:
+    """wc_clip_grads_async: norm = sqrt(sum of g^2 over all gradients); out = g * max_norm / norm where the norm is finite
+    and larger than max_norm, else g.
+
+    norm_dev: one float32; max_norm: at least 0 (infinity: the norm alone)."""
+    call = "wc_clip_grads_async"
+    dev = _current_device()
+    if grads.device != dev:
+        raise WCError(WC_ERR_INVALID_ARG, call, f"the gradients are on cuda:{grads.device}, not on cuda:{dev}")
+    norm = _bytes_ok(norm_dev, 4, dev, "norm", call, "f32")
+    work, work_bytes = _scratch(work_dev, work_bytes, dev, call)
+    _check(_lib.wc_clip_grads_async(ctypes.addressof(grads._array), grads._n, max_norm, norm, work, work_bytes,
+                                    _stream_handle(stream)), call)
 
 
 def exported_symbols():

@@ -1,0 +1,185 @@
+"""GPU tests of products with matrices of e4m3 codes that have scales per block of 128."""
+import pytest
+import torch
+
+from e4m3_ref import BLOCK, blocks, gemm_tolerance, matrix_codes, per_column, quantised, values_of, within
+from gpu_util import log
+
+pytestmark = pytest.mark.gpu
+BF16, F8 = torch.bfloat16, torch.float8_e4m3fn
+GUARD = 64
+
+
+@pytest.fixture(scope="module")
+def wc():
+    assert torch.cuda.is_available(), "GPU tests need a visible MI355X"
+    from lossless_entropy_coded_amd import wc as mod
+    return mod
+
+
+def _case(rows, cols, tokens, seed):
+    """(codes, scales, the matrix; codes, scales, the activations), the matrices they stand for in 64 bits."""
+    g = torch.Generator().manual_seed(seed)
+    w = torch.randn(rows, cols, generator=g) * torch.exp2(torch.randint(-3, 4, (rows, 1), generator=g).float())
+    codes, scales, w = matrix_codes(w)
+    x = torch.randn(tokens, cols, generator=g) * torch.exp2(torch.randint(-6, 7, (tokens, 1), generator=g).float())
+    x[:, ::61] *= 20
+    xc, xs = quantised(x)
+    return codes, scales, w, xc, xs, values_of(xc) * per_column(xs, cols)
+
+
+def _run(wc, W, xc, xs, tokens, out, **kw):
+    n = tokens * W.rows
+    y = torch.full((n + GUARD,), -7.0, dtype=BF16 if out == "bf16" else torch.float32, device="cuda")
+    need = wc.gemm_fp8_work_bytes(W, tokens)
+    work = torch.full((need + GUARD,), 0xFF, dtype=torch.uint8, device="cuda")   # NaN wherever it is read unwritten
+    wc.gemm_fp8_async(W, xc, xs, tokens, y, work if need else None, need, out=out, **kw)
+    torch.cuda.synchronize()
+    assert bool((y[n:] == -7.0).all()) and bool((work[need:] == 0xFF).all()), "wrote past the end"
+    return y[:n].reshape(tokens, W.rows)
+
+
+SHAPES = [(1, 16, 1), (3, 32, 2), (16, 128, 1), (17, 144, 3), (128, 128, 16), (129, 256, 17), (100, 1168, 5),
+          (1000, 512, 1), (1024, 4096, 1), (64, 28672, 2), (333, 2096, 40), (1003, 2096, 65), (256, 1024, 128),
+          (257, 640, 129), (515, 384, 300), (2000, 272, 33), (4096, 128, 9), (96, 65536, 3), (1, 4096, 500),
+          (2, 144, 1025), (640, 1536, 700), (1027, 1040, 515), (5000, 256, 2), (9000, 400, 24)]
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols,tokens", SHAPES)
+def test_products(wc, rows, cols, tokens, out):
+    codes, scales, w, xc, xs, x = _case(rows, cols, tokens, rows + cols + tokens)
+    log(f"case: gemm_fp8 {rows}x{cols}, {tokens} tokens, {out}")
+    W = wc.Fp8Matrix(codes.cuda(), scales.cuda(), rows, cols)
+    y = _run(wc, W, xc.cuda(), xs.cuda(), tokens, out)
+    want = x @ w.t()
+    assert within(y, want, gemm_tolerance(x, w, out == "bf16", want))
+    again = _run(wc, W, xc.cuda(), xs.cuda(), tokens, out)
+    assert torch.equal(y, again), "two runs differ"
+
+
+@pytest.mark.parametrize("tokens", list(range(1, 20)) + [31, 32, 33, 47, 48, 49, 63, 64, 65, 127, 128])
+def test_few_tokens(wc, tokens):
+    rows, cols = 272, 1296
+    codes, scales, w, xc, xs, x = _case(rows, cols, tokens, tokens)
+    log(f"case: gemm_fp8 {rows}x{cols}, {tokens} tokens")
+    y = _run(wc, wc.Fp8Matrix(codes.cuda(), scales.cuda(), rows, cols), xc.cuda(), xs.cuda(), tokens, "f32")
+    want = x @ w.t()
+    assert within(y, want, gemm_tolerance(x, w, False, want))
+
+
+@pytest.mark.parametrize("tokens", [1, 24, 200])
+def test_every_code(wc, tokens):
+    """Each of the 254 finite codes times each other: single products are exact in fp32."""
+    cols, rows = 128, 254
+    finite = torch.tensor([c for c in range(256) if c & 127 != 127], dtype=torch.uint8)
+    codes = torch.zeros(rows, cols, dtype=torch.uint8)
+    codes[:, 77] = finite
+    log(f"case: gemm_fp8 every code, {tokens} tokens")
+    W = wc.Fp8Matrix(codes.cuda(), torch.ones(2, 1, device="cuda"), rows, cols)
+    for start in range(0, 254, tokens):
+        mine = finite[start:start + tokens]
+        xc = torch.zeros(len(mine), cols, dtype=torch.uint8)
+        xc[:, 77] = mine
+        y = _run(wc, W, xc.cuda(), torch.ones(len(mine), 1, device="cuda"), len(mine), "f32")
+        assert torch.equal(y.cpu().double(), values_of(mine)[:, None] * values_of(finite)[None, :])
+
+
+@pytest.mark.parametrize("tokens", [1, 20, 150])
+def test_columns_of_blocks(wc, tokens):
+    """Every column reaches the right block's scales: one nonzero column at a time, scales all different."""
+    rows, cols = 300, 400
+    g = torch.Generator().manual_seed(1)
+    scales = torch.exp2(torch.randint(-8, 8, (3, 4), generator=g).float())
+    xs = torch.exp2(torch.randint(-8, 8, (tokens, 4), generator=g).float())
+    log(f"case: gemm_fp8 columns one by one, {tokens} tokens")
+    for c in (0, 15, 16, 63, 64, 127, 128, 255, 256, 383, 384, 399):
+        codes, xc = torch.zeros(rows, cols, dtype=torch.uint8), torch.zeros(tokens, cols, dtype=torch.uint8)
+        codes[:, c] = torch.randint(1, 127, (rows,), generator=g).to(torch.uint8)
+        xc[:, c] = torch.randint(1, 127, (tokens,), generator=g).to(torch.uint8)
+        W = wc.Fp8Matrix(codes.cuda(), scales.cuda(), rows, cols)
+        y = _run(wc, W, xc.cuda(), xs.cuda(), tokens, "f32")
+        want = (values_of(xc[:, c]) * xs.double()[:, c // BLOCK])[:, None] * \
+            (values_of(codes[:, c]) * scales.double()[torch.arange(rows) // BLOCK, c // BLOCK])[None]
+        assert torch.equal(y.cpu().double(), want), c
+
+
+@pytest.mark.parametrize("rows,cols,tokens", [(256, 512, 1), (256, 512, 20), (300, 400, 200)])
+def test_no_numbers_stay_among_themselves(wc, rows, cols, tokens):
+    """A NaN code or scale reaches its own row or token alone, also where tiles reach past the ends."""
+    codes, scales, w, xc, xs, x = _case(rows, cols, tokens, 9)
+    log(f"case: gemm_fp8 NaN, {rows}x{cols}, {tokens} tokens")
+    want = x @ w.t()
+    tol = gemm_tolerance(x, w, False, want)
+    bad = codes.view(torch.uint8).clone()
+    bad[rows - 1, cols - 1] = 0x7F
+    y = _run(wc, wc.Fp8Matrix(bad.cuda(), scales.cuda(), rows, cols), xc.cuda(), xs.cuda(), tokens, "f32")
+    assert bool(torch.isnan(y[:, rows - 1]).all()) and within(y[:, :rows - 1], want[:, :-1], tol[:, :-1])
+    xs[tokens - 1, 0] = float("nan")
+    y = _run(wc, wc.Fp8Matrix(codes.cuda(), scales.cuda(), rows, cols), xc.cuda(), xs.cuda(), tokens, "f32")
+    assert bool(torch.isnan(y[tokens - 1]).all())
+    if tokens > 1:
+        assert within(y[:-1], want[:-1], tol[:-1])
+
+
+def test_views_streams_and_graph(wc):
+    """Operands that lie inside larger tensors whose neighbours are NaN codes, two streams at once, and captured calls
+    that are replayed with other activations."""
+    rows, cols = 520, 1296
+    big = torch.full((rows * cols + 512,), 0x7F, dtype=torch.uint8, device="cuda")
+    for tokens in (1, 7, 150):
+        codes, scales, w, xc, xs, x = _case(rows, cols, tokens, tokens + 3)
+        log(f"case: gemm_fp8 views, streams and graph, {tokens} tokens")
+        view = big[256:256 + rows * cols]
+        view.copy_(codes.view(torch.uint8).flatten())
+        wide = torch.full((tokens * cols + 512,), 0x7F, dtype=torch.uint8, device="cuda")
+        mine = wide[256:256 + tokens * cols]
+        mine.copy_(xc.view(torch.uint8).flatten())
+        xsd = torch.full((tokens * blocks(cols) + 64,), float("nan"), device="cuda")[32:-32]
+        xsd.copy_(xs.flatten())
+        W = wc.Fp8Matrix(view, scales.cuda(), rows, cols)
+        want = x @ w.t()
+        y = _run(wc, W, mine, xsd, tokens, "f32")
+        assert within(y, want, gemm_tolerance(x, w, False, want))
+        need = wc.gemm_fp8_work_bytes(W, tokens)
+        calls = [(torch.cuda.Stream(), torch.empty(tokens, rows, device="cuda"),
+                  torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")) for _ in range(2)]
+        torch.cuda.synchronize()
+        for stream, out, work in calls:
+            wc.gemm_fp8_async(W, mine, xsd, tokens, out, work, need, out="f32", stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, y) for _, out, _ in calls)
+        out, work = calls[0][1:]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            wc.gemm_fp8_async(W, mine, xsd, tokens, out, work, need, out="f32")
+        for seed in range(3):
+            other, others = quantised(torch.randn(tokens, cols, generator=torch.Generator().manual_seed(seed)))
+            mine.copy_(other.view(torch.uint8).flatten())
+            xsd.copy_(others.flatten())
+            eager = _run(wc, W, mine, xsd, tokens, "f32")
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, eager)
+
+
+def test_nothing(wc):
+    e = torch.empty(0, device="cuda")
+    W = wc.Fp8Matrix(torch.zeros(32, 64, dtype=torch.uint8, device="cuda"), torch.ones(1, 1, device="cuda"), 32, 64)
+    assert wc.gemm_fp8_work_bytes(W, 0) == 0
+    wc.gemm_fp8_async(W, e.to(torch.uint8), e, 0, e.to(BF16), None, 0)
+    none = wc.Fp8Matrix(e.to(torch.uint8), e, 0, 64)
+    wc.gemm_fp8_async(none, torch.zeros(5, 64, dtype=torch.uint8, device="cuda"), torch.ones(5, 1, device="cuda"), 5, e,
+                      None, 0, out="f32")
+
+
+@pytest.mark.parametrize("tokens", [1, 40])
+def test_large_scales(wc, tokens):
+    """Scales far from one whose product is in range."""
+    rows, cols = 130, 384
+    codes, scales, w, xc, xs, x = _case(rows, cols, tokens, 4)
+    log(f"case: gemm_fp8 large and small scales, {tokens} tokens")
+    W = wc.Fp8Matrix(codes.cuda(), (scales * 2.0 ** 90).cuda(), rows, cols)
+    y = _run(wc, W, xc.cuda(), (xs * 2.0 ** -90).cuda(), tokens, "f32")
+    want = x @ w.t()
+    assert within(y, want, gemm_tolerance(x, w, False, want))
