@@ -47,37 +47,46 @@ struct GemmParams {
 // of one chunk that a pass of a 16-byte read touches lie in different banks.
 template <uint32_t R, uint32_t kThreads>
 struct Loader {
-    static constexpr uint32_t kLoads = R * 8 / kThreads;
-    static_assert(R * 8 % kThreads == 0 && kThreads / 8 % 16 == 0, "whole rounds, all of the same place in their rows");
-    const uint8_t* base;
-    uint32_t bytes, cols, column;
-    uint32_t off[kLoads];
-    __device__ __forceinline__ Loader(const uint8_t* p, uint32_t cols_, uint32_t row0, uint32_t rows) : cols(cols_) {   // row0 < rows
-        base = p + (uint64_t)row0 * cols;
-        bytes = (rows - row0 < R ? rows - row0 : R) * cols;
+    static constexpr uint32_t kLoads = R * 8 / kThreads, kRows = kThreads / 8;   // rounds, rows of each
+    static_assert(R * 8 % kThreads == 0 && kRows % 16 == 0, "whole rounds, all of the same place in their rows");
+    u32x4 rsrc;
+    uint32_t cols, column, at;
+    __device__ __forceinline__ Loader(const uint8_t* p, uint32_t cols_, uint32_t row0, uint32_t rows) : cols(cols_) {
+        rsrc = buffer_words(p + (uint64_t)row0 * cols, (rows - row0 < R ? rows - row0 : R) * cols);   // row0 < rows
         const uint32_t row = threadIdx.x / 8;
         column = ((threadIdx.x & 7u) ^ (row / 2 & 7u)) * 16;
-#pragma unroll
-        for (uint32_t i = 0; i < kLoads; ++i) off[i] = (row + i * (kThreads / 8)) * cols + column;
+        at = row * cols + column;
     }
-    // Start copying the stage of columns c0 .. c0 + 127 (zeros past the last).
+    // Start copying the stage of columns c0 .. c0 + 127 (zeros past the last): every kEvery-th round from kFirst on.  The uniform part of an offset stays
+    // within the buffer: past its end the range check of a lane's part, which subtracts it, would wrap.
+    template <uint32_t kFirst = 0, uint32_t kEvery = 1>
     __device__ __forceinline__ void start(uint8_t* lds, uint32_t c0) const {
         const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        const u32x4 rsrc = buffer_words(base, bytes);
-        const bool inside = c0 + column < cols;
+        const uint32_t from = c0 + column < cols ? at : kNoChunk;
 #pragma unroll
-        for (uint32_t i = 0; i < kLoads; ++i)
-            copy_to_lds(lds_address(lds) + (i * kThreads + wave * 64u) * 16u, rsrc, inside ? off[i] + c0 : kNoChunk);
+        for (uint32_t i = kFirst; i < kLoads; i += kEvery)
+            copy_to_lds(lds_address(lds) + (i * kThreads + wave * 64u) * 16u, rsrc, from,
+                        min(i * kRows * cols + c0, rsrc[2]));
     }
 };
 
 // Rows x .. x + 15 of a stage: lane l has row x + l % 16, chunks l / 16 and l / 16 + 4.  (Which columns a lane has is
-// of no account as long as both operands agree.)
-__device__ __forceinline__ i32x8 fragment(const uint8_t* lds, uint32_t x) {
-    const uint32_t lane = threadIdx.x & 63u, row = x + (lane & 15u), at = row / 2 & 7u;
-    const u32x4 lo = *reinterpret_cast<const u32x4*>(lds + row * 128 + ((lane >> 4) ^ at) * 16);
-    const u32x4 hi = *reinterpret_cast<const u32x4*>(lds + row * 128 + ((lane >> 4 | 4u) ^ at) * 16);
-    return __builtin_bit_cast(i32x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+// of no account as long as both operands agree.)  Where they stand; 16 rows further on, 2048 bytes further on.
+struct Places {
+    uint32_t lo, hi;
+    __device__ __forceinline__ explicit Places(uint32_t x) {
+        const uint32_t lane = threadIdx.x & 63u, row = x + (lane & 15u), at = row / 2 & 7u;
+        lo = row * 128 + ((lane >> 4) ^ at) * 16;
+        hi = row * 128 + ((lane >> 4 | 4u) ^ at) * 16;
+    }
+};
+__device__ __forceinline__ i32x8 joined(const uint8_t* lo, const uint8_t* hi) {
+    return __builtin_bit_cast(i32x8, __builtin_shufflevector(*reinterpret_cast<const u32x4*>(lo),
+                                                             *reinterpret_cast<const u32x4*>(hi), 0, 1, 2, 3, 4, 5, 6, 7));
+}
+__device__ __forceinline__ i32x8 fragment(const uint8_t* stage, uint32_t x) {
+    const Places at(x);
+    return joined(stage + at.lo, stage + at.hi);
 }
 
 // Eight codes in bf16, exactly.
@@ -120,9 +129,10 @@ struct Tile {
     static constexpr uint32_t kThreads = 64 * kWavesM * kWavesN;
     static constexpr uint32_t kWaveM = kBm / kWavesM, kWaveN = kBn / kWavesN;
     static constexpr uint32_t kMi = kWaveM / 16, kNi = kWaveN / 16;
-    static constexpr uint32_t kCodeBytes = (kBm + kBn) * 128;
-    static constexpr uint32_t kStageBytes = kCodeBytes + kThreads * 4;   // and 64 tokens' scales per wave
-    static constexpr uint32_t kLdsBytes = kStages * kStageBytes;
+    static constexpr bool kAlternate = kThreads == 512;
+    static constexpr uint32_t kCodeBytes = (kBm + kBn) * 128, kScaleBytes = kThreads * 4;   // 64 tokens' scales per wave
+    static constexpr uint32_t kScalesAt = kStages * kCodeBytes;   // of a stage: codes, and behind all stages' codes, scales
+    static constexpr uint32_t kLdsBytes = kScalesAt + kStages * kScaleBytes;
     static_assert(kWaveN <= 64 && kBlockCols % kWaveM == 0 && kLdsBytes <= 160 * 1024, "shape");
 };
 
@@ -166,8 +176,61 @@ __device__ __forceinline__ void store4(void* y, uint32_t kind, uint64_t at, uint
     }
 }
 
+// A tile's results: put together in LDS, which is free (4 neighbours of a token per lane, 16-byte chunks at chunk ^
+// token, so that the 16 tokens that a wave writes at a time lie in different banks), then written as whole rows.  From
+// the registers, 32 bytes of a token at a time, that took 10 % of the time at 8192 tokens x 28672 x 8192.  Rows that do
+// not begin on 16 bytes are written from the registers.
+template <class T, uint32_t kKind>
+__device__ __forceinline__ void store_tile(uint8_t* lds, void* y, const GemmParams& p, uint32_t m0, uint32_t n0,
+                                           const f32x4 (&acc)[T::kMi][T::kNi]) {
+    constexpr uint32_t kSize = kKind == WC_OUT_F32 ? 4 : 2, kRow = T::kBm * kSize, kChunks = kRow / 16;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63u;
+    const uint32_t wm = wave % T::kWavesM * T::kWaveM, wn = wave / T::kWavesM * T::kWaveN;
+    if (p.rows % (16 / kSize) != 0) {
+#pragma unroll
+        for (uint32_t j = 0; j < T::kNi; ++j) {
+            const uint32_t t = n0 + wn + j * 16 + (lane & 15u);
+            if (t >= p.tokens) continue;
+#pragma unroll
+            for (uint32_t i = 0; i < T::kMi; ++i) {
+                const uint32_t r = m0 + wm + i * 16 + (lane >> 4) * 4;
+                if (r < p.rows) store4(y, kKind, (uint64_t)t * p.rows + r, p.rows - r, acc[i][j]);
+            }
+        }
+        return;
+    }
+    // as many tokens at a time as LDS holds
+    constexpr uint32_t kFit = T::kScalesAt / kRow, kPass = kFit < T::kBn ? kFit : T::kBn;
+    static_assert(T::kBn % kPass == 0 && kPass % T::kWaveN == 0 && kChunks >= 16, "a wave's tokens go together");
+    for (uint32_t from = 0; from < T::kBn; from += kPass) {
+        if (from) __syncthreads();
+        if (wn >= from && wn < from + kPass) {
+#pragma unroll
+            for (uint32_t j = 0; j < T::kNi; ++j)
+#pragma unroll
+                for (uint32_t i = 0; i < T::kMi; ++i) {
+                    const uint32_t n = wn - from + j * 16 + (lane & 15u), m = wm + i * 16 + (lane >> 4) * 4;
+                    uint8_t* const to = lds + n * kRow + (((m * kSize / 16) ^ (n & 15u)) * 16) + m * kSize % 16;
+                    if (kSize == 4) *reinterpret_cast<f32x4*>(to) = acc[i][j];
+                    else
+                        *reinterpret_cast<u32x2*>(to) =
+                            u32x2{pack_bf16(acc[i][j][0], acc[i][j][1]), pack_bf16(acc[i][j][2], acc[i][j][3])};
+                }
+        }
+        __syncthreads();
+        const uint32_t tokens = p.tokens - n0, rows = p.rows - m0;
+        uint8_t* const out = static_cast<uint8_t*>(y) + ((uint64_t)n0 * p.rows + m0) * kSize;
+        for (uint32_t k = threadIdx.x; k < kChunks * kPass; k += T::kThreads) {
+            const uint32_t n = k / kChunks, c = k % kChunks;
+            if (from + n < tokens && c * (16 / kSize) < rows)
+                *reinterpret_cast<u32x4*>(out + (uint64_t)(from + n) * p.rows * kSize + c * 16) =
+                    *reinterpret_cast<const u32x4*>(lds + n * kRow + ((c ^ (n & 15u)) * 16));
+        }
+    }
+}
+
 template <class T, bool kExact>
-__global__ __launch_bounds__(T::kThreads) void gemm_fp8_kernel(GemmParams p) {
+__global__ __launch_bounds__(T::kThreads, T::kAlternate ? 2 : 1) void gemm_fp8_kernel(GemmParams p) {
     __shared__ __align__(16) uint8_t lds[T::kLdsBytes];
     uint32_t mt, nt;
     if (!tile_of(blockIdx.x, (p.rows + T::kBm - 1) / T::kBm, (p.tokens + T::kBn - 1) / T::kBn, mt, nt)) return;
@@ -180,14 +243,26 @@ __global__ __launch_bounds__(T::kThreads) void gemm_fp8_kernel(GemmParams p) {
     constexpr uint32_t kLoads = lw.kLoads + lx.kLoads + 1;   // per thread and stage
     const u32x4 xs_buf = buffer_words(p.xs + (uint64_t)n0 * p.blocks, min(p.tokens - n0, T::kBn) * p.blocks * 4);
     const uint32_t xs_at = lane < T::kWaveN ? (wn + lane) * p.blocks * 4 : kNoChunk;
-    const float* const ws = p.ws + (uint64_t)(min(m0 + wm, p.rows - 1) / kBlockCols) * p.blocks;
-    const auto start = [&](uint32_t stage, uint32_t b) {   // zeros from the split's end on
-        uint8_t* const to = lds + stage * T::kStageBytes;
-        const uint32_t c0 = b < end ? b * kBlockCols : p.cols;
-        lw.start(to, c0);
-        lx.start(to + T::kBm * 128, c0);
-        copy_words_to_lds(lds_address(to) + T::kCodeBytes + wave * 256u, xs_buf,
+    typedef const __attribute__((address_space(4))) float constant_float;   // nothing here writes it: scalar loads
+    constant_float* const ws = (constant_float*)(p.ws + (uint64_t)(min(m0 + wm, p.rows - 1) / kBlockCols) * p.blocks);
+    // Start copying a stage (zeros from the split's end on), or its parts: first the tokens' codes, their scales, and the
+    // rows of the matrix that a wave multiplies in the first half of its step; then the other rows.
+    const auto column_of = [&](uint32_t b) { return b < end ? b * kBlockCols : p.cols; };
+    const auto start_tokens = [&](uint32_t stage, uint32_t b) {
+        lx.start(lds + stage * T::kCodeBytes + T::kBm * 128, column_of(b));
+        copy_words_to_lds(lds_address(lds) + T::kScalesAt + stage * T::kScaleBytes + wave * 256u, xs_buf,
                           b < end && lane < T::kWaveN ? xs_at + b * 4 : kNoChunk);
+    };
+    const auto start = [&](uint32_t stage, uint32_t b) {
+        lw.start(lds + stage * T::kCodeBytes, column_of(b));
+        start_tokens(stage, b);
+    };
+    const auto start_first = [&](uint32_t stage, uint32_t b) {
+        lw.template start<0, 2>(lds + stage * T::kCodeBytes, column_of(b));
+        start_tokens(stage, b);
+    };
+    const auto start_second = [&](uint32_t stage, uint32_t b) {
+        lw.template start<1, 2>(lds + stage * T::kCodeBytes, column_of(b));
     };
     f32x4 acc[T::kMi][T::kNi];
 #pragma unroll
@@ -195,53 +270,152 @@ __global__ __launch_bounds__(T::kThreads) void gemm_fp8_kernel(GemmParams p) {
 #pragma unroll
         for (uint32_t j = 0; j < T::kNi; ++j) acc[i][j] = (f32x4)(0.0f);
 
-#pragma unroll
-    for (uint32_t s = 0; s + 1 < T::kStages; ++s) start(s, begin + s);
-    uint32_t at = 0, to = T::kStages - 1;
-    for (uint32_t b = begin; b < end; ++b) {
-        // this stage has landed once only the later ones' copies are outstanding (each wave waits for its own, the
-        // barrier joins them); past the barrier every wave is done with the stage before, which is refilled
-        constexpr uint32_t kLater = (T::kStages - 2) * kLoads;
-        static_assert(kLater < 64, "the load counter's range");
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kLater) : "memory");
+    if constexpr (T::kAlternate) {
+        // The two waves of each SIMD take turns: waves 4..7 run half a step behind waves 0..3, so that one group reads
+        // its fragments while the other one's products keep the matrix cores busy.  Every wave passes the same
+        // barriers: the late group has one more at the start, the other one at the end.
+        //   waves 0..3   read b,0   multiply b,0   read b,1     multiply b,1   read b+1,0
+        //   waves 4..7              read b,0       multiply b,0 read b,1       multiply b,1
+        // A half of a stage is copied as soon as both groups have read what stands in its place (a group's reads have
+        // returned before the barrier behind them): what is read in b,0 gives way to that of b + 2 in b,1, what is read
+        // in b,1 to that of b + 2 in b + 1,0.  So a copy has five of a stage's four turns to land in, with two stages of
+        // LDS; from memory it takes about 1 us, as long as three of them.  (Whole stages, two to three turns: 1846 us at
+        // 8192 tokens x 28672 x 8192; without any copies 1326.)
+        constexpr uint32_t kSteps = 2, kPer = T::kMi / kSteps, kAway = 4;
+        static_assert(T::kMi == 8 && T::kNi == 4 && T::kStages == 2 && T::kThreads == 512, "steps of two groups of waves");
+        static_assert(lw.kLoads == 4 && lw.kRows == kPer * 16 && T::kWaveM == 2 * kPer * 16,
+                      "rounds of the matrix's copies are of the first and the second step in turn");
+        constexpr uint32_t kOnTheirWay = lw.kLoads + lx.kLoads + 1;   // of both halves
+        const bool late = wave >= 4;
+        start_first(0, begin);
+        start_second(0, begin);
+        start_first(1, begin + 1);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kOnTheirWay) : "memory");
         __builtin_amdgcn_s_barrier();
+        if (late) __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        start(to, b + T::kStages - 1);
-        const uint8_t* const sw = lds + at * T::kStageBytes;
-        const uint8_t* const sx = sw + T::kBm * 128;
-        const float* const sc = reinterpret_cast<const float*>(sw + T::kCodeBytes) + wave * 64;
-        const float scale = ws[b];
-        float s[T::kNi];
+        // a product takes the place of the one 4 before it, which is added to the results while the products in between
+        // keep the matrix core busy (before the very first ones: zeros)
+        f32x4 d[kAway];
+        float s[T::kNi], last[T::kNi];
 #pragma unroll
-        for (uint32_t j = 0; j < T::kNi; ++j) s[j] = sc[j * 16 + (lane & 15u)] * scale;
+        for (uint32_t i = 0; i < kAway; ++i) d[i] = (f32x4)(0.0f);
 #pragma unroll
-        for (uint32_t j = 0; j < T::kNi; ++j) {
-            const Operand<kExact> x(fragment(sx, wn + j * 16));
+        for (uint32_t j = 0; j < T::kNi; ++j) s[j] = 0.0f;
+        const auto add = [&](uint32_t product, const float (&by)[T::kNi]) {
+            f32x4& to = acc[product / T::kNi][product % T::kNi];
 #pragma unroll
-            for (uint32_t i = 0; i < T::kMi; ++i) {
-                const Operand<kExact> w(fragment(sw, wm + i * 16));
-                const f32x4 d = Operand<kExact>::product(w, x);
+            for (uint32_t e = 0; e < 4; ++e) to[e] = __builtin_fmaf(d[product % kAway][e], by[product % T::kNi], to[e]);
+        };
+        constexpr uint32_t kProducts = T::kMi * T::kNi;
+        float scale = ws[begin];
+        uint32_t at = 0;
+        // where the lane reads: the two chunks of its rows of the matrix and of the tokens, and the scales; a stage's are
+        // the other one's with one bit changed
+        static_assert(T::kCodeBytes == 65536, "one bit");
+        const Places places_w(wm), places_x(T::kBm + wn);
+        uint32_t from_w = places_w.lo, from_w4 = places_w.hi, from_x = places_x.lo, from_x4 = places_x.hi;
+        for (uint32_t b = begin; b < end; ++b, at ^= 1) {
+            const float* const sc = reinterpret_cast<const float*>(lds + T::kScalesAt + at * T::kScaleBytes) + wave * 64;
+            i32x8 x[T::kNi];
 #pragma unroll
-                for (uint32_t e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(d[e], s[j], acc[i][j][e]);
+            for (uint32_t step = 0; step < kSteps; ++step) {
+                i32x8 w[kPer];
+                float own[T::kNi];
+#pragma unroll
+                for (uint32_t i = 0; i < kPer; ++i)
+                    w[i] = joined(lds + from_w + (step * kPer + i) * 2048, lds + from_w4 + (step * kPer + i) * 2048);
+                if (step == 0) {
+#pragma unroll
+                    for (uint32_t j = 0; j < T::kNi; ++j) x[j] = joined(lds + from_x + j * 2048, lds + from_x4 + j * 2048);
+#pragma unroll
+                    for (uint32_t j = 0; j < T::kNi; ++j) own[j] = sc[j * 16 + (lane & 15u)];
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                if (step == 0) {
+                    start_second(at ^ 1, b + 1);
+                } else {
+                    start_first(at, b + 2);
+                    from_w ^= T::kCodeBytes, from_w4 ^= T::kCodeBytes, from_x ^= T::kCodeBytes, from_x4 ^= T::kCodeBytes;
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                // of the copies, those that were started in this turn and the one before may be on their way still
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kOnTheirWay) : "memory");
+                if (step == 0) {
+#pragma unroll
+                    for (uint32_t j = 0; j < T::kNi; ++j) last[j] = s[j], s[j] = own[j] * scale;
+                } else {
+                    scale = ws[min(b + 1, end - 1)];
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+                __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+                for (uint32_t i = 0; i < kPer; ++i)
+#pragma unroll
+                    for (uint32_t j = 0; j < T::kNi; ++j) {
+                        const uint32_t product = (step * kPer + i) * T::kNi + j;
+                        if (product < kAway) add(kProducts - kAway + product, last);
+                        else add(product - kAway, s);
+                        d[product % kAway] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[i], x[j], (f32x4)(0.0f), 0,
+                                                                                             0, 0, 0, 0, 0);
+                        __builtin_amdgcn_sched_group_barrier(2, 4, 0);   // four VALU instructions, then the product
+                        __builtin_amdgcn_sched_group_barrier(8, 1, 0);
+                    }
+                __builtin_amdgcn_s_setprio(0);
+                __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
             }
         }
-        to = at;
-        at = at + 1 == T::kStages ? 0 : at + 1;
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing is on its way into LDS any more
-
-    void* const y = p.splits > 1 ? p.part + (uint64_t)blockIdx.y * p.tokens * p.rows : p.y;
-    const uint32_t kind = p.splits > 1 ? WC_OUT_F32 : p.out_kind;
+        if (!late) __builtin_amdgcn_s_barrier();
 #pragma unroll
-    for (uint32_t j = 0; j < T::kNi; ++j) {
-        const uint32_t t = n0 + wn + j * 16 + (lane & 15u);
-        if (t >= p.tokens) continue;
+        for (uint32_t product = kProducts - kAway; product < kProducts; ++product) add(product, s);
+    } else {
 #pragma unroll
-        for (uint32_t i = 0; i < T::kMi; ++i) {
-            const uint32_t r = m0 + wm + i * 16 + (lane >> 4) * 4;
-            if (r < p.rows) store4(y, kind, (uint64_t)t * p.rows + r, p.rows - r, acc[i][j]);
+        for (uint32_t s = 0; s + 1 < T::kStages; ++s) start(s, begin + s);
+        uint32_t at = 0, to = T::kStages - 1;
+        for (uint32_t b = begin; b < end; ++b) {
+            // this stage has landed once only the later ones' copies are outstanding (each wave waits for its own, the
+            // barrier joins them); past the barrier every wave is done with the stage before, which is refilled
+            constexpr uint32_t kLater = (T::kStages - 2) * kLoads;
+            static_assert(kLater < 64, "the load counter's range");
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kLater) : "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            start(to, b + T::kStages - 1);
+            const uint8_t* const sw = lds + at * T::kCodeBytes;
+            const uint8_t* const sx = sw + T::kBm * 128;
+            const float* const sc = reinterpret_cast<const float*>(lds + T::kScalesAt + at * T::kScaleBytes) + wave * 64;
+            const float scale = ws[b];
+            float s[T::kNi];
+#pragma unroll
+            for (uint32_t j = 0; j < T::kNi; ++j) s[j] = sc[j * 16 + (lane & 15u)] * scale;
+#pragma unroll
+            for (uint32_t j = 0; j < T::kNi; ++j) {
+                const Operand<kExact> x(fragment(sx, wn + j * 16));
+#pragma unroll
+                for (uint32_t i = 0; i < T::kMi; ++i) {
+                    const Operand<kExact> w(fragment(sw, wm + i * 16));
+                    const f32x4 d = Operand<kExact>::product(w, x);
+#pragma unroll
+                    for (uint32_t e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(d[e], s[j], acc[i][j][e]);
+                }
+            }
+            to = at;
+            at = at + 1 == T::kStages ? 0 : at + 1;
         }
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing is on its way into LDS any more
+    __syncthreads();
+    if (p.splits > 1)
+        store_tile<T, WC_OUT_F32>(lds, p.part + (uint64_t)blockIdx.y * p.tokens * p.rows, p, m0, n0, acc);
+    else if (kExact && p.out_kind == WC_OUT_F32)
+        store_tile<T, WC_OUT_F32>(lds, p.y, p, m0, n0, acc);
+    else
+        store_tile<T, WC_OUT_BF16>(lds, p.y, p, m0, n0, acc);
 }
 
 // The splits' sums, in order.
@@ -258,18 +432,20 @@ __global__ __launch_bounds__(256) void gemm_fp8_join_kernel(GemmParams p) {
 
 uint32_t cdiv(uint64_t a, uint32_t b) { return (uint32_t)((a + b - 1) / b); }
 
+using Big = Tile<256, 256, 2, 4, 2>;
 using Mid = Tile<128, 128, 2, 2, 2>;
 using Thin = Tile<128, 32, 4, 1, 4>;
 constexpr uint32_t kCus = 256;
 
 struct GemmPlan {
-    bool thin;
+    bool thin, big;
     uint32_t splits, split_blocks;
     uint64_t work_bytes;
 };
 GemmPlan plan_of(uint32_t rows, uint32_t cols, uint64_t tokens) {
     GemmPlan g{};
     g.thin = tokens <= 32;
+    g.big = (uint64_t)cdiv(rows, 256) * cdiv(tokens, 256) >= kCus;
     const uint32_t blocks = cdiv(cols, kBlockCols);
     const uint64_t tiles = (uint64_t)cdiv(rows, 128) * cdiv(tokens, g.thin ? 32 : 128);
     uint32_t splits = tiles < kCus ? (uint32_t)(kCus / tiles) : 1;
@@ -326,6 +502,7 @@ extern "C" int wc_gemm_fp8_async(const wc_fp8_matrix* W, const uint8_t* x_codes,
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (g.thin) launch<Thin, true>(p, s);
     else if (out_kind == WC_OUT_F32) launch<Mid, true>(p, s);
+    else if (g.big) launch<Big, false>(p, s);
     else launch<Mid, false>(p, s);
     if (g.splits > 1) {
         const uint32_t groups = cdiv((uint64_t)p.tokens * p.rows, 1024);

@@ -92,12 +92,13 @@ def eights(t):
 
 def _largest_of_eights(x, w):
     """Sum over groups of 8 columns of the largest |product| there, for each row of x and of w."""
-    xe, we = eights(x), eights(w)
-    total = torch.zeros(x.shape[0], w.shape[0], dtype=torch.float64)
-    for t0 in range(0, x.shape[0], 64):
+    device = "cuda" if torch.cuda.is_available() else "cpu"
+    xe, we = eights(x).to(device), eights(w).to(device)
+    total = torch.zeros(x.shape[0], w.shape[0], dtype=torch.float64, device=device)
+    for t0 in range(0, x.shape[0], 512):
         for k in range(xe.shape[1]):
-            total[t0:t0 + 64] += (xe[t0:t0 + 64, None, k] * we[None, :, k]).amax(dim=2)
-    return total
+            total[t0:t0 + 512] += (xe[t0:t0 + 512, None, k] * we[None, :, k]).amax(dim=2)
+    return total.cpu()
 
 
 def gemm_tolerance(x, w, out_bf16, y):

@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from e4m3_ref import BLOCK, blocks, gemm_tolerance, matrix_codes, per_column, quantised, values_of, within
+from e4m3_ref import BLOCK, UBF16, _largest_of_eights, blocks, gemm_tolerance, matrix_codes, per_column, quantised, values_of, within
 from gpu_util import log
 
 pytestmark = pytest.mark.gpu
@@ -55,6 +55,21 @@ def test_products(wc, rows, cols, tokens, out):
     want = x @ w.t()
     assert within(y, want, gemm_tolerance(x, w, out == "bf16", want))
     again = _run(wc, W, xc.cuda(), xs.cuda(), tokens, out)
+    assert torch.equal(y, again), "two runs differ"
+
+
+@pytest.mark.parametrize("rows,cols,tokens", [(4352, 128, 4100), (8200, 400, 2049), (4100, 656, 4352), (4097, 272, 4097)])
+def test_many_tiles(wc, rows, cols, tokens):
+    """Enough rows and tokens for the largest tiles, whole and cut, with one block of columns to several."""
+    codes, scales, w, xc, xs, x = _case(rows, cols, tokens, rows)
+    log(f"case: gemm_fp8 {rows}x{cols}, {tokens} tokens")
+    W = wc.Fp8Matrix(codes.cuda(), scales.cuda(), rows, cols)
+    y = _run(wc, W, xc.cuda(), xs.cuda(), tokens, "bf16")
+    want = (x.cuda() @ w.cuda().t()).cpu()
+    tol = 2.0 ** -23 * (128 + 2 * blocks(cols) + 4) * (x.cuda().abs() @ w.cuda().abs().t()).cpu()
+    tol += 2.0 ** -11 * _largest_of_eights(x, w)
+    assert within(y, want, tol + UBF16 * (want.abs() + tol) + 1e-40)
+    again = _run(wc, W, xc.cuda(), xs.cuda(), tokens, "bf16")
     assert torch.equal(y, again), "two runs differ"
 
 
