@@ -58,18 +58,28 @@ def test_products(wc, rows, cols, tokens, out):
     assert torch.equal(y, again), "two runs differ"
 
 
-@pytest.mark.parametrize("rows,cols,tokens", [(4352, 128, 4100), (8200, 400, 2049), (4100, 656, 4352), (4097, 272, 4097)])
-def test_many_tiles(wc, rows, cols, tokens):
-    """Enough rows and tokens for the largest tiles, whole and cut, with one block of columns to several."""
+# tiles of every size, whole and cut at rows, tokens and columns; sums in one part and in up to 16
+TILES = [(1304, 2704, 90), (1003, 2096, 333), (1027, 1040, 515), (1001, 4112, 1000), (5000, 1008, 200), (1000, 2064, 1200),
+         (1601, 800, 2000), (4100, 656, 1030), (4352, 128, 4100), (8200, 400, 2049), (4100, 656, 4352), (4097, 272, 4097),
+         (64, 28672, 40), (97, 65536, 70), (300, 20000, 64), (130, 16400, 300), (1024, 14336, 100), (2050, 8208, 130),
+         (4096, 14336, 128), (8192, 4112, 16), (8209, 4112, 31), (9001, 1296, 5)]
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols,tokens", TILES)
+def test_tiles(wc, rows, cols, tokens, out):
     codes, scales, w, xc, xs, x = _case(rows, cols, tokens, rows)
-    log(f"case: gemm_fp8 {rows}x{cols}, {tokens} tokens")
+    log(f"case: gemm_fp8 {rows}x{cols}, {tokens} tokens, {out}")
     W = wc.Fp8Matrix(codes.cuda(), scales.cuda(), rows, cols)
-    y = _run(wc, W, xc.cuda(), xs.cuda(), tokens, "bf16")
-    want = (x.cuda() @ w.cuda().t()).cpu()
-    tol = 2.0 ** -23 * (128 + 2 * blocks(cols) + 4) * (x.cuda().abs() @ w.cuda().abs().t()).cpu()
-    tol += 2.0 ** -11 * _largest_of_eights(x, w)
-    assert within(y, want, tol + UBF16 * (want.abs() + tol) + 1e-40)
-    again = _run(wc, W, xc.cuda(), xs.cuda(), tokens, "bf16")
+    y = _run(wc, W, xc.cuda(), xs.cuda(), tokens, out)
+    xd, wd = x.cuda(), w.cuda()
+    want = xd @ wd.t()
+    tol = 2.0 ** -23 * (128 + 2 * blocks(cols) + 4) * (xd.abs() @ wd.abs().t()) + 1e-40
+    if out == "bf16":
+        tol += 2.0 ** -11 * _largest_of_eights(x, w).cuda()
+        tol += UBF16 * (want.abs() + tol)
+    assert within(y, want.cpu(), tol.cpu())
+    again = _run(wc, W, xc.cuda(), xs.cuda(), tokens, out)
     assert torch.equal(y, again), "two runs differ"
 
 
