@@ -547,10 +547,10 @@ int wc_gemm_fp8_async(const wc_fp8_matrix* W, const uint8_t* x_codes, const floa
  *   work_dev  device scratch of at least wc_clip_grads_work_bytes(grads, n)
  *             bytes (0: it may be NULL), 256-byte aligned, overwritten; calls
  *             that may overlap need one each.
- * Two launches per 96 tensors.  n is at most WC_MAX_GRADS.
+ * Two launches per 96 tensors, and at most one more.  n is at most WC_MAX_GRADS.
  */
 #define WC_MAX_GRADS      (1u << 20)
-#define WC_MAX_GRAD_NUMEL (1ull << 38)
+#define WC_MAX_GRAD_NUMEL (1ull << 34)
 typedef struct {
     const void* g;    /* device, numel elements, aligned to them (faster: to 16 bytes) */
     void* out;        /* the same, written: g itself, or no part of any tensor read    */

@@ -9,10 +9,18 @@
 // of a batch are cut into chunks of one size in bytes; a workgroup of the norm
 // takes chunks block, block + grid, ... and leaves one partial sum, in double
 // precision (no gradient of fp32 or bf16 overflows there, and long sums keep
-// fp32's digits).  Every workgroup of the second pass adds all partial sums
-// itself, in the same order, which is less than a launch in between would cost.
-// The second pass goes through the chunks from the last to the first: those read
-// last by the first pass may still lie in the 256 MB cache.
+// fp32's digits).  Of up to kOwnParts partial sums every workgroup of the second
+// pass adds all by itself, in the same order, which is less than a launch in
+// between would cost; more are added by such a launch.  The second pass takes one
+// chunk per workgroup, from the last to the first: those read last by the first
+// pass may still lie in the 256 MB cache.
+//
+// Four blocks of an 8B-shape model in bf16 (1.74 GB, read twice, written once), us:
+//   2048 workgroups at a time, chunks of 64 KiB, plain loads and stores      993
+//   loads and stores past the caches                                         920
+//   8192 workgroups, chunks of 32 KiB                                        868
+//   chunks of 16 KiB, one per workgroup of the second pass                   834
+// which is 6.28 TB/s; a copy of 2 GB reaches 6.44.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -25,7 +33,9 @@ namespace {
 
 constexpr uint32_t kThreads = 256;
 constexpr uint32_t kBatch = 96;            // tensors per launch: 32 bytes of arguments each
-constexpr uint32_t kGroups = 2048;         // workgroups per launch at most
+constexpr uint32_t kGroups = 8192;         // workgroups of a norm's launch at most
+constexpr uint32_t kOwnParts = 1024;
+constexpr uint32_t kMostChunks = 1u << 23;
 constexpr uint32_t kRounds = 4;            // 16-byte loads per thread on their way
 
 struct ClipTensor {
@@ -41,7 +51,7 @@ struct ClipParams {
     double* part;
     uint32_t tensors, chunks, chunk_bytes;
     uint32_t part_at;   // the batch's first partial sum
-    uint32_t parts;     // of all batches
+    uint32_t parts;     // that the second pass adds, from `part` on
     float max_norm;
     float* norm;        // written by the first workgroup, where not NULL
 };
@@ -92,6 +102,7 @@ __device__ __forceinline__ float value(const ClipTensor& t, uint64_t i) {
                                 : __uint_as_float((uint32_t) static_cast<const uint16_t*>(t.g)[i] << 16);
 }
 
+template <bool kStream>
 __global__ __launch_bounds__(kThreads) void clip_norm_kernel(ClipParams p) {
     double sum = 0.0;
     for (uint32_t chunk = blockIdx.x; chunk < p.chunks; chunk += gridDim.x) {
@@ -104,7 +115,7 @@ __global__ __launch_bounds__(kThreads) void clip_norm_kernel(ClipParams p) {
                     u32x4 w[kRounds];
 #pragma unroll
                     for (uint32_t k = 0; k < kRounds; ++k)
-                        w[k] = i + k * kThreads < lanes ? g[i + k * kThreads] : u32x4{0, 0, 0, 0};
+                        w[k] = i + k * kThreads < lanes ? load16<kStream>(g + i + k * kThreads) : u32x4{0, 0, 0, 0};
 #pragma unroll
                     for (uint32_t k = 0; k < kRounds; ++k)
 #pragma unroll
@@ -120,6 +131,22 @@ __global__ __launch_bounds__(kThreads) void clip_norm_kernel(ClipParams p) {
     if (threadIdx.x == 0) p.part[p.part_at + blockIdx.x] = sum;
 }
 
+constexpr uint32_t kJoinThreads = 1024;
+// The partial sums' sum, in a fixed order, behind them.
+__global__ __launch_bounds__(kJoinThreads) void clip_join_kernel(double* part, uint32_t parts) {
+    __shared__ double sums[kJoinThreads / 64];
+    double v = 0.0;
+    for (uint32_t i = threadIdx.x; i < parts; i += kJoinThreads) v += part[i];
+#pragma unroll
+    for (uint32_t d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+    if ((threadIdx.x & 63u) == 0) sums[threadIdx.x >> 6] = v;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (uint32_t k = 1; k < kJoinThreads / 64; ++k) v += sums[k];
+    part[parts] = v;
+}
+
+template <bool kStream>
 __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipParams p) {
     double sum = 0.0;
     for (uint32_t i = threadIdx.x; i < p.parts; i += kThreads) sum += p.part[i];
@@ -128,60 +155,61 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipParams p) {
     if (p.norm && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = norm;
     const bool clips = norm > p.max_norm && norm < INFINITY;
     const float factor = clips ? (float)((double)p.max_norm / total) : 1.0f;
-    for (uint32_t at = blockIdx.x; at < p.chunks; at += gridDim.x) {
-        const uint32_t chunk = p.chunks - 1 - at;
-        const ClipTensor& t = p.tensor[tensor_of(p, chunk)];
-        if (!clips && t.g == t.out) continue;
-        for_chunk(
-            p, t, chunk,
-            [&](uint64_t from, uint32_t lanes) {
-                const u32x4* const g = static_cast<const u32x4*>(t.g) + from;
-                u32x4* const out = static_cast<u32x4*>(t.out) + from;
-                for (uint32_t i = threadIdx.x; i < lanes; i += kThreads * kRounds) {
-                    u32x4 w[kRounds];
+    if (blockIdx.x >= p.chunks) return;   // a list without elements
+    const uint32_t chunk = p.chunks - 1 - blockIdx.x;
+    const ClipTensor& t = p.tensor[tensor_of(p, chunk)];
+    if (!clips && t.g == t.out) return;
+    for_chunk(
+        p, t, chunk,
+        [&](uint64_t from, uint32_t lanes) {
+            const u32x4* const g = static_cast<const u32x4*>(t.g) + from;
+            u32x4* const out = static_cast<u32x4*>(t.out) + from;
+            for (uint32_t i = threadIdx.x; i < lanes; i += kThreads * kRounds) {
+                u32x4 w[kRounds];
 #pragma unroll
-                    for (uint32_t k = 0; k < kRounds; ++k)
-                        w[k] = i + k * kThreads < lanes ? g[i + k * kThreads] : u32x4{0, 0, 0, 0};
+                for (uint32_t k = 0; k < kRounds; ++k)
+                    w[k] = i + k * kThreads < lanes ? load16<kStream>(g + i + k * kThreads) : u32x4{0, 0, 0, 0};
 #pragma unroll
-                    for (uint32_t k = 0; k < kRounds; ++k) {
-                        if (i + k * kThreads >= lanes) break;
-                        if (clips) {
+                for (uint32_t k = 0; k < kRounds; ++k) {
+                    if (i + k * kThreads >= lanes) break;
+                    if (clips) {
 #pragma unroll
-                            for (uint32_t e = 0; e < 4; ++e)
-                                w[k][e] = t.kind == WC_OUT_F32
-                                              ? __float_as_uint(__uint_as_float(w[k][e]) * factor)
-                                              : pack_bf16(bf16_lo(w[k][e]) * factor, bf16_hi(w[k][e]) * factor);
-                        }
-                        out[i + k * kThreads] = w[k];
+                        for (uint32_t e = 0; e < 4; ++e)
+                            w[k][e] = t.kind == WC_OUT_F32 ? __float_as_uint(__uint_as_float(w[k][e]) * factor)
+                                                           : pack_bf16(bf16_lo(w[k][e]) * factor, bf16_hi(w[k][e]) * factor);
                     }
+                    store16<kStream>(out + i + k * kThreads, w[k]);
                 }
-            },
-            [&](uint64_t i) {
-                if (t.kind == WC_OUT_F32) {
-                    const float v = static_cast<const float*>(t.g)[i];
-                    static_cast<float*>(t.out)[i] = clips ? v * factor : v;
-                } else {
-                    const uint16_t v = static_cast<const uint16_t*>(t.g)[i];
-                    static_cast<uint16_t*>(t.out)[i] =
-                        clips ? (uint16_t)pack_bf16(__uint_as_float((uint32_t)v << 16) * factor, 0.0f) : v;
-                }
-            });
-    }
+            }
+        },
+        [&](uint64_t i) {
+            if (t.kind == WC_OUT_F32) {
+                const float v = static_cast<const float*>(t.g)[i];
+                static_cast<float*>(t.out)[i] = clips ? v * factor : v;
+            } else {
+                const uint16_t v = static_cast<const uint16_t*>(t.g)[i];
+                static_cast<uint16_t*>(t.out)[i] =
+                    clips ? (uint16_t)pack_bf16(__uint_as_float((uint32_t)v << 16) * factor, 0.0f) : v;
+            }
+        });
 }
 
 uint32_t size_of(const wc_grad& g) { return g.kind == WC_OUT_F32 ? 4 : 2; }
 
-// A list's chunks: 4 to 64 KiB, so that few gradients still are work for many workgroups and large ones are not cut
-// finer than the memory asks for.
-uint32_t chunk_bytes(const wc_grad* grads, uint32_t n) {
+// A list's chunks: of few gradients small ones, so that they still are work for many workgroups.  Lists past the 256 MB
+// cache are read and written past the caches.
+struct ClipShape {
+    uint32_t chunk_bytes;
+    bool stream;
+};
+ClipShape shape_of(const wc_grad* grads, uint32_t n) {
     uint64_t bytes = 0;
     for (uint32_t i = 0; i < n; ++i) bytes += grads[i].numel * size_of(grads[i]);
-    uint32_t c = 4096;
-    while (c < 65536 && (uint64_t)c * kGroups < bytes) c *= 2;
-    return c;
+    return {bytes < (8u << 20) ? 4096u : 16384u, bytes > kCacheBytes};
 }
 
-// The next batch: as many tensors from `at` on as fit, but those without elements.  Returns where the one after it begins.
+// The next batch: as many tensors from `at` on as fit, but those without elements, and no more chunks than a launch's
+// fewer than 2^32 threads allow (one tensor has 2^22 at most).  Returns where the one after it begins.
 uint32_t next_batch(const wc_grad* grads, uint32_t n, uint32_t at, uint32_t bytes, ClipParams& p) {
     p.tensors = p.chunks = 0;
     p.chunk_bytes = bytes;
@@ -189,6 +217,7 @@ uint32_t next_batch(const wc_grad* grads, uint32_t n, uint32_t at, uint32_t byte
         const wc_grad& g = grads[at];
         if (g.numel == 0) continue;
         const uint64_t chunks = (g.numel * size_of(g) + bytes - 1) / bytes;
+        if (p.tensors && p.chunks + chunks > kMostChunks) break;
         p.tensor[p.tensors++] = ClipTensor{g.g, g.out, g.numel, p.chunks, g.kind};
         p.chunks += (uint32_t)chunks;
     }
@@ -214,11 +243,11 @@ using namespace wc;
 
 extern "C" int wc_clip_grads_work_bytes(const wc_grad* grads, uint32_t n, uint64_t* work_bytes) {
     if (!work_bytes || !list_fits(grads, n)) return WC_ERR_INVALID_ARG;
-    const uint32_t bytes = chunk_bytes(grads, n);
+    const uint32_t bytes = shape_of(grads, n).chunk_bytes;
     uint64_t parts = 0;
     ClipParams p{};
     for (uint32_t at = 0; at < n;) at = next_batch(grads, n, at, bytes, p), parts += groups_of(p);
-    *work_bytes = parts * sizeof(double);
+    *work_bytes = parts ? (parts + 1) * sizeof(double) : 0;
     return WC_OK;
 }
 
@@ -230,23 +259,30 @@ extern "C" int wc_clip_grads_async(const wc_grad* grads, uint32_t n, float max_n
     if (!(max_norm >= 0.0f) || !aligned(norm, 4) || (need && (!aligned(work_dev, 256) || work_bytes < need)))
         return WC_ERR_INVALID_ARG;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    const uint32_t bytes = chunk_bytes(grads, n);
+    const ClipShape shape = shape_of(grads, n);
     ClipParams p{};
     p.part = static_cast<double*>(work_dev);
     p.max_norm = max_norm;
     for (uint32_t at = 0; at < n;) {
-        at = next_batch(grads, n, at, bytes, p);
+        at = next_batch(grads, n, at, shape.chunk_bytes, p);
         if (p.chunks == 0) continue;
-        hipLaunchKernelGGL(clip_norm_kernel, dim3(groups_of(p)), dim3(kThreads), 0, s, p);
+        const auto kernel = shape.stream ? clip_norm_kernel<true> : clip_norm_kernel<false>;
+        hipLaunchKernelGGL(kernel, dim3(groups_of(p)), dim3(kThreads), 0, s, p);
         p.part_at += groups_of(p);
     }
     p.parts = p.part_at;
+    if (p.parts > kOwnParts) {
+        hipLaunchKernelGGL(clip_join_kernel, dim3(1), dim3(kJoinThreads), 0, s, p.part, p.parts);
+        p.part += p.parts;
+        p.parts = 1;
+    }
     p.norm = norm;
     uint32_t at = 0;
     do {   // a list without elements: its norm alone, 0
-        at = next_batch(grads, n, at, bytes, p);
+        at = next_batch(grads, n, at, shape.chunk_bytes, p);
         if (p.chunks == 0 && !p.norm) continue;
-        hipLaunchKernelGGL(clip_scale_kernel, dim3(p.chunks ? groups_of(p) : 1), dim3(kThreads), 0, s, p);
+        const auto kernel = shape.stream ? clip_scale_kernel<true> : clip_scale_kernel<false>;
+        hipLaunchKernelGGL(kernel, dim3(p.chunks ? p.chunks : 1), dim3(kThreads), 0, s, p);
         p.norm = nullptr;
     } while (at < n);
     return hipGetLastError() == hipSuccess ? WC_OK : WC_ERR_HIP;

@@ -31,6 +31,18 @@ __device__ __forceinline__ u32x4 pack_bf16(const float (&f)[8]) {
     return u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
 }
 
+// Loads and stores, kStream: past the caches, for what is too large to be found in them again.
+constexpr uint64_t kCacheBytes = 256ull << 20;
+template <bool kStream, class T>
+__device__ __forceinline__ T load16(const T* p) {
+    return kStream ? __builtin_nontemporal_load(p) : *p;
+}
+template <bool kStream, class T>
+__device__ __forceinline__ void store16(T* p, const T& v) {
+    if (kStream) __builtin_nontemporal_store(v, p);
+    else *p = v;
+}
+
 // The lane's value in the lane that the four DPP steps pair it with: lane ^ 1, lane ^ 2, half row mirrored, row
 // mirrored.  After all four, a row of 16 lanes holds one result.
 template <int kStep>

@@ -12,11 +12,13 @@
 // without being rounded to bf16 first.
 //
 // Both kernels read each input once and are bound by memory.  A row is held in
-// registers (8 columns per lane and round), by one wave where rows are short
-// enough (then nothing waits for other waves), else by a workgroup.  The
-// gradient's waves take many rows each, sum dw over them in registers and leave
-// one partial row per workgroup; a second kernel adds those in order, so that
-// results are the same bits on every run.
+// registers, 8 columns per lane and round.  The gradient's workgroups take many
+// rows each, sum dw over them in registers and leave one partial row; a second
+// kernel adds those in order, so that results are the same bits on every run.
+// Rows past the 256 MB cache are read and written past the caches (8192 x 8192
+// with the residual, into codes: 78 us, 6.05 TB/s; 86 with plain loads and stores.
+// 16384 x 4096: norm 87 us, 6.2 TB/s; gradient 96, 5.6 TB/s, its second kernel
+// among them).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -42,13 +44,13 @@ struct NormParams {
     float eps, inv_dim;
 };
 
-// The sum over a row that blockDim.x threads hold: one wave, or a workgroup of
-// one row.  `sums` is LDS of kMaxWaves floats, free for the next call after one
-// more barrier.
+// The sum over the row that blockDim.x threads hold: one wave, or several, where the whole workgroup waits.  `sums` is LDS
+// of kMaxWaves floats, free for the next call after one more barrier.
 __device__ __forceinline__ float row_sum(float v, float* sums) {
     v = wave_sum(v);
     const uint32_t waves = blockDim.x >> 6;
     if (waves == 1) return v;
+    sums += threadIdx.y * waves;
     if ((threadIdx.x & 63u) == 0) sums[threadIdx.x >> 6] = v;
     __syncthreads();
     v = sums[0];
@@ -56,29 +58,30 @@ __device__ __forceinline__ float row_sum(float v, float* sums) {
     return v;
 }
 
+template <bool kStream>
 __device__ __forceinline__ u32x4 load8(const uint16_t* row, uint32_t c, uint32_t dim) {
-    return c < dim ? *reinterpret_cast<const u32x4*>(row + c) : u32x4{0, 0, 0, 0};
+    return c < dim ? load16<kStream>(reinterpret_cast<const u32x4*>(row + c)) : u32x4{0, 0, 0, 0};
 }
 
 // blockDim.x threads hold a row, 8 columns each in kRounds rounds; blockDim.y rows (one, unless a row is one wave).
-template <uint32_t kRounds, bool kCodes>
+template <uint32_t kRounds, bool kCodes, bool kStream>
 __global__ __launch_bounds__(64 * kMaxWaves) void rms_norm_kernel(NormParams p) {
     __shared__ float sums[kMaxWaves];
     const uint32_t row = __builtin_amdgcn_readfirstlane(blockIdx.x * blockDim.y + threadIdx.y);
-    if (row >= p.n) return;   // whole waves, and none where waves wait for each other
+    const uint32_t dim = row < p.n ? p.dim : 0;   // past the last row, nothing is read or written: others may wait
     const uint64_t first = (uint64_t)row * p.dim;
     u32x4 h[kRounds], w[kRounds];
 #pragma unroll
     for (uint32_t k = 0; k < kRounds; ++k) {
         const uint32_t c = (k * blockDim.x + threadIdx.x) * 8;
-        h[k] = load8(p.x + first, c, p.dim);
+        h[k] = load8<kStream>(p.x + first, c, dim);
     }
     if (p.residual) {
         u32x4 r[kRounds];
 #pragma unroll
         for (uint32_t k = 0; k < kRounds; ++k) {
             const uint32_t c = (k * blockDim.x + threadIdx.x) * 8;
-            r[k] = load8(p.residual + first, c, p.dim);
+            r[k] = load8<kStream>(p.residual + first, c, dim);
         }
 #pragma unroll
         for (uint32_t k = 0; k < kRounds; ++k) {
@@ -89,11 +92,11 @@ __global__ __launch_bounds__(64 * kMaxWaves) void rms_norm_kernel(NormParams p) 
 #pragma unroll
             for (uint32_t i = 0; i < 8; ++i) a[i] += b[i];
             h[k] = pack_bf16(a);
-            if (c < p.dim) *reinterpret_cast<u32x4*>(p.sum + first + c) = h[k];
+            if (c < dim) store16<kStream>(reinterpret_cast<u32x4*>(p.sum + first + c), h[k]);
         }
     }
 #pragma unroll
-    for (uint32_t k = 0; k < kRounds; ++k) w[k] = load8(p.weight, (k * blockDim.x + threadIdx.x) * 8, p.dim);
+    for (uint32_t k = 0; k < kRounds; ++k) w[k] = load8<false>(p.weight, (k * blockDim.x + threadIdx.x) * 8, p.dim);
     float squares = 0.0f;
 #pragma unroll
     for (uint32_t k = 0; k < kRounds; ++k) {
@@ -103,7 +106,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void rms_norm_kernel(NormParams p) 
         for (uint32_t i = 0; i < 8; ++i) squares = __builtin_fmaf(a[i], a[i], squares);
     }
     const float rstd = 1.0f / sqrtf(__builtin_fmaf(row_sum(squares, sums), p.inv_dim, p.eps));
-    if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
+    if (p.rstd && threadIdx.x == 0 && row < p.n) p.rstd[row] = rstd;
 #pragma unroll
     for (uint32_t k = 0; k < kRounds; ++k) {
         const uint32_t c = (k * blockDim.x + threadIdx.x) * 8;
@@ -112,11 +115,11 @@ __global__ __launch_bounds__(64 * kMaxWaves) void rms_norm_kernel(NormParams p) 
         unpack_bf16(w[k], g);
 #pragma unroll
         for (uint32_t i = 0; i < 8; ++i) y[i] = y[i] * rstd * g[i];
-        if (p.y && c < p.dim) *reinterpret_cast<u32x4*>(p.y + first + c) = pack_bf16(y);
+        if (p.y && c < dim) store16<kStream>(reinterpret_cast<u32x4*>(p.y + first + c), pack_bf16(y));
         if (kCodes) {
             const BlockCodes q = block_codes(y);
-            if (c < p.dim) {
-                *reinterpret_cast<u32x2*>(p.codes + first + c) = q.codes;
+            if (c < dim) {
+                store16<kStream>(reinterpret_cast<u32x2*>(p.codes + first + c), q.codes);
                 if (threadIdx.x % kBlockLanes == 0) p.scales[(uint64_t)row * p.blocks + c / kBlockCols] = q.scale;
             }
         }
@@ -135,32 +138,35 @@ struct NormGradParams {
     float inv_dim;
 };
 
-// A team (the threads that hold a row) takes rows team, team + teams, ...
-template <uint32_t kRounds, uint32_t kMost>
-__global__ __launch_bounds__(64 * kMost) void rms_norm_grad_kernel(NormGradParams p) {
-    extern __shared__ __align__(16) float lds[];   // dw of one team; blockDim.y > 1 only
+// A team (the threads that hold a row) takes rows team, team + teams, ...  All teams take as many turns, as those of a
+// workgroup may wait for each other; past the last row they read nothing and write nothing.
+template <uint32_t kRounds, bool kStream>
+__global__ __launch_bounds__(64 * kMaxWaves) void rms_norm_grad_kernel(NormGradParams p) {
+    extern __shared__ __align__(16) float lds[];   // dw of one team, where there are several
     __shared__ float sums[2][kMaxWaves];
     const uint32_t team = __builtin_amdgcn_readfirstlane(blockIdx.x * blockDim.y + threadIdx.y);
     u32x4 w[kRounds];
     float dw[kRounds][8];
 #pragma unroll
     for (uint32_t k = 0; k < kRounds; ++k) {
-        w[k] = load8(p.weight, (k * blockDim.x + threadIdx.x) * 8, p.dim);
+        w[k] = load8<false>(p.weight, (k * blockDim.x + threadIdx.x) * 8, p.dim);
 #pragma unroll
         for (uint32_t i = 0; i < 8; ++i) dw[k][i] = 0.0f;
     }
     uint32_t turn = 0;
-    for (uint32_t row = team; row < p.n; row += p.teams, turn ^= 1) {
+    for (uint32_t from = 0; from < p.n; from += p.teams, turn ^= 1) {
+        const uint32_t row = from + team;
+        const uint32_t dim = row < p.n ? p.dim : 0;
         const uint64_t first = (uint64_t)row * p.dim;
         u32x4 dy[kRounds], h[kRounds], add[kRounds];
 #pragma unroll
         for (uint32_t k = 0; k < kRounds; ++k) {
             const uint32_t c = (k * blockDim.x + threadIdx.x) * 8;
-            dy[k] = load8(p.dy + first, c, p.dim);
-            h[k] = load8(p.h + first, c, p.dim);
-            add[k] = p.dsum ? load8(p.dsum + first, c, p.dim) : u32x4{0, 0, 0, 0};
+            dy[k] = load8<kStream>(p.dy + first, c, dim);
+            h[k] = load8<kStream>(p.h + first, c, dim);
+            add[k] = p.dsum ? load8<kStream>(p.dsum + first, c, dim) : u32x4{0, 0, 0, 0};
         }
-        const float rstd = p.rstd[row];
+        const float rstd = row < p.n ? p.rstd[row] : 0.0f;
         float along = 0.0f;
 #pragma unroll
         for (uint32_t k = 0; k < kRounds; ++k) {
@@ -188,7 +194,7 @@ __global__ __launch_bounds__(64 * kMost) void rms_norm_grad_kernel(NormGradParam
 #pragma unroll
             for (uint32_t i = 0; i < 8; ++i)
                 out[i] = __builtin_fmaf(rstd, __builtin_fmaf(-along, u[i] * rstd, d[i] * g[i]), out[i]);
-            if (c < p.dim) *reinterpret_cast<u32x4*>(p.dh + first + c) = pack_bf16(out);
+            if (c < dim) store16<kStream>(reinterpret_cast<u32x4*>(p.dh + first + c), pack_bf16(out));
         }
     }
     if (!p.part) return;
@@ -198,7 +204,7 @@ __global__ __launch_bounds__(64 * kMost) void rms_norm_grad_kernel(NormGradParam
             for (uint32_t k = 0; k < kRounds; ++k)
 #pragma unroll
                 for (uint32_t i = 0; i < 2; ++i)
-                    *reinterpret_cast<f32x4*>(lds + ((k * 2 + i) * 64 + threadIdx.x) * 4) =
+                    *reinterpret_cast<f32x4*>(lds + ((k * 2 + i) * blockDim.x + threadIdx.x) * 4) =
                         f32x4{dw[k][4 * i], dw[k][4 * i + 1], dw[k][4 * i + 2], dw[k][4 * i + 3]};
         __syncthreads();
         if (threadIdx.y == 0)
@@ -206,7 +212,7 @@ __global__ __launch_bounds__(64 * kMost) void rms_norm_grad_kernel(NormGradParam
             for (uint32_t k = 0; k < kRounds; ++k)
 #pragma unroll
                 for (uint32_t i = 0; i < 2; ++i) {
-                    const f32x4 v = *reinterpret_cast<const f32x4*>(lds + ((k * 2 + i) * 64 + threadIdx.x) * 4);
+                    const f32x4 v = *reinterpret_cast<const f32x4*>(lds + ((k * 2 + i) * blockDim.x + threadIdx.x) * 4);
 #pragma unroll
                     for (uint32_t e = 0; e < 4; ++e) dw[k][4 * i + e] += v[e];
                 }
@@ -223,7 +229,7 @@ __global__ __launch_bounds__(64 * kMost) void rms_norm_grad_kernel(NormGradParam
     }
 }
 
-constexpr uint32_t kJoinLanes = 8, kJoinSlices = 32;   // 4 columns per lane
+constexpr uint32_t kJoinLanes = 8, kJoinSlices = 64;   // 4 columns per lane
 
 // dw: the partial rows of each slice in order, then the slices in order.
 __global__ __launch_bounds__(kJoinLanes * kJoinSlices) void rms_norm_join_kernel(const float* part, uint32_t parts,
@@ -236,6 +242,7 @@ __global__ __launch_bounds__(kJoinLanes * kJoinSlices) void rms_norm_join_kernel
     const uint32_t per = (parts + kJoinSlices - 1) / kJoinSlices, begin = slice * per;
     const uint32_t end = begin + per < parts ? begin + per : parts;
     if (c < dim)
+#pragma unroll 8
         for (uint32_t k = begin; k < end; ++k) v += *reinterpret_cast<const f32x4*>(part + (uint64_t)k * dim + c);
     shared[threadIdx.x] = v;
     __syncthreads();
@@ -247,21 +254,24 @@ __global__ __launch_bounds__(kJoinLanes * kJoinSlices) void rms_norm_join_kernel
 
 uint32_t cdiv(uint64_t a, uint32_t b) { return (uint32_t)((a + b - 1) / b); }
 
-// How a row is held: by `waves` waves in 1, 2, 4 or 8 rounds.
+// How a row is held: by as many waves as take kRoundsAim rounds, up to 16 (rows past 16384 columns: in 4 or 8 rounds);
+// several short rows make a workgroup of 4 waves.  Measured (us; 8 rounds, 4, 2 and, of the norm, 1):
+//   norm, 8192 x 8192, codes       81.2  79.7  78.3  80.2      gradient, 16384 x 4096    114  94  96
+//   norm, 16384 x 4096, bf16       90.5  89.7  87.8  86.4      gradient, 1000 x 4096    17.7  16.9  14.6
+//   norm, 1 x 4096, codes           4.7   3.6   3.0   3.0      gradient, 64 x 4096       9.9  7.6  6.9
+// 512 workgroups of the gradient each leave a partial row (16384 x 4096: 256 take 112 us, 1024 111).
+constexpr uint32_t kRoundsAim = 2;
 struct RowShape {
-    uint32_t waves, rounds, rows;   // rows per workgroup: 4 where a row is one wave
+    uint32_t waves, rounds, rows;
 };
 RowShape row_shape(uint32_t dim) {
     const uint32_t lanes = cdiv(dim, 8);
-    RowShape s{};
-    s.waves = 1;
-    while (s.waves * 64 * 8 < lanes) s.waves *= 2;
-    s.rounds = 1;
+    RowShape s{1, 1, 1};
+    while (s.waves * 64 * kRoundsAim < lanes && s.waves < kMaxWaves) s.waves *= 2;
     while (s.waves * 64 * s.rounds < lanes) s.rounds *= 2;
-    s.rows = s.waves == 1 ? 4 : 1;
+    s.rows = s.waves < 4 ? 4 / s.waves : 1;
     return s;
 }
-
 constexpr uint32_t kGradGroups = 512;
 uint32_t grad_groups(uint64_t n, const RowShape& s) {
     const uint32_t groups = cdiv(n, s.rows);
@@ -275,16 +285,19 @@ bool sizes_fit(uint64_t n, uint32_t dim) {
 template <uint32_t kRounds>
 void launch_norm(const NormParams& p, const RowShape& r, hipStream_t s) {
     const dim3 grid(cdiv(p.n, r.rows)), block(64 * r.waves, r.rows);
-    if (p.codes) hipLaunchKernelGGL((rms_norm_kernel<kRounds, true>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((rms_norm_kernel<kRounds, false>), grid, block, 0, s, p);
+    const bool streams = (uint64_t)p.n * p.dim * (2 + (p.residual ? 4 : 0) + (p.y ? 2 : 0) + (p.codes ? 1 : 0)) > kCacheBytes;
+    const auto kernel = p.codes ? (streams ? rms_norm_kernel<kRounds, true, true> : rms_norm_kernel<kRounds, true, false>)
+                                : (streams ? rms_norm_kernel<kRounds, false, true> : rms_norm_kernel<kRounds, false, false>);
+    hipLaunchKernelGGL(kernel, grid, block, 0, s, p);
 }
 
 template <uint32_t kRounds>
 void launch_grad(const NormGradParams& p, const RowShape& r, uint32_t groups, hipStream_t s) {
-    const uint32_t bytes = r.rows > 1 ? kRounds * 64 * 8 * 4 : 0;
+    const uint32_t bytes = r.rows > 1 ? r.waves * kRounds * 64 * 8 * 4 : 0;
     const dim3 grid(groups), block(64 * r.waves, r.rows);
-    if (r.waves <= 4) hipLaunchKernelGGL((rms_norm_grad_kernel<kRounds, 4>), grid, block, bytes, s, p);
-    else hipLaunchKernelGGL((rms_norm_grad_kernel<kRounds, kMaxWaves>), grid, block, bytes, s, p);
+    const bool streams = (uint64_t)p.n * p.dim * (4 + (p.dsum ? 2 : 0) + (p.dh ? 2 : 0)) > kCacheBytes;
+    const auto kernel = streams ? rms_norm_grad_kernel<kRounds, true> : rms_norm_grad_kernel<kRounds, false>;
+    hipLaunchKernelGGL(kernel, grid, block, bytes, s, p);
 }
 
 }  // namespace

@@ -729,7 +729,7 @@ def ce_grad_async(h_dev, W_dev, targets_dev, tokens: int, vocab: int, dim: int, 
 
 FP8_BLOCK = 128   # columns (and rows of a matrix) that share a scale
 MAX_GRADS = 1 << 20
-MAX_GRAD_NUMEL = 1 << 38
+MAX_GRAD_NUMEL = 1 << 34
 _CODE_KIND = "float8_e4m3fn"
 
 

@@ -132,7 +132,7 @@ def test_clip_refusals(wc):
     assert lib.wc_clip_grads_work_bytes(good, 3, ctypes.byref(b)) == wc.WC_OK and b.value > 0
     need = b.value
     for bad in ((0, P, 1, 0), (P, 0, 1, 0), (P + 2, P, 1, 0), (P, P + 2, 1, 0), (P + 1, P, 1, 1), (P, P, 1, 2),
-                (P, P, (1 << 38) + 1, 0)):
+                (P, P, wc.MAX_GRAD_NUMEL + 1, 0)):
         assert lib.wc_clip_grads_work_bytes(_grads(wc, bad), 1, ctypes.byref(b)) == INV, bad
         assert lib.wc_clip_grads_async(_grads(wc, bad), 1, 1.0, P, P, 1 << 40, None) == INV, bad
     assert lib.wc_clip_grads_work_bytes(good, 3, None) == INV
@@ -143,8 +143,8 @@ def test_clip_refusals(wc):
     for bad in (dict(max=-1.0), dict(max=math.nan), dict(norm=0), dict(norm=P + 2), dict(work=0), dict(work=P + 128),
                 dict(work_bytes=need - 1)):
         assert call(**bad) == INV, bad
-    most = _grads(wc, *[(P, P, 1 << 38, 0)] * 200)
-    assert lib.wc_clip_grads_work_bytes(most, 200, ctypes.byref(b)) == wc.WC_OK and b.value < 1 << 20
+    most = _grads(wc, *[(P, P, wc.MAX_GRAD_NUMEL, 0)] * 200)
+    assert lib.wc_clip_grads_work_bytes(most, 200, ctypes.byref(b)) == wc.WC_OK and b.value < 1 << 24
 
 
 # ---- the binding's checks of tensors -----------------------------------------------
