@@ -138,8 +138,55 @@ struct NormGradParams {
     float inv_dim;
 };
 
-// A team (the threads that hold a row) takes rows team, team + teams, ...  All teams take as many turns, as those of a
-// workgroup may wait for each other; past the last row they read nothing and write nothing.
+// One row's dh, by the blockDim.x threads that hold it, and each dy u to `take(round, column of 8, value)`.  Past the last
+// row nothing is read or written: others of the workgroup may wait.
+template <uint32_t kRounds, bool kStream, class Take>
+__device__ __forceinline__ void grad_row(const NormGradParams& p, const u32x4 (&w)[kRounds], uint32_t row, float* sums,
+                                         Take take) {
+    const uint32_t dim = row < p.n ? p.dim : 0;
+    const uint64_t first = (uint64_t)row * p.dim;
+    u32x4 dy[kRounds], h[kRounds], add[kRounds];
+#pragma unroll
+    for (uint32_t k = 0; k < kRounds; ++k) {
+        const uint32_t c = (k * blockDim.x + threadIdx.x) * 8;
+        dy[k] = load8<kStream>(p.dy + first, c, dim);
+        h[k] = load8<kStream>(p.h + first, c, dim);
+        add[k] = p.dsum ? load8<kStream>(p.dsum + first, c, dim) : u32x4{0, 0, 0, 0};
+    }
+    const float rstd = row < p.n ? p.rstd[row] : 0.0f;
+    float along = 0.0f;
+#pragma unroll
+    for (uint32_t k = 0; k < kRounds; ++k) {
+        float d[8], u[8], g[8];
+        unpack_bf16(dy[k], d);
+        unpack_bf16(h[k], u);
+        unpack_bf16(w[k], g);
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) {
+            const float du = d[i] * (u[i] * rstd);
+            take(k, i, du);
+            along = __builtin_fmaf(du, g[i], along);
+        }
+    }
+    if (!p.dh) return;
+    along = row_sum(along, sums) * p.inv_dim;
+#pragma unroll
+    for (uint32_t k = 0; k < kRounds; ++k) {
+        const uint32_t c = (k * blockDim.x + threadIdx.x) * 8;
+        float d[8], u[8], g[8], out[8];
+        unpack_bf16(dy[k], d);
+        unpack_bf16(h[k], u);
+        unpack_bf16(w[k], g);
+        unpack_bf16(add[k], out);
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i)
+            out[i] = __builtin_fmaf(rstd, __builtin_fmaf(-along, u[i] * rstd, d[i] * g[i]), out[i]);
+        if (c < dim) store16<kStream>(reinterpret_cast<u32x4*>(p.dh + first + c), pack_bf16(out));
+    }
+}
+
+// A team (the threads that hold a row) takes rows team, team + teams, ...; all teams take as many turns, as those of a
+// workgroup may wait for each other.
 template <uint32_t kRounds, bool kStream>
 __global__ __launch_bounds__(64 * kMaxWaves) void rms_norm_grad_kernel(NormGradParams p) {
     extern __shared__ __align__(16) float lds[];   // dw of one team, where there are several
@@ -154,49 +201,9 @@ __global__ __launch_bounds__(64 * kMaxWaves) void rms_norm_grad_kernel(NormGradP
         for (uint32_t i = 0; i < 8; ++i) dw[k][i] = 0.0f;
     }
     uint32_t turn = 0;
-    for (uint32_t from = 0; from < p.n; from += p.teams, turn ^= 1) {
-        const uint32_t row = from + team;
-        const uint32_t dim = row < p.n ? p.dim : 0;
-        const uint64_t first = (uint64_t)row * p.dim;
-        u32x4 dy[kRounds], h[kRounds], add[kRounds];
-#pragma unroll
-        for (uint32_t k = 0; k < kRounds; ++k) {
-            const uint32_t c = (k * blockDim.x + threadIdx.x) * 8;
-            dy[k] = load8<kStream>(p.dy + first, c, dim);
-            h[k] = load8<kStream>(p.h + first, c, dim);
-            add[k] = p.dsum ? load8<kStream>(p.dsum + first, c, dim) : u32x4{0, 0, 0, 0};
-        }
-        const float rstd = row < p.n ? p.rstd[row] : 0.0f;
-        float along = 0.0f;
-#pragma unroll
-        for (uint32_t k = 0; k < kRounds; ++k) {
-            float d[8], u[8], g[8];
-            unpack_bf16(dy[k], d);
-            unpack_bf16(h[k], u);
-            unpack_bf16(w[k], g);
-#pragma unroll
-            for (uint32_t i = 0; i < 8; ++i) {
-                const float du = d[i] * (u[i] * rstd);
-                dw[k][i] += du;
-                along = __builtin_fmaf(du, g[i], along);
-            }
-        }
-        if (!p.dh) continue;
-        along = row_sum(along, sums[turn]) * p.inv_dim;
-#pragma unroll
-        for (uint32_t k = 0; k < kRounds; ++k) {
-            const uint32_t c = (k * blockDim.x + threadIdx.x) * 8;
-            float d[8], u[8], g[8], out[8];
-            unpack_bf16(dy[k], d);
-            unpack_bf16(h[k], u);
-            unpack_bf16(w[k], g);
-            unpack_bf16(add[k], out);
-#pragma unroll
-            for (uint32_t i = 0; i < 8; ++i)
-                out[i] = __builtin_fmaf(rstd, __builtin_fmaf(-along, u[i] * rstd, d[i] * g[i]), out[i]);
-            if (c < dim) store16<kStream>(reinterpret_cast<u32x4*>(p.dh + first + c), pack_bf16(out));
-        }
-    }
+    for (uint32_t from = 0; from < p.n; from += p.teams, turn ^= 1)
+        grad_row<kRounds, kStream>(p, w, from + team, sums[turn],
+                                   [&](uint32_t k, uint32_t i, float du) { dw[k][i] += du; });
     if (!p.part) return;
     for (uint32_t y = 1; y < blockDim.y; ++y) {   // the workgroup's teams in order
         if (threadIdx.y == y)
@@ -227,6 +234,59 @@ __global__ __launch_bounds__(64 * kMaxWaves) void rms_norm_grad_kernel(NormGradP
         *reinterpret_cast<f32x4*>(part + c) = f32x4{dw[k][0], dw[k][1], dw[k][2], dw[k][3]};
         *reinterpret_cast<f32x4*>(part + c + 4) = f32x4{dw[k][4], dw[k][5], dw[k][6], dw[k][7]};
     }
+}
+
+// Few rows: one launch.  The first workgroups take a row (or several short ones) each, the others 64 columns of dw, for
+// which they read dy and h again, from the caches, 8 columns per lane and the rows in slices: each slice's sum in order,
+// then the slices in order.
+constexpr uint32_t kFewCols = 64;
+constexpr uint32_t kAhead = 8;   // rows of a slice on their way at a time
+template <uint32_t kRounds>
+__global__ __launch_bounds__(64 * kMaxWaves) void rms_norm_grad_few_kernel(NormGradParams p, uint32_t row_groups, float* dw,
+                                                                          int accumulate) {
+    __shared__ __align__(16) float lds[64 * kMaxWaves * 8];
+    if (blockIdx.x < row_groups) {
+        u32x4 w[kRounds];
+#pragma unroll
+        for (uint32_t k = 0; k < kRounds; ++k) w[k] = load8<false>(p.weight, (k * blockDim.x + threadIdx.x) * 8, p.dim);
+        const uint32_t row = __builtin_amdgcn_readfirstlane(blockIdx.x * blockDim.y + threadIdx.y);
+        grad_row<kRounds, false>(p, w, row, lds, [](uint32_t, uint32_t, float) {});
+        return;
+    }
+    const uint32_t thread = threadIdx.y * blockDim.x + threadIdx.x, slices = blockDim.x * blockDim.y / 8;
+    const uint32_t lane = thread % 8, slice = thread / 8;
+    const uint32_t c0 = (blockIdx.x - row_groups) * kFewCols, c = c0 + lane * 8;
+    float sum[8];
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) sum[i] = 0.0f;
+    for (uint32_t from = slice; from < p.n; from += kAhead * slices) {
+        u32x4 dy[kAhead], h[kAhead];
+        float rstd[kAhead];
+#pragma unroll
+        for (uint32_t k = 0; k < kAhead; ++k) {
+            const uint32_t row = from + k * slices, dim = row < p.n ? p.dim : 0;
+            dy[k] = load8<false>(p.dy + (uint64_t)row * p.dim, c, dim);
+            h[k] = load8<false>(p.h + (uint64_t)row * p.dim, c, dim);
+            rstd[k] = row < p.n ? p.rstd[row] : 0.0f;
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < kAhead; ++k) {
+            float d[8], u[8];
+            unpack_bf16(dy[k], d);
+            unpack_bf16(h[k], u);
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i) sum[i] += d[i] * (u[i] * rstd[k]);
+        }
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < 2; ++i)
+        *reinterpret_cast<f32x4*>(lds + thread * 8 + i * 4) =
+            f32x4{sum[4 * i], sum[4 * i + 1], sum[4 * i + 2], sum[4 * i + 3]};
+    __syncthreads();
+    if (thread >= kFewCols || c0 + thread >= p.dim) return;
+    float v = lds[thread];
+    for (uint32_t k = 1; k < slices; ++k) v += lds[k * kFewCols + thread];
+    dw[c0 + thread] = accumulate ? dw[c0 + thread] + v : v;
 }
 
 constexpr uint32_t kJoinLanes = 8, kJoinSlices = 64;   // 4 columns per lane
@@ -273,6 +333,9 @@ RowShape row_shape(uint32_t dim) {
     return s;
 }
 constexpr uint32_t kGradGroups = 512;
+// Up to so many rows the gradient is one launch (us, in two and in one, with dweight): 64 x 4096 7.0 and 3.6, 512 x 2048
+// 9.6 and 6.8, 512 x 8192 19.0 and 12.1, 1000 x 4096 15.3 and 13.5, 1024 x 1024 9.5 and 10.0; a launch costs its caller 3.
+constexpr uint64_t kFewRows = 1024;
 uint32_t grad_groups(uint64_t n, const RowShape& s) {
     const uint32_t groups = cdiv(n, s.rows);
     return groups < kGradGroups ? groups : kGradGroups;
@@ -292,12 +355,19 @@ void launch_norm(const NormParams& p, const RowShape& r, hipStream_t s) {
 }
 
 template <uint32_t kRounds>
-void launch_grad(const NormGradParams& p, const RowShape& r, uint32_t groups, hipStream_t s) {
+void launch_grad(const NormGradParams& p, const RowShape& r, uint32_t groups, float* dweight, int accumulate, bool few,
+                 hipStream_t s) {
+    const dim3 block(64 * r.waves, r.rows);
+    if (few) {
+        const uint32_t row_groups = p.dh ? cdiv(p.n, r.rows) : 0;
+        hipLaunchKernelGGL((rms_norm_grad_few_kernel<kRounds>), dim3(row_groups + cdiv(p.dim, kFewCols)), block, 0, s, p,
+                           row_groups, dweight, accumulate);
+        return;
+    }
     const uint32_t bytes = r.rows > 1 ? r.waves * kRounds * 64 * 8 * 4 : 0;
-    const dim3 grid(groups), block(64 * r.waves, r.rows);
     const bool streams = (uint64_t)p.n * p.dim * (4 + (p.dsum ? 2 : 0) + (p.dh ? 2 : 0)) > kCacheBytes;
     const auto kernel = streams ? rms_norm_grad_kernel<kRounds, true> : rms_norm_grad_kernel<kRounds, false>;
-    hipLaunchKernelGGL(kernel, grid, block, bytes, s, p);
+    hipLaunchKernelGGL(kernel, dim3(groups), block, bytes, s, p);
 }
 
 }  // namespace
@@ -349,16 +419,18 @@ extern "C" int wc_rms_norm_grad_async(const uint16_t* dy, const uint16_t* h, con
         return WC_ERR_INVALID_ARG;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     NormGradParams p{};
+    // rows that are being overwritten cannot be read again
+    const bool few = n != 0 && n <= kFewRows && dweight && dh != dy && dh != h;
     if (n != 0) {
         p.dy = dy, p.h = h, p.weight = weight, p.rstd = rstd, p.dsum = dsum, p.dh = dh;
         p.part = dweight ? static_cast<float*>(work_dev) : nullptr;
         p.n = (uint32_t)n, p.dim = dim, p.teams = groups * r.rows, p.inv_dim = 1.0f / (float)dim;
-        if (r.rounds == 1) launch_grad<1>(p, r, groups, s);
-        else if (r.rounds == 2) launch_grad<2>(p, r, groups, s);
-        else if (r.rounds == 4) launch_grad<4>(p, r, groups, s);
-        else launch_grad<8>(p, r, groups, s);
+        if (r.rounds == 1) launch_grad<1>(p, r, groups, dweight, accumulate, few, s);
+        else if (r.rounds == 2) launch_grad<2>(p, r, groups, dweight, accumulate, few, s);
+        else if (r.rounds == 4) launch_grad<4>(p, r, groups, dweight, accumulate, few, s);
+        else launch_grad<8>(p, r, groups, dweight, accumulate, few, s);
     }
-    if (dweight)   // of no tokens: zeros
+    if (dweight && !few)   // of no tokens: zeros
         hipLaunchKernelGGL(rms_norm_join_kernel, dim3(cdiv(dim, kJoinLanes * 4)), dim3(kJoinLanes * kJoinSlices), 0, s,
                            p.part, n ? groups : 0, dim, dweight, accumulate);
     return hipGetLastError() == hipSuccess ? WC_OK : WC_ERR_HIP;

@@ -543,15 +543,17 @@ def _bytes_ok(t, nbytes: int, device, what: str, call: str, kind: str = "") -> i
     """The device pointer of a tensor that _require accepts (or of a raw integer pointer).  kind: the floating type
     that the call reads or writes ("bf16", "f32"), or "words" for whole numbers alone; a tensor of whole numbers is
     taken as the words that it holds in any case.  Empty: any type."""
+    try:   # what every call of a good tensor takes, without a further look
+        found = _KINDS[t.dtype]
+        if ((found == kind or found == "words" or not kind) and t.is_cuda and t.get_device() == device and
+                t.nbytes >= nbytes and t.is_contiguous()):
+            return t.data_ptr()
+    except (AttributeError, KeyError):
+        pass
     if kind and hasattr(t, "dtype"):
-        found = _KINDS.get(t.dtype) or _kind_of(t.dtype)
+        found = _kind_of(t.dtype)
         if found != kind and found != "words":
             raise WCError(WC_ERR_INVALID_ARG, call, f"{what} is {t.dtype}, where {kind} is read or written")
-    try:
-        if t.is_cuda and t.get_device() == device and t.nbytes >= nbytes and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
     _require(t, nbytes, device, what, call)
     return _ptr(t)
 
