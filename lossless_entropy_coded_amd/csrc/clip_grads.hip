@@ -32,11 +32,13 @@ namespace wc {
 namespace {
 
 constexpr uint32_t kThreads = 256;
-constexpr uint32_t kBatch = 96;            // tensors per launch: 32 bytes of arguments each
+// Tensors per launch: 32 bytes of arguments each, which a launch copies: 24 of them cost their caller 1.3 us less than 96.
+constexpr uint32_t kBatch = 96, kSmallBatch = 24;
 constexpr uint32_t kGroups = 8192;         // workgroups of a norm's launch at most
 constexpr uint32_t kOwnParts = 1024;
 constexpr uint32_t kMostChunks = 1u << 23;
-constexpr uint32_t kRounds = 4;            // 16-byte loads per thread on their way
+constexpr uint32_t kMostChunk = 16384;     // bytes of a chunk
+constexpr uint32_t kRounds = kMostChunk / 16 / kThreads;   // 16-byte loads per thread, all on their way
 
 struct ClipTensor {
     const void* g;
@@ -46,8 +48,9 @@ struct ClipTensor {
     uint32_t kind;
 };
 
+template <uint32_t kTensors>
 struct ClipParams {
-    ClipTensor tensor[kBatch];
+    ClipTensor tensor[kTensors];
     double* part;
     uint32_t tensors, chunks, chunk_bytes;
     uint32_t part_at;   // the batch's first partial sum
@@ -55,16 +58,20 @@ struct ClipParams {
     float max_norm;
     float* norm;        // written by the first workgroup, where not NULL
 };
-static_assert(sizeof(ClipParams) <= 4096, "kernel arguments");
+static_assert(sizeof(ClipParams<kBatch>) <= 4096, "kernel arguments");
 
-__device__ __forceinline__ uint32_t tensor_of(const ClipParams& p, uint32_t chunk) {
-    uint32_t lo = 0, hi = p.tensors;   // first[lo] <= chunk < first[hi]
-    while (hi - lo > 1) {
-        const uint32_t mid = (lo + hi) / 2;
-        if (p.tensor[mid].first <= chunk) lo = mid;
-        else hi = mid;
+// The tensor of a chunk: the last one whose first chunk is not behind it.  Each lane looks at one tensor: a binary search
+// would be a chain of loads.
+template <class Params>
+__device__ __forceinline__ uint32_t tensor_of(const Params& p, uint32_t chunk) {
+    constexpr uint32_t kTensors = sizeof(p.tensor) / sizeof(p.tensor[0]);
+    uint32_t found = 0;
+#pragma unroll
+    for (uint32_t from = 0; from < kTensors; from += 64) {
+        const uint32_t i = from + (threadIdx.x & 63u);
+        found += __popcll(__ballot(i < p.tensors && p.tensor[i < kTensors ? i : 0].first <= chunk));
     }
-    return lo;
+    return __builtin_amdgcn_readfirstlane(found - 1);
 }
 
 // The workgroup's sum of v, in every thread; always in the same order.
@@ -82,19 +89,30 @@ __device__ __forceinline__ double group_sum(double v) {
 
 __device__ __forceinline__ double square(float f) { return (double)f * (double)f; }
 
-// Calls wide(k-th 16 bytes' index within the chunk's tensor) or, for what is not whole 16 bytes (or not aligned to
-// them), one(element).
-template <class Wide, class One>
-__device__ __forceinline__ void for_chunk(const ClipParams& p, const ClipTensor& t, uint32_t chunk, Wide wide, One one) {
-    const uint32_t size = t.kind == WC_OUT_F32 ? 4 : 2;
-    const uint32_t per = p.chunk_bytes / size;
-    const uint64_t begin = (uint64_t)(chunk - t.first) * per;
-    const uint64_t left = t.numel - begin;
-    const uint32_t count = left < per ? (uint32_t)left : per;
-    const bool whole = ((reinterpret_cast<uintptr_t>(t.g) | reinterpret_cast<uintptr_t>(t.out)) & 15u) == 0;
-    const uint32_t lanes = whole ? count / (16 / size) : 0;
-    if (lanes) wide(begin / (16 / size), lanes);
-    for (uint32_t i = lanes * (16 / size) + threadIdx.x; i < count; i += kThreads) one(begin + i);
+// A chunk's elements begin, .. + count; the first `lanes` 16 bytes of them are taken whole (none, if the tensor is not
+// aligned to them).
+struct Chunk {
+    uint64_t begin, wide;   // wide: the first of the 16 bytes, within the tensor
+    uint32_t count, lanes, per_lane;
+    template <class Params>
+    __device__ __forceinline__ Chunk(const Params& p, const ClipTensor& t, uint32_t chunk) {
+        const uint32_t size = t.kind == WC_OUT_F32 ? 4 : 2, per = p.chunk_bytes / size;
+        per_lane = 16 / size;
+        begin = (uint64_t)(chunk - t.first) * per;
+        const uint64_t left = t.numel - begin;
+        count = left < per ? (uint32_t)left : per;
+        lanes = ((reinterpret_cast<uintptr_t>(t.g) | reinterpret_cast<uintptr_t>(t.out)) & 15u) == 0 ? count / per_lane : 0;
+        wide = begin / per_lane;
+    }
+};
+template <bool kStream>
+__device__ __forceinline__ void load_chunk(const ClipTensor& t, const Chunk& c, u32x4 (&w)[kRounds]) {
+    const u32x4* const g = static_cast<const u32x4*>(t.g) + c.wide;
+#pragma unroll
+    for (uint32_t k = 0; k < kRounds; ++k) {
+        const uint32_t i = threadIdx.x + k * kThreads;
+        w[k] = i < c.lanes ? load16<kStream>(g + i) : u32x4{0, 0, 0, 0};
+    }
 }
 
 __device__ __forceinline__ float value(const ClipTensor& t, uint64_t i) {
@@ -102,30 +120,22 @@ __device__ __forceinline__ float value(const ClipTensor& t, uint64_t i) {
                                 : __uint_as_float((uint32_t) static_cast<const uint16_t*>(t.g)[i] << 16);
 }
 
-template <bool kStream>
-__global__ __launch_bounds__(kThreads) void clip_norm_kernel(ClipParams p) {
+template <class Params, bool kStream>
+__global__ __launch_bounds__(kThreads) void clip_norm_kernel(Params p) {
     double sum = 0.0;
     for (uint32_t chunk = blockIdx.x; chunk < p.chunks; chunk += gridDim.x) {
         const ClipTensor& t = p.tensor[tensor_of(p, chunk)];
-        for_chunk(
-            p, t, chunk,
-            [&](uint64_t from, uint32_t lanes) {
-                const u32x4* const g = static_cast<const u32x4*>(t.g) + from;
-                for (uint32_t i = threadIdx.x; i < lanes; i += kThreads * kRounds) {
-                    u32x4 w[kRounds];
+        const Chunk c(p, t, chunk);
+        u32x4 w[kRounds];
+        load_chunk<kStream>(t, c, w);
 #pragma unroll
-                    for (uint32_t k = 0; k < kRounds; ++k)
-                        w[k] = i + k * kThreads < lanes ? load16<kStream>(g + i + k * kThreads) : u32x4{0, 0, 0, 0};
+        for (uint32_t k = 0; k < kRounds; ++k)
 #pragma unroll
-                    for (uint32_t k = 0; k < kRounds; ++k)
-#pragma unroll
-                        for (uint32_t e = 0; e < 4; ++e) {
-                            if (t.kind == WC_OUT_F32) sum += square(__uint_as_float(w[k][e]));
-                            else sum += square(bf16_lo(w[k][e])) + square(bf16_hi(w[k][e]));
-                        }
-                }
-            },
-            [&](uint64_t i) { sum += square(value(t, i)); });
+            for (uint32_t e = 0; e < 4; ++e) {
+                if (t.kind == WC_OUT_F32) sum += square(__uint_as_float(w[k][e]));
+                else sum += square(bf16_lo(w[k][e])) + square(bf16_hi(w[k][e]));
+            }
+        for (uint32_t i = c.lanes * c.per_lane + threadIdx.x; i < c.count; i += kThreads) sum += square(value(t, c.begin + i));
     }
     sum = group_sum(sum);
     if (threadIdx.x == 0) p.part[p.part_at + blockIdx.x] = sum;
@@ -146,8 +156,14 @@ __global__ __launch_bounds__(kJoinThreads) void clip_join_kernel(double* part, u
     part[parts] = v;
 }
 
-template <bool kStream>
-__global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipParams p) {
+template <class Params, bool kStream>
+__global__ __launch_bounds__(kThreads) void clip_scale_kernel(Params p) {
+    const bool any = blockIdx.x < p.chunks;   // else: a list without elements, its norm alone
+    const uint32_t chunk = any ? p.chunks - 1 - blockIdx.x : 0;
+    const ClipTensor& t = p.tensor[any ? tensor_of(p, chunk) : 0];
+    const Chunk c(p, t, chunk);
+    u32x4 w[kRounds];
+    if (!kStream && any) load_chunk<false>(t, c, w);   // beside the norm's sum; of large lists only what is needed
     double sum = 0.0;
     for (uint32_t i = threadIdx.x; i < p.parts; i += kThreads) sum += p.part[i];
     const double total = sqrt(group_sum(sum));
@@ -155,43 +171,31 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipParams p) {
     if (p.norm && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = norm;
     const bool clips = norm > p.max_norm && norm < INFINITY;
     const float factor = clips ? (float)((double)p.max_norm / total) : 1.0f;
-    if (blockIdx.x >= p.chunks) return;   // a list without elements
-    const uint32_t chunk = p.chunks - 1 - blockIdx.x;
-    const ClipTensor& t = p.tensor[tensor_of(p, chunk)];
-    if (!clips && t.g == t.out) return;
-    for_chunk(
-        p, t, chunk,
-        [&](uint64_t from, uint32_t lanes) {
-            const u32x4* const g = static_cast<const u32x4*>(t.g) + from;
-            u32x4* const out = static_cast<u32x4*>(t.out) + from;
-            for (uint32_t i = threadIdx.x; i < lanes; i += kThreads * kRounds) {
-                u32x4 w[kRounds];
+    if (!any || (!clips && t.g == t.out)) return;
+    if (kStream) load_chunk<true>(t, c, w);
+    u32x4* const out = static_cast<u32x4*>(t.out) + c.wide;
 #pragma unroll
-                for (uint32_t k = 0; k < kRounds; ++k)
-                    w[k] = i + k * kThreads < lanes ? load16<kStream>(g + i + k * kThreads) : u32x4{0, 0, 0, 0};
+    for (uint32_t k = 0; k < kRounds; ++k) {
+        const uint32_t i = threadIdx.x + k * kThreads;
+        if (i >= c.lanes) break;
+        if (clips) {
 #pragma unroll
-                for (uint32_t k = 0; k < kRounds; ++k) {
-                    if (i + k * kThreads >= lanes) break;
-                    if (clips) {
-#pragma unroll
-                        for (uint32_t e = 0; e < 4; ++e)
-                            w[k][e] = t.kind == WC_OUT_F32 ? __float_as_uint(__uint_as_float(w[k][e]) * factor)
-                                                           : pack_bf16(bf16_lo(w[k][e]) * factor, bf16_hi(w[k][e]) * factor);
-                    }
-                    store16<kStream>(out + i + k * kThreads, w[k]);
-                }
-            }
-        },
-        [&](uint64_t i) {
-            if (t.kind == WC_OUT_F32) {
-                const float v = static_cast<const float*>(t.g)[i];
-                static_cast<float*>(t.out)[i] = clips ? v * factor : v;
-            } else {
-                const uint16_t v = static_cast<const uint16_t*>(t.g)[i];
-                static_cast<uint16_t*>(t.out)[i] =
-                    clips ? (uint16_t)pack_bf16(__uint_as_float((uint32_t)v << 16) * factor, 0.0f) : v;
-            }
-        });
+            for (uint32_t e = 0; e < 4; ++e)
+                w[k][e] = t.kind == WC_OUT_F32 ? __float_as_uint(__uint_as_float(w[k][e]) * factor)
+                                               : pack_bf16(bf16_lo(w[k][e]) * factor, bf16_hi(w[k][e]) * factor);
+        }
+        store16<kStream>(out + i, w[k]);
+    }
+    for (uint32_t i = c.lanes * c.per_lane + threadIdx.x; i < c.count; i += kThreads) {
+        if (t.kind == WC_OUT_F32) {
+            const float v = static_cast<const float*>(t.g)[c.begin + i];
+            static_cast<float*>(t.out)[c.begin + i] = clips ? v * factor : v;
+        } else {
+            const uint16_t v = static_cast<const uint16_t*>(t.g)[c.begin + i];
+            static_cast<uint16_t*>(t.out)[c.begin + i] =
+                clips ? (uint16_t)pack_bf16(__uint_as_float((uint32_t)v << 16) * factor, 0.0f) : v;
+        }
+    }
 }
 
 uint32_t size_of(const wc_grad& g) { return g.kind == WC_OUT_F32 ? 4 : 2; }
@@ -205,15 +209,16 @@ struct ClipShape {
 ClipShape shape_of(const wc_grad* grads, uint32_t n) {
     uint64_t bytes = 0;
     for (uint32_t i = 0; i < n; ++i) bytes += grads[i].numel * size_of(grads[i]);
-    return {bytes < (8u << 20) ? 4096u : 16384u, bytes > kCacheBytes};
+    return {bytes < (8u << 20) ? 4096u : kMostChunk, bytes > kCacheBytes};
 }
 
 // The next batch: as many tensors from `at` on as fit, but those without elements, and no more chunks than a launch's
 // fewer than 2^32 threads allow (one tensor has 2^22 at most).  Returns where the one after it begins.
-uint32_t next_batch(const wc_grad* grads, uint32_t n, uint32_t at, uint32_t bytes, ClipParams& p) {
+template <uint32_t kTensors>
+uint32_t next_batch(const wc_grad* grads, uint32_t n, uint32_t at, uint32_t bytes, ClipParams<kTensors>& p) {
     p.tensors = p.chunks = 0;
     p.chunk_bytes = bytes;
-    for (; at < n && p.tensors < kBatch; ++at) {
+    for (; at < n && p.tensors < kTensors; ++at) {
         const wc_grad& g = grads[at];
         if (g.numel == 0) continue;
         const uint64_t chunks = (g.numel * size_of(g) + bytes - 1) / bytes;
@@ -223,7 +228,7 @@ uint32_t next_batch(const wc_grad* grads, uint32_t n, uint32_t at, uint32_t byte
     }
     return at;
 }
-uint32_t groups_of(const ClipParams& p) { return p.chunks < kGroups ? p.chunks : kGroups; }
+uint32_t groups_of(uint32_t chunks) { return chunks < kGroups ? chunks : kGroups; }
 
 bool list_fits(const wc_grad* grads, uint32_t n) {
     if (n > WC_MAX_GRADS || (n && !grads)) return false;
@@ -236,6 +241,43 @@ bool list_fits(const wc_grad* grads, uint32_t n) {
     return true;
 }
 
+// Partial sums of a list.
+template <uint32_t kTensors>
+uint64_t parts_of(const wc_grad* grads, uint32_t n, uint32_t bytes) {
+    uint64_t parts = 0;
+    ClipParams<kTensors> p{};
+    for (uint32_t at = 0; at < n;) at = next_batch(grads, n, at, bytes, p), parts += groups_of(p.chunks);
+    return parts;
+}
+
+template <uint32_t kTensors, bool kStream>
+void run(const wc_grad* grads, uint32_t n, uint32_t bytes, float max_norm, float* norm, double* work, hipStream_t s) {
+    using Params = ClipParams<kTensors>;
+    Params p{};
+    p.part = work;
+    p.max_norm = max_norm;
+    for (uint32_t at = 0; at < n;) {
+        at = next_batch(grads, n, at, bytes, p);
+        if (p.chunks == 0) continue;
+        hipLaunchKernelGGL((clip_norm_kernel<Params, kStream>), dim3(groups_of(p.chunks)), dim3(kThreads), 0, s, p);
+        p.part_at += groups_of(p.chunks);
+    }
+    p.parts = p.part_at;
+    if (p.parts > kOwnParts) {
+        hipLaunchKernelGGL(clip_join_kernel, dim3(1), dim3(kJoinThreads), 0, s, p.part, p.parts);
+        p.part += p.parts;
+        p.parts = 1;
+    }
+    p.norm = norm;
+    uint32_t at = 0;
+    do {   // a list without elements: its norm alone, 0
+        at = next_batch(grads, n, at, bytes, p);
+        if (p.chunks == 0 && !p.norm) continue;
+        hipLaunchKernelGGL((clip_scale_kernel<Params, kStream>), dim3(p.chunks ? p.chunks : 1), dim3(kThreads), 0, s, p);
+        p.norm = nullptr;
+    } while (at < n);
+}
+
 }  // namespace
 }  // namespace wc
 
@@ -244,9 +286,7 @@ using namespace wc;
 extern "C" int wc_clip_grads_work_bytes(const wc_grad* grads, uint32_t n, uint64_t* work_bytes) {
     if (!work_bytes || !list_fits(grads, n)) return WC_ERR_INVALID_ARG;
     const uint32_t bytes = shape_of(grads, n).chunk_bytes;
-    uint64_t parts = 0;
-    ClipParams p{};
-    for (uint32_t at = 0; at < n;) at = next_batch(grads, n, at, bytes, p), parts += groups_of(p);
+    const uint64_t parts = n <= kSmallBatch ? parts_of<kSmallBatch>(grads, n, bytes) : parts_of<kBatch>(grads, n, bytes);
     *work_bytes = parts ? (parts + 1) * sizeof(double) : 0;
     return WC_OK;
 }
@@ -260,30 +300,13 @@ extern "C" int wc_clip_grads_async(const wc_grad* grads, uint32_t n, float max_n
         return WC_ERR_INVALID_ARG;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     const ClipShape shape = shape_of(grads, n);
-    ClipParams p{};
-    p.part = static_cast<double*>(work_dev);
-    p.max_norm = max_norm;
-    for (uint32_t at = 0; at < n;) {
-        at = next_batch(grads, n, at, shape.chunk_bytes, p);
-        if (p.chunks == 0) continue;
-        const auto kernel = shape.stream ? clip_norm_kernel<true> : clip_norm_kernel<false>;
-        hipLaunchKernelGGL(kernel, dim3(groups_of(p)), dim3(kThreads), 0, s, p);
-        p.part_at += groups_of(p);
+    double* const work = static_cast<double*>(work_dev);
+    if (n <= kSmallBatch) {
+        if (shape.stream) run<kSmallBatch, true>(grads, n, shape.chunk_bytes, max_norm, norm, work, s);
+        else run<kSmallBatch, false>(grads, n, shape.chunk_bytes, max_norm, norm, work, s);
+    } else {
+        if (shape.stream) run<kBatch, true>(grads, n, shape.chunk_bytes, max_norm, norm, work, s);
+        else run<kBatch, false>(grads, n, shape.chunk_bytes, max_norm, norm, work, s);
     }
-    p.parts = p.part_at;
-    if (p.parts > kOwnParts) {
-        hipLaunchKernelGGL(clip_join_kernel, dim3(1), dim3(kJoinThreads), 0, s, p.part, p.parts);
-        p.part += p.parts;
-        p.parts = 1;
-    }
-    p.norm = norm;
-    uint32_t at = 0;
-    do {   // a list without elements: its norm alone, 0
-        at = next_batch(grads, n, at, shape.chunk_bytes, p);
-        if (p.chunks == 0 && !p.norm) continue;
-        const auto kernel = shape.stream ? clip_scale_kernel<true> : clip_scale_kernel<false>;
-        hipLaunchKernelGGL(kernel, dim3(p.chunks ? p.chunks : 1), dim3(kThreads), 0, s, p);
-        p.norm = nullptr;
-    } while (at < n);
     return hipGetLastError() == hipSuccess ? WC_OK : WC_ERR_HIP;
 }
