@@ -19,7 +19,6 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
-#include <type_traits>
 
 #include "../../include/wc.h"
 #include "e4m3.h"
@@ -211,8 +210,8 @@ __device__ __forceinline__ void store_tile(uint8_t* lds, void* y, const GemmPara
         return;
     }
     // as many tokens at a time as LDS holds
-    constexpr uint32_t kFit = T::kScalesAt / kRow, kPass = kFit < T::kBn ? kFit : T::kBn;
-    static_assert(T::kBn % kPass == 0 && kPass % T::kWaveN == 0 && (kChunks & (kChunks - 1)) == 0, "a wave's tokens go together");
+    constexpr uint32_t kPass = T::kBn * kRow <= T::kScalesAt ? T::kBn : T::kBn / 2;
+    static_assert(kPass * kRow <= T::kScalesAt && kPass % T::kWaveN == 0 && (kChunks & (kChunks - 1)) == 0, "a wave's tokens go together");
     for (uint32_t from = 0; from < T::kBn; from += kPass) {
         if (from) __syncthreads();
         if (holds && wn >= from && wn < from + kPass) {
@@ -352,7 +351,6 @@ __global__ __launch_bounds__(T::kThreads, 2) void gemm_fp8_big_kernel(GemmParams
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (uint32_t i = 0; i < kPer; ++i)
 #pragma unroll
@@ -365,7 +363,6 @@ __global__ __launch_bounds__(T::kThreads, 2) void gemm_fp8_big_kernel(GemmParams
                     __builtin_amdgcn_sched_group_barrier(2, 4, 0);   // four VALU instructions, then the product
                     __builtin_amdgcn_sched_group_barrier(8, 1, 0);
                 }
-            __builtin_amdgcn_s_setprio(0);
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
@@ -605,11 +602,11 @@ constexpr uint32_t kCus = 256;
 constexpr uint32_t kFewTokens = 32;
 constexpr uint32_t kFewWideRows = 8192;
 
-// Tiles and splits of more tokens are those that a model of the time likes best.  What the model rests on: a CU takes in
-// about 40 bytes per ns, whatever the tile (measured: 36 to 41 with operands past the L2 cache, tiles of 32 x 32 to 256 x
-// 256; 30 where codes are made bf16), a workgroup's start and end take 3 us, and joining splits a launch of 2.5 us and
-// their sums written and read at 4 TB/s.  Few and small tiles leave CUs idle, large ones re-read the least.  Measured (us,
-// tile:splits; * what the model takes):
+// Tiles and splits of more tokens are those that a model of the time likes best.  It knows what a tile takes per block of
+// columns: a CU takes in about 40 bytes per ns, whatever the tile (measured: 36 to 41 with operands past the L2 cache, from
+// 32 x 32 to 256 x 256), or, where codes are made bf16, up to half of that, as the products then bound it; a workgroup's
+// start and end, 3 us; and for joining splits a launch of 2.5 us and their sums, written and read at 4 TB/s.  Few and small
+// tiles leave CUs idle, large ones re-read the least.  Measured (us, tile:splits; * what the model takes):
 //                                32x32   32x64   64x64     64x64:2  128x64     128x128  128x128:8  256x256
 //    90 tokens x 1304 x 2704       7.3*    9.2    10.0      10.0      10.0:4     -
 //   333 x 1003 x 2096             11.8     8.3*    9.7      11.0      12.9:2     -
@@ -617,12 +614,20 @@ constexpr uint32_t kFewWideRows = 8192;
 //   200 x 5000 x 1008              -      12.3     9.8       -         7.7*      9.7
 //   128 x 4096 x 14336            43.2    37.0    47.5      31.1      27.9:4    -         26.9*
 //  1024 x 4096 x 4096              -       -      45.0       -        33.1      28.8*
-//  4096 x 14336 x 4096             -       -       -         -         -         -          -         239*
+//  4096 x 14336 x 4096             -       -       -         -         -         -          -         224*
+// and of fp32 results (128 x 128 in 4 waves, 256 x 128 in 8):
+//   333 x 1003 x 2096              -      9.3*    11.0
+//  1024 x 4096 x 4096              -       -       -         -         -        48*       62 (256x128)
+//  4096 x 8192 x 8192              -       -       -         -         -       520       484* (256x128)
 struct Kind {
     uint32_t bm, bn, per_cu;   // workgroups per CU (LDS)
+    double us;                 // per block of columns
 };
-constexpr Kind kKinds[] = {{32, 32, 1}, {32, 64, 1}, {64, 64, 1}, {128, 64, 2}, {128, 128, 1}, {256, 256, 1}};
-constexpr uint32_t kBigKind = 5;
+constexpr uint32_t kKinds = 6, kLast = kKinds - 1;
+constexpr Kind kCodeKinds[kKinds] = {{32, 32, 1, 0.2}, {32, 64, 1, 0.3}, {64, 64, 1, 0.4}, {128, 64, 2, 0.6}, {128, 128, 1, 0.8},
+                                     {256, 256, 1, 1.6}};
+constexpr Kind kExactKinds[kKinds] = {{32, 32, 1, 0.26}, {32, 64, 1, 0.4}, {64, 64, 1, 0.42}, {128, 64, 2, 0.65},
+                                      {128, 128, 2, 1.35}, {256, 128, 1, 2.0}};
 
 struct GemmPlan {
     uint32_t kind, splits, split_blocks;
@@ -632,17 +637,16 @@ GemmPlan plan_of(uint32_t rows, uint32_t cols, uint64_t tokens, bool exact) {
     const uint32_t blocks = cdiv(cols, kBlockCols);
     GemmPlan best{0, 1, blocks, 0};
     if (tokens <= kFewTokens) return best;
-    const double rate = exact ? 30e3 : 40e3;   // bytes per us
     double best_us = 1e300;
-    for (uint32_t k = 0; k < (exact ? kBigKind : kBigKind + 1); ++k) {
-        const Kind& kind = kKinds[k];
+    for (uint32_t k = 0; k < kKinds; ++k) {
+        const Kind& kind = exact ? kExactKinds[k] : kCodeKinds[k];
         const uint64_t tiles = (uint64_t)cdiv(rows, kind.bm) * cdiv(tokens, kind.bn);
         for (uint32_t s = 1; s <= 16; s *= 2) {
-            if (s > 1 && (k == kBigKind || blocks < 8 * s || tiles * s > kCus * kind.per_cu)) break;
+            if (s > 1 && (k == kLast || blocks < 8 * s || tiles * s > kCus * kind.per_cu)) break;
             const uint32_t per = cdiv(blocks, s);
             const uint64_t groups = tiles * s;
             const double us = 3.0 * (double)((groups + kCus * kind.per_cu - 1) / (kCus * kind.per_cu)) +
-                              (double)((groups + kCus - 1) / kCus) * per * (kind.bm + kind.bn) * kBlockCols / rate +
+                              (double)((groups + kCus - 1) / kCus) * per * kind.us +
                               (s > 1 ? 2.5 + (double)s * (double)tokens * rows * 8 / 4e6 : 0.0);
             if (us < best_us) best_us = us, best = {k, cdiv(blocks, per), per, 0};
         }
@@ -675,15 +679,19 @@ void launch(const GemmParams& p, hipStream_t s) {
                        dim3(tile_grid(cdiv(p.rows, T::kBm), cdiv(p.tokens, T::kBn)), p.splits), dim3(T::kThreads), 0, s, p);
 }
 
-// Waves, stages and groups of each kind as they measured best; codes made bf16 take 4 larger waves in 128 x 128 (4096
-// tokens x 4096 x 2048 in fp32: 71 us, 85 with 8).
+// Waves, stages and groups of each kind as they measured best.
 template <bool kExact>
 void launch_tiles(uint32_t kind, const GemmParams& p, hipStream_t s) {
     if (kind == 0) launch<Tile<32, 32, 2, 2, 4, 4>, kExact>(p, s);
     else if (kind == 1) launch<Tile<32, 64, 2, 2, 4, 2>, kExact>(p, s);
     else if (kind == 2) launch<Tile<64, 64, 2, 2, 3, 2>, kExact>(p, s);
     else if (kind == 3) launch<Tile<128, 64, 4, 2, 3, 1>, kExact>(p, s);
-    else launch<typename std::conditional<kExact, Tile<128, 128, 2, 2, 2, 1>, Tile<128, 128, 2, 4, 3, 1>>::type, kExact>(p, s);
+    else if constexpr (kExact) kind == 4 ? launch<Tile<128, 128, 2, 2, 2, 1>, true>(p, s)
+                                         : launch<Tile<256, 128, 4, 2, 3, 1>, true>(p, s);
+    else if (kind == 4) launch<Tile<128, 128, 2, 4, 3, 1>, false>(p, s);
+    else
+        hipLaunchKernelGGL(gemm_fp8_big_kernel<Big>, dim3(tile_grid(cdiv(p.rows, Big::kBm), cdiv(p.tokens, Big::kBn))),
+                           dim3(Big::kThreads), 0, s, p);
 }
 
 }  // namespace
@@ -731,9 +739,6 @@ extern "C" int wc_gemm_fp8_async(const wc_fp8_matrix* W, const uint8_t* x_codes,
     p.split_blocks = g.split_blocks, p.splits = g.splits, p.out_kind = out_kind;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (tokens <= kFewTokens) launch_few_tokens(p, s);
-    else if (g.kind == kBigKind)
-        hipLaunchKernelGGL(gemm_fp8_big_kernel<Big>, dim3(tile_grid(cdiv(p.rows, Big::kBm), cdiv(p.tokens, Big::kBn))),
-                           dim3(Big::kThreads), 0, s, p);
     else if (exact) launch_tiles<true>(g.kind, p, s);
     else launch_tiles<false>(g.kind, p, s);
     if (g.splits > 1) {
