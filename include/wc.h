@@ -517,7 +517,10 @@ int wc_fp8_check(const wc_fp8_matrix* W);
  *   y[t][r] = sum_b (x_scales[t][b] scales[r / 128][b]) sum_{c in block b} x_codes[t][c] codes[r][c].
  * The product of the scales is taken first, in fp32 (it must be in its range);
  * sums are fp32 in a fixed order that depends on the sizes alone, so y is the
- * same bits on every run.  At most two launches.
+ * same bits on every run.  bf16 results of more than 32 tokens come of the 8-bit
+ * matrix instructions, which sum eight neighbouring products at a time and drop
+ * what lies below 2^-14 of the largest of them; fp32 results, and those of up to
+ * 32 tokens, keep every product.  At most two launches.
  *   x_codes   device, tokens x cols e4m3, 16-byte aligned;
  *   x_scales  device, tokens x ceil(cols / 128) float32 (both as
  *             wc_quant_fp8_async or wc_rms_norm_async writes them);
@@ -553,7 +556,7 @@ int wc_gemm_fp8_async(const wc_fp8_matrix* W, const uint8_t* x_codes, const floa
 #define WC_MAX_GRAD_NUMEL (1ull << 34)
 typedef struct {
     const void* g;    /* device, numel elements, aligned to them (faster: to 16 bytes) */
-    void* out;        /* the same, written: g itself, or no part of any tensor read    */
+    void* out;        /* the same, written: g itself, or no part of any other g or out */
     uint64_t numel;   /* at most WC_MAX_GRAD_NUMEL; 0: nothing                         */
     uint32_t kind;    /* of both: WC_OUT_F32 or WC_OUT_BF16                            */
 } wc_grad;

@@ -866,7 +866,8 @@ def gemm_fp8_async(W: Fp8Matrix, x_codes_dev, x_scales_dev, tokens: int, y_dev, 
 
 class GradList:
     """A list of gradients for clip_grads_async (kept alive by this handle): float32 or bf16 device tensors, and where the
-    clipped ones go (outs: tensors of the same sizes and types; None: in place)."""
+    clipped ones go (outs: tensors of the same sizes and types, any of them the gradient itself; None: all in place).
+    No output may overlap another tensor of the list."""
 
     def __init__(self, grads, outs=None):
         call = "wc_clip_grads_async"
@@ -878,6 +879,7 @@ class GradList:
         self._tensors = (grads, outs)
         self._array = (_Grad * max(len(grads), 1))()
         self._n = len(grads)
+        spans = []   # what is read and written: (begin, end, writes, index)
         for i, (g, out) in enumerate(zip(grads, outs)):
             kind = _kind_of(g.dtype)
             if kind not in OUT_KINDS or _kind_of(out.dtype) != kind:
@@ -888,6 +890,18 @@ class GradList:
             size = (4 if kind == "f32" else 2) * n
             self._array[i] = _Grad(_bytes_ok(g, size, self.device, f"gradient {i}", call),
                                    _bytes_ok(out, size, self.device, f"output {i}", call), n, OUT_KINDS[kind])
+            if n:
+                read, write = self._array[i].g, self._array[i].out
+                spans.append((write, write + size, True, i))
+                if read != write:
+                    spans.append((read, read + size, False, i))
+        # an element that is written must be no other's: workgroups read and write in no order
+        written = seen = 0
+        for begin, end, writes, i in sorted(spans):
+            if begin < (seen if writes else written):
+                raise WCError(WC_ERR_INVALID_ARG, call, f"gradient {i} overlaps another one's output")
+            seen = max(seen, end)
+            written = max(written, end) if writes else written
 
 
 def clip_grads_work_bytes(grads: GradList) -> int:

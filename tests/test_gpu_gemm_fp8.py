@@ -93,9 +93,10 @@ def test_few_tokens(wc, tokens):
     assert within(y, want, gemm_tolerance(x, w, False, want))
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("tokens", [1, 24, 200])
-def test_every_code(wc, tokens):
-    """Each of the 254 finite codes times each other: single products are exact in fp32."""
+def test_every_code(wc, tokens, out):
+    """Each of the 254 finite codes times each other: single products, of 8 bits, are exact in fp32 and in bf16."""
     cols, rows = 128, 254
     finite = torch.tensor([c for c in range(256) if c & 127 != 127], dtype=torch.uint8)
     codes = torch.zeros(rows, cols, dtype=torch.uint8)
@@ -106,12 +107,13 @@ def test_every_code(wc, tokens):
         mine = finite[start:start + tokens]
         xc = torch.zeros(len(mine), cols, dtype=torch.uint8)
         xc[:, 77] = mine
-        y = _run(wc, W, xc.cuda(), torch.ones(len(mine), 1, device="cuda"), len(mine), "f32")
+        y = _run(wc, W, xc.cuda(), torch.ones(len(mine), 1, device="cuda"), len(mine), out)
         assert torch.equal(y.cpu().double(), values_of(mine)[:, None] * values_of(finite)[None, :])
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("tokens", [1, 20, 150])
-def test_columns_of_blocks(wc, tokens):
+def test_columns_of_blocks(wc, tokens, out):
     """Every column reaches the right block's scales: one nonzero column at a time, scales all different."""
     rows, cols = 300, 400
     g = torch.Generator().manual_seed(1)
@@ -123,7 +125,7 @@ def test_columns_of_blocks(wc, tokens):
         codes[:, c] = torch.randint(1, 127, (rows,), generator=g).to(torch.uint8)
         xc[:, c] = torch.randint(1, 127, (tokens,), generator=g).to(torch.uint8)
         W = wc.Fp8Matrix(codes.cuda(), scales.cuda(), rows, cols)
-        y = _run(wc, W, xc.cuda(), xs.cuda(), tokens, "f32")
+        y = _run(wc, W, xc.cuda(), xs.cuda(), tokens, out)
         want = (values_of(xc[:, c]) * xs.double()[:, c // BLOCK])[:, None] * \
             (values_of(codes[:, c]) * scales.double()[torch.arange(rows) // BLOCK, c // BLOCK])[None]
         assert torch.equal(y.cpu().double(), want), c
@@ -208,3 +210,22 @@ def test_large_scales(wc, tokens):
     y = _run(wc, W, xc.cuda(), (xs * 2.0 ** -90).cuda(), tokens, "f32")
     want = x @ w.t()
     assert within(y, want, gemm_tolerance(x, w, False, want))
+
+
+@pytest.mark.parametrize("tokens", [1, 20, 60, 300])
+def test_sums_that_cancel(wc, tokens):
+    """Large products that cancel beside small ones: fp32 results, and those of few tokens, keep the small ones whole."""
+    rows, cols = 200, 256
+    codes, xc = torch.zeros(rows, cols), torch.zeros(tokens, cols)
+    codes[:, 0], codes[:, 1], xc[:, 0], xc[:, 1] = 448.0, -448.0, 448.0, 448.0
+    codes[:, 2:], xc[:, 2:] = 0.125, 0.0625                   # 254 products of 2^-7, beside 448 * 448
+    xc[:, 128:130] = 0.0625
+    log(f"case: gemm_fp8 cancelling sums, {tokens} tokens")
+    W = wc.Fp8Matrix(codes.to(F8).cuda(), torch.ones(2, 2, device="cuda"), rows, cols)
+    y = _run(wc, W, xc.to(F8).cuda(), torch.ones(tokens, 2, device="cuda"), tokens, "f32")
+    # in any order each partial sum is a multiple of 2^-7 below 2^18: up to one bit more than fp32 holds is lost per sum
+    assert bool(((y.cpu().double() - 254 / 128).abs() <= 128 * 2.0 ** -7).all())
+    alone = torch.zeros(tokens, cols)
+    alone[:, 2:] = xc[:, 2:]
+    y = _run(wc, W, alone.to(F8).cuda(), torch.ones(tokens, 2, device="cuda"), tokens, "f32")
+    assert torch.equal(y.cpu().double(), torch.full((tokens, rows), 254 / 128, dtype=torch.float64))

@@ -205,9 +205,15 @@ def test_binding_clip(device0):
     wc = device0
 
     class Grad(DevTensor):
-        def __init__(self, n, dtype="torch.float32", **kw):
+        next_at = 1 << 24
+
+        def __init__(self, n, dtype="torch.float32", at=None, **kw):
             super().__init__(n * (4 if dtype == "torch.float32" else 2), dtype=dtype, **kw)
-            self._n = n
+            self._n, self._at = n, at or Grad.next_at
+            Grad.next_at += 1 << 12
+
+        def data_ptr(self):
+            return self._at
 
         def numel(self):
             return self._n
@@ -229,6 +235,20 @@ def test_binding_clip(device0):
         assert _status(lambda: wc.GradList(grads, outs)) == INV
     handle.device = 1
     assert _status(lambda: wc.clip_grads_async(handle, 1.0, t, t, 4096, stream=0)) == INV
+
+    def g(at, n=10):
+        return Grad(n, at=at)
+
+    a = 1 << 20
+    for grads, outs in (([g(a), g(a)], None),                            # the same tensor twice, in place
+                        ([g(a), g(a + 36)], None),                       # the last element of one is the other's first
+                        ([g(a), g(a + 400)], [g(a + 800), g(a + 836)]),  # outputs that overlap
+                        ([g(a), g(a + 400)], [g(a + 400), g(a + 800)]),  # an output that is another's gradient
+                        ([g(a), g(a + 40)], [g(a + 4), g(a + 400)])):    # an output that is part of its own gradient
+        assert _status(lambda: wc.GradList(grads, outs)) == INV
+    for grads, outs in (([g(a), g(a + 40)], None), ([g(a), g(a)], [g(a + 400), g(a + 440)]),
+                        ([g(a), g(a + 400)], [g(a), g(a + 800)]), ([g(a, 0), g(a), g(a, 0)], None)):
+        assert len(wc.GradList(grads, outs)._tensors[0]) == len(grads)
 
 
 def test_operators_fail_without_a_device(wc):
