@@ -184,9 +184,9 @@ __device__ __forceinline__ void store4(void* y, uint32_t kind, uint64_t at, uint
 }
 
 // A tile's results: put together in LDS, which is free (4 neighbours of a token per lane, 16-byte chunks at chunk ^
-// token, so that the 16 tokens that a wave writes at a time lie in different banks), then written as whole rows.  From
-// the registers, 32 bytes of a token at a time, that took 10 % of the time at 8192 tokens x 28672 x 8192.  Rows that do
-// not begin on 16 bytes are written from the registers.
+// token, so that the 16 tokens that a wave writes at a time lie in different banks), then written as whole rows, 16 bytes
+// per lane, or where rows do not begin on 16 bytes, 4.  From the registers, 32 bytes of a token at a time, that took 10 %
+// of the time at 8192 tokens x 28672 x 8192, and a quarter at 8193 rows.
 template <class T, uint32_t kKind>
 __device__ __forceinline__ void store_tile(uint8_t* lds, void* y, const GemmParams& p, uint32_t m0, uint32_t n0,
                                            const f32x4 (&acc)[T::kMi][T::kNi]) {
@@ -195,23 +195,10 @@ __device__ __forceinline__ void store_tile(uint8_t* lds, void* y, const GemmPara
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63u;
     const uint32_t wm = wave % T::kWavesM * T::kWaveM, wn = wave / T::kWavesM * T::kWaveN;
     const bool holds = wave < T::kWaves;   // the first group
-    if (p.rows % (16 / kSize) != 0) {
-        if (!holds) return;
-#pragma unroll
-        for (uint32_t j = 0; j < T::kNi; ++j) {
-            const uint32_t t = n0 + wn + j * 16 + (lane & 15u);
-            if (t >= p.tokens) continue;
-#pragma unroll
-            for (uint32_t i = 0; i < T::kMi; ++i) {
-                const uint32_t r = m0 + wm + i * 16 + (lane >> 4) * 4;
-                if (r < p.rows) store4(y, kKind, (uint64_t)t * p.rows + r, p.rows - r, acc[i][j]);
-            }
-        }
-        return;
-    }
     // as many tokens at a time as LDS holds
     constexpr uint32_t kPass = T::kBn * kRow <= T::kScalesAt ? T::kBn : T::kBn / 2;
-    static_assert(kPass * kRow <= T::kScalesAt && kPass % T::kWaveN == 0 && (kChunks & (kChunks - 1)) == 0, "a wave's tokens go together");
+    static_assert(kPass * kRow <= T::kScalesAt && kPass % T::kWaveN == 0 && kPass <= T::kThreads, "a wave's tokens go together");
+    static_assert((kChunks & (kChunks - 1)) == 0, "chunks are permuted");
     for (uint32_t from = 0; from < T::kBn; from += kPass) {
         if (from) __syncthreads();
         if (holds && wn >= from && wn < from + kPass) {
@@ -228,13 +215,39 @@ __device__ __forceinline__ void store_tile(uint8_t* lds, void* y, const GemmPara
                 }
         }
         __syncthreads();
-        const uint32_t tokens = p.tokens - n0, rows = p.rows - m0;
-        uint8_t* const out = static_cast<uint8_t*>(y) + ((uint64_t)n0 * p.rows + m0) * kSize;
-        for (uint32_t k = threadIdx.x; k < kChunks * kPass; k += T::kThreads) {
-            const uint32_t n = k / kChunks, c = k % kChunks;
-            if (from + n < tokens && c * (16 / kSize) < rows)
-                *reinterpret_cast<u32x4*>(out + (uint64_t)(from + n) * p.rows * kSize + c * 16) =
-                    *reinterpret_cast<const u32x4*>(lds + n * kRow + ((c ^ (n & kTurn)) * 16));
+        const uint32_t tokens = p.tokens - n0 - min(p.tokens - n0, from), rows = p.rows - m0;
+        if (p.rows % (16 / kSize) == 0) {
+            uint8_t* const out = static_cast<uint8_t*>(y) + ((uint64_t)(n0 + from) * p.rows + m0) * kSize;
+            for (uint32_t k = threadIdx.x; k < kChunks * kPass; k += T::kThreads) {
+                const uint32_t n = k / kChunks, c = k % kChunks;
+                if (n < tokens && c * (16 / kSize) < rows)
+                    *reinterpret_cast<u32x4*>(out + (uint64_t)n * p.rows * kSize + c * 16) =
+                        *reinterpret_cast<const u32x4*>(lds + n * kRow + ((c ^ (n & kTurn)) * 16));
+            }
+            continue;
+        }
+        const uint32_t count = min(rows, T::kBm);
+        const auto at = [&](uint32_t n, uint32_t e) {
+            return lds + n * kRow + (((e * kSize / 16) ^ (n & kTurn)) * 16) + e * kSize % 16;
+        };
+        const auto half = [&](uint32_t n, uint32_t e) { return (uint32_t) * reinterpret_cast<const uint16_t*>(at(n, e)); };
+        constexpr uint32_t kWords = kRow / 4;   // of a token
+#pragma unroll 8
+        for (uint32_t k = threadIdx.x; k < kWords * kPass; k += T::kThreads) {
+            const uint32_t n = k / kWords, i = k % kWords;
+            const uint64_t first = (uint64_t)(n0 + from + n) * p.rows + m0;
+            const uint32_t odd = kSize == 2 ? (uint32_t)first & 1u : 0, e = kSize == 2 ? 2 * i + odd : i;
+            if (n < tokens && e + 4 / kSize <= count)
+                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(y) + (first + e) * kSize) =
+                    kSize == 4 ? *reinterpret_cast<const uint32_t*>(at(n, e)) : half(n, e) | half(n, e + 1) << 16;
+        }
+        if (kSize == 2 && threadIdx.x < kPass && threadIdx.x < tokens) {   // what no pair has: left of the first, the last
+            const uint32_t n = threadIdx.x;
+            const uint64_t first = (uint64_t)(n0 + from + n) * p.rows + m0;
+            const uint32_t odd = (uint32_t)first & 1u;
+            uint16_t* const out = static_cast<uint16_t*>(y) + first;
+            if (odd) out[0] = (uint16_t)half(n, 0);
+            if ((count - odd) & 1u) out[count - 1] = (uint16_t)half(n, count - 1);
         }
     }
 }
