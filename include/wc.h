@@ -441,7 +441,8 @@ int wc_ce_grad_async(const uint16_t* h, const uint16_t* W, const void* targets, 
  * a block that holds an infinity or a NaN gets the scale NaN.  One launch.
  *   x       device, 16-byte aligned bf16, dim a multiple of 8; gated 0: n x dim,
  *           y = x; else n x 2 dim, each row gate and then up:
- *           y = silu(gate) up = gate / (1 + exp(-gate)) up, in fp32;
+ *           y = silu(gate) up = gate / (1 + exp(-gate)) up, in fp32 (0 where
+ *           1 + exp(-gate) is past 2^126: gates below -87);
  *   codes   device, n x dim bytes (written), 16-byte aligned;
  *   scales  device, n x ceil(dim / WC_FP8_BLOCK) float32 (written).
  * n == 0 is a no-op; n is at most WC_MAX_TOKENS.
@@ -464,7 +465,7 @@ int wc_quant_fp8_async(const uint16_t* x, uint64_t n, uint32_t dim, int gated, u
  *             (y or codes must be given);
  *   rstd      device, n float32 (written): r, for the gradient; or NULL.
  * bf16 tensors and codes are 16-byte aligned.  sum may be x or residual itself,
- * y may be x or (without a residual) x; no other outputs may overlap inputs.
+ * y may be x itself; no other output may overlap an input or another output.
  * eps is at least 0.  n == 0 is a no-op.  Squares are summed in fp32: a row whose
  * sum of squares leaves its range has r = 0.
  */
