@@ -62,14 +62,16 @@ struct Loader {
     // Start copying the stage of columns c0 .. c0 + 127 (zeros past the last): every kEvery-th round from kFirst on.  The
     // uniform part of an offset stays within the buffer: past its end the range check of a lane's part, which subtracts
     // it, would wrap.
-    template <uint32_t kFirst = 0, uint32_t kEvery = 1>
+    template <uint32_t kFirst = 0, uint32_t kEvery = 1, bool kOnce = false>
     __device__ __forceinline__ void start(uint8_t* lds, uint32_t c0) const {
         const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % (kThreads / 64);
         const uint32_t from = c0 + column < cols ? at : kNoChunk;
 #pragma unroll
-        for (uint32_t i = kFirst; i < kLoads; i += kEvery)
-            copy_to_lds(lds_address(lds) + (i * kThreads + wave * 64u) * 16u, rsrc, from,
-                        min(i * kRows * cols + c0, rsrc[2]));
+        for (uint32_t i = kFirst; i < kLoads; i += kEvery) {
+            const uint32_t to = lds_address(lds) + (i * kThreads + wave * 64u) * 16u;
+            const uint32_t uniform = min(i * kRows * cols + c0, rsrc[2]);
+            kOnce ? copy_once_to_lds(to, rsrc, from, uniform) : copy_to_lds(to, rsrc, from, uniform);
+        }
     }
 };
 
@@ -392,7 +394,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void gemm_fp8_big_kernel(GemmParams
 
 // A tile whose group of waves takes every kGroups-th block of columns: a step is kGroups blocks, one barrier, and the
 // groups' chains of waiting, reading and multiplying run beside each other; their sums are added in order at the end.
-template <class T, bool kExact>
+template <class T, bool kExact, bool kOnce>
 __global__ __launch_bounds__(T::kThreads) void gemm_fp8_tile_kernel(GemmParams p) {
     __shared__ __align__(16) uint8_t lds[T::kLdsBytes];
     uint32_t mt, nt;
@@ -410,13 +412,17 @@ __global__ __launch_bounds__(T::kThreads) void gemm_fp8_tile_kernel(GemmParams p
     constant_float* const ws = (constant_float*)(p.ws + (uint64_t)(min(m0 + wm, p.rows - 1) / kBlockCols) * p.blocks);
     uint8_t* const codes = lds + group * T::kCodeBytes;
     uint8_t* const scales = lds + T::kScalesAt + group * T::kScaleBytes + wave * 256;
+    // where the matrix is read once, in one split, tiles begin at different blocks, as few tokens' groups do (64 tokens x
+    // 28672 x 8192: 48.7 us, from the first one on 54.2)
+    const uint32_t turn = kOnce && p.splits == 1 ? blockIdx.x / kDies * T::kGroups % (end - begin) : 0;
+    const auto turned = [&](uint32_t b) { return !kOnce || b >= end ? b : b + turn < end ? b + turn : b + turn - (end - begin); };
     const auto start = [&](uint32_t stage, uint32_t b) {   // zeros from the split's end on
-        const uint32_t c0 = b < end ? b * kBlockCols : p.cols;
+        const uint32_t c0 = b < end ? turned(b) * kBlockCols : p.cols;
         uint8_t* const to = codes + stage * (T::kGroups * T::kCodeBytes);
-        lw.start(to, c0);
+        lw.template start<0, 1, kOnce>(to, c0);
         lx.start(to + T::kBm * 128, c0);
         copy_words_to_lds(lds_address(scales) + stage * (T::kGroups * T::kScaleBytes), xs_buf,
-                          b < end && lane < T::kWaveN ? xs_at + b * 4 : kNoChunk);
+                          b < end && lane < T::kWaveN ? xs_at + turned(b) * 4 : kNoChunk);
     };
     f32x4 acc[T::kMi][T::kNi];
 #pragma unroll
@@ -426,7 +432,7 @@ __global__ __launch_bounds__(T::kThreads) void gemm_fp8_tile_kernel(GemmParams p
 #pragma unroll
     for (uint32_t s = 0; s + 1 < T::kStages; ++s) start(s, begin + s * T::kGroups + group);
     uint32_t at = 0, to = T::kStages - 1;
-    float scale = begin + group < end ? ws[begin + group] : 0.0f;
+    float scale = begin + group < end ? ws[turned(begin + group)] : 0.0f;
     for (uint32_t b = begin + group; b < end + group; b += T::kGroups) {   // as often for every group
         // this stage has landed once only the later ones' copies are outstanding (each wave waits for its own, the
         // barrier joins them); past the barrier every wave is done with the stage before, which is refilled
@@ -459,7 +465,7 @@ __global__ __launch_bounds__(T::kThreads) void gemm_fp8_tile_kernel(GemmParams p
                 for (uint32_t e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(d[e], s[j], acc[i][j][e]);
             }
         }
-        scale = b + T::kGroups < end ? ws[b + T::kGroups] : 0.0f;
+        scale = b + T::kGroups < end ? ws[turned(b + T::kGroups)] : 0.0f;
         to = at;
         at = at + 1 == T::kStages ? 0 : at + 1;
     }
@@ -494,7 +500,8 @@ __global__ __launch_bounds__(T::kThreads) void gemm_fp8_tile_kernel(GemmParams p
 
 // Few tokens: up to 16 kNi, bound by reading the matrix.  A workgroup takes 16 kMi rows; its waves take blocks of columns
 // in turn, each with kDepth stages of LDS of its own, so that none waits for another until the end, when their sums are
-// added in order: one launch, and everything in a fixed order.
+// added in order: one launch, and everything in a fixed order.  The matrix is read past the caches (1 token x 131072 x 8192:
+// 170 us, through them 193, floor 167; 16 x 28672 x 8192: 48.0 and 54.4).
 template <uint32_t kMi_, uint32_t kNi_, uint32_t kDepth_>
 struct Few {
     static constexpr uint32_t kMi = kMi_, kNi = kNi_, kDepth = kDepth_;
@@ -527,8 +534,8 @@ __global__ __launch_bounds__(1024) void gemm_fp8_few_kernel(GemmParams p) {
             const bool inside = c0 + column < p.cols;
 #pragma unroll
             for (uint32_t i = 0; i < F::kMi; ++i)
-                copy_to_lds(lds_address(to) + i * 2048 + half * 1024, w_buf,
-                            inside ? (r + i * 16) * p.cols + column : kNoChunk, min(c0, w_buf[2]));
+                copy_once_to_lds(lds_address(to) + i * 2048 + half * 1024, w_buf,
+                                 inside ? (r + i * 16) * p.cols + column : kNoChunk, min(c0, w_buf[2]));
 #pragma unroll
             for (uint32_t j = 0; j < F::kNi; ++j)
                 copy_to_lds(lds_address(to) + (F::kMi + j) * 2048 + half * 1024, x_buf,
@@ -542,8 +549,9 @@ __global__ __launch_bounds__(1024) void gemm_fp8_few_kernel(GemmParams p) {
     for (uint32_t i = 0; i < F::kMi; ++i)
 #pragma unroll
         for (uint32_t j = 0; j < F::kNi; ++j) acc[i][j] = (f32x4)(0.0f);
-    // workgroups begin at different blocks, so that not all of them read the same columns of rows a power of two apart
-    const uint32_t turn = blockIdx.x % p.blocks;
+    // workgroups begin at different blocks, those of one die one behind the other, so that they do not all read the same
+    // columns of rows a power of two apart
+    const uint32_t turn = blockIdx.x / kDies * waves % p.blocks;
     const auto turned = [&](uint32_t b) {
         return b >= p.blocks ? b : b + turn < p.blocks ? b + turn : b + turn - p.blocks;
     };
@@ -614,34 +622,36 @@ uint32_t cdiv(uint64_t a, uint32_t b) { return (uint32_t)((a + b - 1) / b); }
 using Big = Tile<256, 256, 2, 4, 2, 1>;
 constexpr uint32_t kCus = 256;
 constexpr uint32_t kFewTokens = 32;
-constexpr uint32_t kFewWideRows = 8192;
 
 // Tiles and splits of more tokens are those that a model of the time likes best.  It knows what a tile takes per block of
 // columns: a CU takes in about 40 bytes per ns, whatever the tile (measured: 36 to 41 with operands past the L2 cache, from
 // 32 x 32 to 256 x 256), or, where codes are made bf16, up to half of that, as the products then bound it; a workgroup's
 // start and end, 3 us; and for joining splits a launch of 2.5 us and their sums, written and read at 4 TB/s.  Few and small
 // tiles leave CUs idle, large ones re-read the least.  Measured (us, tile:splits; * what the model takes):
-//                                32x32   32x64   64x64     64x64:2  128x64     128x128  128x128:8  256x256
-//    90 tokens x 1304 x 2704       7.3*    9.2    10.0      10.0      10.0:4     -
-//   333 x 1003 x 2096             11.8     8.3*    9.7      11.0      12.9:2     -
-//   256 x 4096 x 4096              -      17.1    11.6*      -        15.9      28.8
-//   200 x 5000 x 1008              -      12.3     9.8       -         7.7*      9.7
-//   128 x 4096 x 14336            43.2    37.0    47.5      31.1      27.9:4    -         26.9*
-//  1024 x 4096 x 4096              -       -      45.0       -        33.1      28.8*
-//  4096 x 14336 x 4096             -       -       -         -         -         -          -         224*
-// and of fp32 results (128 x 128 in 4 waves, 256 x 128 in 8):
-//   333 x 1003 x 2096              -      9.3*    11.0
-//  1024 x 4096 x 4096              -       -       -         -         -        48*       62 (256x128)
-//  4096 x 8192 x 8192              -       -       -         -         -       520       484* (256x128)
+//                                32x32   32x64   64x64     128x64    128x128   256x128   256x256
+//    64 tokens x 4096 x 4096       7.6*   12.7    12.8       -         -         -         -
+//   128 x 4096 x 4096             13.1     9.3*   10.8      14.2:2     -         -         -
+//   256 x 4096 x 4096              -      16.4    11.3*     15.2      17.7:4     -         -
+//    64 x 28672 x 8192             -       -      61.2      49.1*     49.7      63.5:2     -
+//   128 x 4096 x 14336             -       -       -        28.3:4    28.7:8*   29.0:16    -
+//   128 x 8192 x 28672             -       -       -        86.3:2    69.4:4*   61.9:8     -
+//   128 x 28672 x 8192             -       -       -        82.2      62.3*     69.1:2     -
+//   512 x 4096 x 4096              -       -      20.0      16.4*     22.0       -         -
+//   512 x 14336 x 4096             -       -      94.2      62.6      57.5      45.9*     58.9
+//  1000 x 8192 x 8192              -       -       -         122       101      82.6*      105
+//  1024 x 14336 x 4096             -       -       -         110       103      78.9      63.8*
+//  5000 x 300 x 9008 fp32          -       -       -        52.0*     52.8:4    72.5:2
+//   512 x 14336 x 4096 fp32        -       161     104      82.1      70.9      65.2*
+//  1024 x 4096 x 4096 fp32         -       -      56.9      45.0*     54.9      48.3:2
 struct Kind {
     uint32_t bm, bn, per_cu;   // workgroups per CU (LDS)
     double us;                 // per block of columns
 };
-constexpr uint32_t kKinds = 6, kLast = kKinds - 1;
-constexpr Kind kCodeKinds[kKinds] = {{32, 32, 1, 0.2}, {32, 64, 1, 0.3}, {64, 64, 1, 0.4}, {128, 64, 2, 0.6}, {128, 128, 1, 0.8},
-                                     {256, 256, 1, 1.6}};
-constexpr Kind kExactKinds[kKinds] = {{32, 32, 1, 0.26}, {32, 64, 1, 0.4}, {64, 64, 1, 0.42}, {128, 64, 2, 0.65},
-                                      {128, 128, 2, 1.35}, {256, 128, 1, 2.0}};
+constexpr uint32_t kKinds = 7, kBig = kKinds - 1;   // the last of codes alone, and without splits
+constexpr Kind kCodeKinds[kKinds] = {{32, 32, 1, 0.2}, {32, 64, 1, 0.3}, {64, 64, 1, 0.4}, {128, 64, 2, 0.6},
+                                     {128, 128, 1, 0.8}, {256, 128, 1, 1.4}, {256, 256, 1, 1.6}};
+constexpr Kind kExactKinds[kBig] = {{32, 32, 1, 0.26}, {32, 64, 1, 0.4}, {64, 64, 1, 0.42}, {128, 64, 2, 0.65},
+                                    {128, 128, 2, 1.35}, {256, 128, 1, 2.0}};
 
 struct GemmPlan {
     uint32_t kind, splits, split_blocks;
@@ -652,11 +662,11 @@ GemmPlan plan_of(uint32_t rows, uint32_t cols, uint64_t tokens, bool exact) {
     GemmPlan best{0, 1, blocks, 0};
     if (tokens <= kFewTokens) return best;
     double best_us = 1e300;
-    for (uint32_t k = 0; k < kKinds; ++k) {
+    for (uint32_t k = 0; k < (exact ? kBig : kKinds); ++k) {
         const Kind& kind = exact ? kExactKinds[k] : kCodeKinds[k];
         const uint64_t tiles = (uint64_t)cdiv(rows, kind.bm) * cdiv(tokens, kind.bn);
         for (uint32_t s = 1; s <= 16; s *= 2) {
-            if (s > 1 && (k == kLast || blocks < 8 * s || tiles * s > kCus * kind.per_cu)) break;
+            if (s > 1 && (k == kBig || blocks < 8 * s || tiles * s > kCus * kind.per_cu)) break;
             const uint32_t per = cdiv(blocks, s);
             const uint64_t groups = tiles * s;
             const double us = 3.0 * (double)((groups + kCus * kind.per_cu - 1) / (kCus * kind.per_cu)) +
@@ -675,35 +685,54 @@ void launch_few(const GemmParams& p, uint32_t waves, hipStream_t s) {
                        p);
 }
 
-// Rows and waves of few tokens (us, groups of 16 rows in 8 waves, and of 32 in 4; 17 to 32 tokens: 4 and 4): from 8192 rows
-// on there are groups enough of 32 rows, which share the work on the tokens.
-//   16 tokens x 14336 x 4096     18.2  16.6     32 tokens x 14336 x 4096     21.3  18.3
-//   16 x 8192 x 28672            60.3  51.2     32 x 8192 x 28672            74.5  53.8
-//    8 x 4096 x 14336            16.0  20.3     32 x 4096 x 14336            20.2  25.3
-//    1 x 1024 x 4096              5.1   6.7     24 x 1024 x 4096              6.5   7.9
+// Rows of a group of few tokens, and its waves and stages (us): past 4096 rows there are groups enough of 32 rows, which
+// share the work on the tokens; from 10240 to 16384 rows groups of 64, one per CU, are all in work at once.
+//                          16 rows, 8 waves   32 rows, 4 waves   64 rows, 4 waves
+//    1 token  x 1024 x 4096        4.8               5.9                8.4
+//    8 tokens x 4096 x 14336      12.3              16.0               24.8
+//    1 x 4608 x 8192              12.1               9.4               14.3
+//   16 x 10240 x 8192             20.4              21.0               17.9
+//   16 x 14336 x 4096             15.9              13.2               12.3
+//   16 x 16384 x 8192             29.7              24.4               23.6
+//   16 x 24576 x 8192             44.9              36.3               42.4
+//   16 x 57344 x 8192             98.3              80.8               85.4
+// 17 to 32 tokens: 16 and 32 rows, 4 waves of 2 stages: 24 x 1024 x 4096 6.6 and 8.0, 32 x 4096 x 14336 19.2 and 24.5, 32 x
+// 5120 x 8192 19.6 and 14.7, 32 x 28672 x 8192 69 and 52.
+constexpr uint32_t kNarrowRows = 4096, kTallFrom = 10240, kTallRows = 16384;
 void launch_few_tokens(const GemmParams& p, hipStream_t s) {
-    const bool wide = p.rows >= kFewWideRows;
-    if (p.tokens <= 16) wide ? launch_few<Few<2, 1, 3>>(p, 4, s) : launch_few<Few<1, 1, 2>>(p, 8, s);
-    else wide ? launch_few<Few<2, 2, 2>>(p, 4, s) : launch_few<Few<1, 2, 2>>(p, 4, s);
+    const bool narrow = p.rows <= kNarrowRows, tall = p.rows >= kTallFrom && p.rows <= kTallRows;
+    if (p.tokens > 16) narrow ? launch_few<Few<1, 2, 2>>(p, 4, s) : launch_few<Few<2, 2, 2>>(p, 4, s);
+    else if (narrow) launch_few<Few<1, 1, 2>>(p, 8, s);
+    else if (tall) launch_few<Few<4, 1, 2>>(p, 4, s);
+    else launch_few<Few<2, 1, 3>>(p, 4, s);
 }
 
+// A matrix that one tile of tokens takes whole is read once, and past the caches (us, and through them): 64 tokens x 28672 x
+// 8192 52.7 and 59.2, 128 tokens 62.9 and 68.7, 64 tokens x 14336 x 4096 17.9 and 19.6; not if two do: 128 tokens x 4096 x
+// 14336 in tiles of 64, 28.3 and 26.3.
 template <class T, bool kExact>
 void launch(const GemmParams& p, hipStream_t s) {
-    hipLaunchKernelGGL((gemm_fp8_tile_kernel<T, kExact>),
-                       dim3(tile_grid(cdiv(p.rows, T::kBm), cdiv(p.tokens, T::kBn)), p.splits), dim3(T::kThreads), 0, s, p);
+    const dim3 grid(tile_grid(cdiv(p.rows, T::kBm), cdiv(p.tokens, T::kBn)), p.splits);
+    if constexpr (T::kBn > kFewTokens)
+        if (p.tokens <= T::kBn) {
+            hipLaunchKernelGGL((gemm_fp8_tile_kernel<T, kExact, true>), grid, dim3(T::kThreads), 0, s, p);
+            return;
+        }
+    hipLaunchKernelGGL((gemm_fp8_tile_kernel<T, kExact, false>), grid, dim3(T::kThreads), 0, s, p);
 }
 
-// Waves, stages and groups of each kind as they measured best.
+// Waves, stages and groups of each kind as they measured best.  128 x 64 where no CU has two workgroups: two groups of
+// waves, so that as much is on its way (64 tokens x 28672 x 8192, us: 48.7, and 56.3 with one).
 template <bool kExact>
 void launch_tiles(uint32_t kind, const GemmParams& p, hipStream_t s) {
+    const bool alone = kind == 3 && cdiv(p.rows, 128) * (uint64_t)cdiv(p.tokens, 64) * p.splits <= kCus;
     if (kind == 0) launch<Tile<32, 32, 2, 2, 4, 4>, kExact>(p, s);
     else if (kind == 1) launch<Tile<32, 64, 2, 2, 4, 2>, kExact>(p, s);
     else if (kind == 2) launch<Tile<64, 64, 2, 2, 3, 2>, kExact>(p, s);
-    else if (kind == 3) launch<Tile<128, 64, 4, 2, 3, 1>, kExact>(p, s);
-    else if constexpr (kExact) kind == 4 ? launch<Tile<128, 128, 2, 2, 2, 1>, true>(p, s)
-                                         : launch<Tile<256, 128, 4, 2, 3, 1>, true>(p, s);
-    else if (kind == 4) launch<Tile<128, 128, 2, 4, 3, 1>, false>(p, s);
-    else
+    else if (kind == 3) alone ? launch<Tile<128, 64, 4, 2, 3, 2>, kExact>(p, s) : launch<Tile<128, 64, 4, 2, 3, 1>, kExact>(p, s);
+    else if (kind == 4) launch<Tile<128, 128, 2, kExact ? 2 : 4, kExact ? 2 : 3, 1>, kExact>(p, s);
+    else if (kind == 5) launch<Tile<256, 128, 4, 2, 3, 1>, kExact>(p, s);
+    else if constexpr (!kExact)
         hipLaunchKernelGGL(gemm_fp8_big_kernel<Big>, dim3(tile_grid(cdiv(p.rows, Big::kBm), cdiv(p.tokens, Big::kBn))),
                            dim3(Big::kThreads), 0, s, p);
 }

@@ -44,6 +44,13 @@ __device__ __forceinline__ void copy_to_lds(uint32_t to, const u32x4& rsrc, uint
                  : "memory", "m0");
 }
 
+// The same past the caches, for what is read once.
+__device__ __forceinline__ void copy_once_to_lds(uint32_t to, const u32x4& rsrc, uint32_t offset, uint32_t uniform) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds" ::"s"(to), "v"(offset),
+                 "s"(rsrc), "s"(uniform)
+                 : "memory", "m0");
+}
+
 // The same with 4 bytes per lane.
 __device__ __forceinline__ void copy_words_to_lds(uint32_t to, const u32x4& rsrc, uint32_t offset) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(to), "v"(offset),
