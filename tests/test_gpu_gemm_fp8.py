@@ -65,8 +65,15 @@ TILES = [(1304, 2704, 90), (1003, 2096, 333), (1027, 1040, 515), (1001, 4112, 10
          (4096, 14336, 128), (8192, 4112, 16), (8209, 4112, 31), (9001, 1296, 5)]
 
 
+# a matrix that one tile of tokens reads once, whose tiles and groups begin at different blocks of columns; groups of 16, 32
+# and 64 rows on either side of where they are taken
+ONCE = [(12000, 144, 60), (16400, 272, 100), (28672, 272, 60), (28673, 400, 64), (9000, 2064, 50), (14337, 400, 509),
+        (4096, 400, 3), (4097, 1168, 16), (10239, 272, 16), (10240, 400, 5), (10241, 1296, 16), (16384, 272, 1), (16385, 272, 16),
+        (10250, 400, 32), (4100, 272, 17)]
+
+
 @pytest.mark.parametrize("out", ["bf16", "f32"])
-@pytest.mark.parametrize("rows,cols,tokens", TILES)
+@pytest.mark.parametrize("rows,cols,tokens", TILES + ONCE)
 def test_tiles(wc, rows, cols, tokens, out):
     codes, scales, w, xc, xs, x = _case(rows, cols, tokens, rows)
     log(f"case: gemm_fp8 {rows}x{cols}, {tokens} tokens, {out}")
