@@ -158,6 +158,7 @@ def test_gradient(wc, n, dim, dsum):
         wc.rms_norm_grad_async(names["dy"], names["h"], wd, rstd, n, dim, into, dw, work, work.numel(),
                                dsum_dev=names["ds"])
         assert torch.equal(into, dh)
+        assert within(dw, want_dw, tol_dw)
 
 
 def test_gradient_by_differences(wc):
