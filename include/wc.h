@@ -437,8 +437,9 @@ int wc_ce_grad_async(const uint16_t* h, const uint16_t* W, const void* targets, 
  *
  * wc_quant_fp8_async -- rows of activations to such codes.  With a the largest
  * magnitude of a row's block,
- *   scale = max(a, 2^-100) / 448,   code = y / scale, rounded to nearest even;
- * a block that holds an infinity or a NaN gets the scale NaN.  One launch.
+ *   scale = max(a, 2^-100) * (1 / 448),   code = y / scale,
+ * each rounded to fp32 (1 / 448 too), the code then to e4m3, to nearest even; a
+ * block that holds an infinity or a NaN gets the scale NaN.  One launch.
  *   x       device, 16-byte aligned bf16, dim a multiple of 8; gated 0: n x dim,
  *           y = x; else n x 2 dim, each row gate and then up:
  *           y = silu(gate) up = gate / (1 + exp(-gate)) up, in fp32 (0 where

@@ -69,15 +69,25 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // Codes of a block whose 128 columns lie in a row of 16 lanes, 8 in each (lanes past the row's end hold zeros):
-//   scale = max(largest |y|, 2^-100) / 448,   code = y / scale rounded to e4m3 (to nearest, ties to even).
-// The largest value becomes 448, the largest code, within a rounding of fp32 that e4m3's absorbs, so no code
-// overflows; the lower bound keeps the quotient of a block of zeros, or of values near fp32's end, finite.  Compared
-// as words without their signs, infinities and NaNs are larger than any number: a block that has one gets the scale
-// NaN, so that all its values are.
+//   scale = max(largest |y|, 2^-100) * (1 / 448),   code = y / scale,
+// each in fp32 (1 / 448 too), the quotient then rounded to e4m3 (to nearest, ties to even).
+// The largest value becomes 448, the largest code, within roundings of fp32 that e4m3's absorbs, so no code overflows;
+// the lower bound keeps the quotient of a block of zeros, or of values near fp32's end, finite.  Compared as words without
+// their signs, infinities and NaNs are larger than any number: a block that has one gets the scale NaN, so that all its
+// values are.
 struct BlockCodes {
     u32x2 codes;
     float scale;
 };
+// y / scale, from 1 / scale rounded to nearest: the product, and what its remainder adds.  A quotient next to a border of
+// two codes is on the right side of it (compared with the quotient in double precision, for every mantissa of the scale
+// and each y near a border); the product alone is not, for one pair of bf16 mantissas in some thousands, and saves no time
+// (8192 x 28672, gated, us: 184, and 182 so).  The remainder must not leave fp32's range: scales of at least 2^-64.  Zeros
+// keep their signs.
+__device__ __forceinline__ float quotient(float y, float scale, float inverse) {
+    const float q = y * inverse;
+    return __builtin_fmaf(-__builtin_fmaf(q, scale, -y), inverse, q);
+}
 __device__ __forceinline__ BlockCodes block_codes(const float (&y)[8]) {
     uint32_t top = 0;
 #pragma unroll
@@ -89,12 +99,23 @@ __device__ __forceinline__ BlockCodes block_codes(const float (&y)[8]) {
     const float largest = top < 0x7F800000u ? __uint_as_float(max(top, 0x0D800000u)) : NAN;   // 2^-100
     BlockCodes b;
     b.scale = largest * (1.0f / 448.0f);
-    const float inverse = __builtin_amdgcn_rcpf(b.scale);   // within 2^-23; between 2^-120 and 2^109
+    float v[8], scale = b.scale;
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) v[i] = y[i];
+    if (__any(largest < 0x1p-50f)) {   // small ones are lifted, both operands, so that remainders stay in range
+        const float lift = largest < 0x1p-50f ? 0x1p60f : 1.0f;
+        scale *= lift;
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) v[i] *= lift;
+    }
+    const float inverse = 1.0f / scale;
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) v[i] = quotient(v[i], scale, inverse);
 #pragma unroll
     for (uint32_t i = 0; i < 2; ++i) {
         int w = 0;
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i] * inverse, y[4 * i + 1] * inverse, w, false);
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2] * inverse, y[4 * i + 3] * inverse, w, true);
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i], v[4 * i + 1], w, false);
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2], v[4 * i + 3], w, true);
         b.codes[i] = (uint32_t)w;
     }
     return b;

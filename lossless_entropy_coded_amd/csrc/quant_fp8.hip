@@ -8,8 +8,8 @@
 // The kernel moves bytes: a lane takes 8 columns, so that a row of 16 lanes has
 // a block and its largest value comes from four lane exchanges; a wave takes 512
 // columns of one row.  Rows past the 256 MB cache are read and written past the
-// caches.  8192 x 28672, gated (1.18 GB), us: 184, which is the rate of a large copy
-// (6.4 TB/s); 194 with two or four times 512 columns per wave; two times 512 and
+// caches.  8192 x 28672, gated (1.18 GB), us: 182, which is the rate of a large copy
+// (6.5 TB/s); 194 with two or four times 512 columns per wave; two times 512 and
 // plain loads and stores: 211.
 #include <hip/hip_runtime.h>
 
