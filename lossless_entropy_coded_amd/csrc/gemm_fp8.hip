@@ -25,6 +25,7 @@
 
 #include "../../include/wc.h"
 #include "e4m3.h"
+#include "gemm_fp8_plan.h"
 #include "lds_copy.h"
 
 namespace wc {
@@ -161,9 +162,6 @@ __device__ __forceinline__ bool tile_of(uint32_t id, uint32_t ms, uint32_t ns, u
     return true;
 }
 uint32_t tile_grid(uint32_t ms, uint32_t ns) { return (ms * ns + kDies - 1) / kDies * kDies; }
-
-// Elements of one split's sums: they begin on 16 bytes.
-__host__ __device__ __forceinline__ uint64_t split_elems(uint64_t tokens, uint32_t rows) { return (tokens * rows + 3) / 4 * 4; }
 
 // Four neighbouring results of a token, those past the last row left out.
 __device__ __forceinline__ void store4(void* y, uint32_t kind, uint64_t at, uint32_t left, const f32x4& v) {
@@ -620,121 +618,43 @@ __global__ __launch_bounds__(256) void gemm_fp8_join_kernel(GemmParams p) {
     store4(p.y, p.out_kind, i, n - i < 4 ? (uint32_t)(n - i) : 4, v);
 }
 
-uint32_t cdiv(uint64_t a, uint32_t b) { return (uint32_t)((a + b - 1) / b); }
-
-using Big = Tile<256, 256, 2, 4, 2, 1>;
-constexpr uint32_t kCus = 256;
-constexpr uint32_t kFewTokens = 32;
-
-// Tiles and splits of more tokens are those that a model of the time likes best.  It knows what a tile takes per block of
-// columns: a CU takes in about 40 bytes per ns, whatever the tile (measured: 36 to 41 with operands past the L2 cache, from
-// 32 x 32 to 256 x 256), or, where codes are made bf16, up to half of that, as the products then bound it; a workgroup's
-// start and end, 3 us; and for joining splits a launch of 2.5 us and their sums, written and read at 4 TB/s.  Few and small
-// tiles leave CUs idle, large ones re-read the least.  Measured (us, tile:splits; * what the model takes):
-//                                32x32   32x64   64x64     128x64    128x128   256x128   256x256
-//    64 tokens x 4096 x 4096       7.6*   12.7    12.8       -         -         -         -
-//   128 x 4096 x 4096             13.1     9.3*   10.8      14.2:2     -         -         -
-//   256 x 4096 x 4096              -      16.4    11.3*     15.2      17.7:4     -         -
-//    64 x 28672 x 8192             -       -      61.2      49.1*     49.7      63.5:2     -
-//   128 x 4096 x 14336             -       -       -        28.3:4    28.7:8*   29.0:16    -
-//   128 x 8192 x 28672             -       -       -        86.3:2    69.4:4*   61.9:8     -
-//   128 x 28672 x 8192             -       -       -        82.2      62.3*     69.1:2     -
-//   512 x 4096 x 4096              -       -      20.0      16.4*     22.0       -         -
-//   512 x 14336 x 4096             -       -      94.2      62.6      57.5      45.9*     58.9
-//  1000 x 8192 x 8192              -       -       -         122       101      82.6*      105
-//  1024 x 14336 x 4096             -       -       -         110       103      78.9      63.8*
-//  5000 x 300 x 9008 fp32          -       -       -        52.0*     52.8:4    72.5:2
-//   512 x 14336 x 4096 fp32        -       161     104      82.1      70.9      65.2*
-//  1024 x 4096 x 4096 fp32         -       -      56.9      45.0*     54.9      48.3:2
-struct Kind {
-    uint32_t bm, bn, per_cu;   // workgroups per CU (LDS)
-    double us;                 // per block of columns
-};
-constexpr uint32_t kKinds = 7, kBig = kKinds - 1;   // the last of codes alone, and without splits
-constexpr Kind kCodeKinds[kKinds] = {{32, 32, 1, 0.2}, {32, 64, 1, 0.3}, {64, 64, 1, 0.4}, {128, 64, 2, 0.6},
-                                     {128, 128, 1, 0.8}, {256, 128, 1, 1.4}, {256, 256, 1, 1.6}};
-constexpr Kind kExactKinds[kBig] = {{32, 32, 1, 0.26}, {32, 64, 1, 0.4}, {64, 64, 1, 0.42}, {128, 64, 2, 0.65},
-                                    {128, 128, 2, 1.35}, {256, 128, 1, 2.0}};
-
-struct GemmPlan {
-    uint32_t kind, splits, split_blocks;
-    uint64_t work_bytes;
-};
-GemmPlan plan_of(uint32_t rows, uint32_t cols, uint64_t tokens, bool exact) {
-    const uint32_t blocks = cdiv(cols, kBlockCols);
-    GemmPlan best{0, 1, blocks, 0};
-    if (tokens <= kFewTokens) return best;
-    double best_us = 1e300;
-    for (uint32_t k = 0; k < (exact ? kBig : kKinds); ++k) {
-        const Kind& kind = exact ? kExactKinds[k] : kCodeKinds[k];
-        const uint64_t tiles = (uint64_t)cdiv(rows, kind.bm) * cdiv(tokens, kind.bn);
-        for (uint32_t s = 1; s <= 16; s *= 2) {
-            if (s > 1 && (k == kBig || blocks < 8 * s || tiles * s > kCus * kind.per_cu)) break;
-            const uint32_t per = cdiv(blocks, s);
-            const uint64_t groups = tiles * s;
-            const double us = 3.0 * (double)((groups + kCus * kind.per_cu - 1) / (kCus * kind.per_cu)) +
-                              (double)((groups + kCus - 1) / kCus) * per * kind.us +
-                              (s > 1 ? 2.5 + (double)s * (double)tokens * rows * 8 / 4e6 : 0.0);
-            if (us < best_us) best_us = us, best = {k, cdiv(blocks, per), per, 0};
-        }
-    }
-    best.work_bytes = best.splits > 1 ? best.splits * split_elems(tokens, rows) * 4 : 0;
-    return best;
-}
-
 template <class F>
 void launch_few(const GemmParams& p, uint32_t waves, hipStream_t s) {
     hipLaunchKernelGGL((gemm_fp8_few_kernel<F>), dim3(cdiv(p.rows, 16 * F::kMi)), dim3(64 * waves), waves * F::kWaveBytes, s,
                        p);
 }
 
-// Rows of a group of few tokens, and its waves and stages (us): past 4096 rows there are groups enough of 32 rows, which
-// share the work on the tokens; from 10240 to 16384 rows groups of 64, one per CU, are all in work at once.
-//                          16 rows, 8 waves   32 rows, 4 waves   64 rows, 4 waves
-//    1 token  x 1024 x 4096        4.8               5.9                8.4
-//    8 tokens x 4096 x 14336      12.3              16.0               24.8
-//    1 x 4608 x 8192              12.1               9.4               14.3
-//   16 x 10240 x 8192             20.4              21.0               17.9
-//   16 x 14336 x 4096             15.9              13.2               12.3
-//   16 x 16384 x 8192             29.7              24.4               23.6
-//   16 x 24576 x 8192             44.9              36.3               42.4
-//   16 x 57344 x 8192             98.3              80.8               85.4
-// 17 to 32 tokens: 16 and 32 rows, 4 waves of 2 stages: 24 x 1024 x 4096 6.6 and 8.0, 32 x 4096 x 14336 19.2 and 24.5, 32 x
-// 5120 x 8192 19.6 and 14.7, 32 x 28672 x 8192 69 and 52.
-constexpr uint32_t kNarrowRows = 4096, kTallFrom = 10240, kTallRows = 16384;
-void launch_few_tokens(const GemmParams& p, hipStream_t s) {
-    const bool narrow = p.rows <= kNarrowRows, tall = p.rows >= kTallFrom && p.rows <= kTallRows;
-    if (p.tokens > 16) narrow ? launch_few<Few<1, 2, 2>>(p, 4, s) : launch_few<Few<2, 2, 2>>(p, 4, s);
-    else if (narrow) launch_few<Few<1, 1, 2>>(p, 8, s);
-    else if (tall) launch_few<Few<4, 1, 2>>(p, 4, s);
-    else launch_few<Few<2, 1, 3>>(p, 4, s);
+void launch_few_tokens(uint32_t kind, const GemmParams& p, hipStream_t s) {
+    if (kind == kFew16) launch_few<Few<1, 1, 2>>(p, 8, s);
+    else if (kind == kFew32) launch_few<Few<2, 1, 3>>(p, 4, s);
+    else if (kind == kFew64) launch_few<Few<4, 1, 2>>(p, 4, s);
+    else if (kind == kFewPairs16) launch_few<Few<1, 2, 2>>(p, 4, s);
+    else launch_few<Few<2, 2, 2>>(p, 4, s);
 }
 
-// A matrix that one tile of tokens takes whole is read once, and past the caches (us, and through them): 64 tokens x 28672 x
-// 8192 52.7 and 59.2, 128 tokens 62.9 and 68.7, 64 tokens x 14336 x 4096 17.9 and 19.6; not if two do: 128 tokens x 4096 x
-// 14336 in tiles of 64, 28.3 and 26.3.
-template <class T, bool kExact>
-void launch(const GemmParams& p, hipStream_t s) {
+template <class T, bool kExact, bool kMayBeOnce>
+void launch(const GemmPlan& g, const GemmParams& p, hipStream_t s) {
     const dim3 grid(tile_grid(cdiv(p.rows, T::kBm), cdiv(p.tokens, T::kBn)), p.splits);
-    if constexpr (T::kBn > kFewTokens)
-        if (p.tokens <= T::kBn) {
+    if constexpr (kMayBeOnce)
+        if (g.once) {
             hipLaunchKernelGGL((gemm_fp8_tile_kernel<T, kExact, true>), grid, dim3(T::kThreads), 0, s, p);
             return;
         }
     hipLaunchKernelGGL((gemm_fp8_tile_kernel<T, kExact, false>), grid, dim3(T::kThreads), 0, s, p);
 }
 
-// Waves, stages and groups of each kind as they measured best.  128 x 64 where no CU has two workgroups: two groups of
-// waves, so that as much is on its way (64 tokens x 28672 x 8192, us: 48.7, and 56.3 with one).
+using Big = Tile<256, 256, 2, 4, 2, 1>;
+
+// Waves, stages and groups of each kind as they measured best.
 template <bool kExact>
-void launch_tiles(uint32_t kind, const GemmParams& p, hipStream_t s) {
-    const bool alone = kind == 3 && cdiv(p.rows, 128) * (uint64_t)cdiv(p.tokens, 64) * p.splits <= kCus;
-    if (kind == 0) launch<Tile<32, 32, 2, 2, 4, 4>, kExact>(p, s);
-    else if (kind == 1) launch<Tile<32, 64, 2, 2, 4, 2>, kExact>(p, s);
-    else if (kind == 2) launch<Tile<64, 64, 2, 2, 3, 2>, kExact>(p, s);
-    else if (kind == 3) alone ? launch<Tile<128, 64, 4, 2, 3, 2>, kExact>(p, s) : launch<Tile<128, 64, 4, 2, 3, 1>, kExact>(p, s);
-    else if (kind == 4) launch<Tile<128, 128, 2, kExact ? 2 : 4, kExact ? 2 : 3, 1>, kExact>(p, s);
-    else if (kind == 5) launch<Tile<256, 128, 4, 2, 3, 1>, kExact>(p, s);
+void launch_tiles(const GemmPlan& g, const GemmParams& p, hipStream_t s) {
+    if (g.kind == 0) launch<Tile<32, 32, 2, 2, 4, 4>, kExact, false>(g, p, s);
+    else if (g.kind == 1) launch<Tile<32, 64, 2, 2, 4, 2>, kExact, true>(g, p, s);
+    else if (g.kind == 2) launch<Tile<64, 64, 2, 2, 3, 2>, kExact, true>(g, p, s);
+    else if (g.kind == kHalf && g.pair) launch<Tile<128, 64, 4, 2, 3, 2>, kExact, true>(g, p, s);
+    else if (g.kind == kHalf) launch<Tile<128, 64, 4, 2, 3, 1>, kExact, true>(g, p, s);
+    else if (g.kind == kSquare) launch<Tile<128, 128, 2, kExact ? 2 : 4, kExact ? 2 : 3, 1>, kExact, !kExact>(g, p, s);
+    else if (g.kind == 5) launch<Tile<256, 128, 4, 2, 3, 1>, kExact, true>(g, p, s);
     else if constexpr (!kExact)
         hipLaunchKernelGGL(gemm_fp8_big_kernel<Big>, dim3(tile_grid(cdiv(p.rows, Big::kBm), cdiv(p.tokens, Big::kBn))),
                            dim3(Big::kThreads), 0, s, p);
@@ -784,9 +704,9 @@ extern "C" int wc_gemm_fp8_async(const wc_fp8_matrix* W, const uint8_t* x_codes,
     p.rows = W->rows, p.cols = W->cols, p.tokens = (uint32_t)tokens, p.blocks = cdiv(W->cols, kBlockCols);
     p.split_blocks = g.split_blocks, p.splits = g.splits, p.out_kind = out_kind;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    if (tokens <= kFewTokens) launch_few_tokens(p, s);
-    else if (exact) launch_tiles<true>(g.kind, p, s);
-    else launch_tiles<false>(g.kind, p, s);
+    if (g.few) launch_few_tokens(g.kind, p, s);
+    else if (exact) launch_tiles<true>(g, p, s);
+    else launch_tiles<false>(g, p, s);
     if (g.splits > 1) {
         const uint32_t groups = cdiv((uint64_t)p.tokens * p.rows, 1024);
         hipLaunchKernelGGL(gemm_fp8_join_kernel, dim3(groups), dim3(256), 0, s, p);
