@@ -36,6 +36,7 @@
 
 #include "../../include/wc.h"
 #include "lds_copy.h"
+#include "tiles.h"
 
 namespace wc {
 namespace {
@@ -326,23 +327,6 @@ __device__ __forceinline__ void store_rows(uint16_t* lds, uint16_t* out, uint64_
                 *reinterpret_cast<const u32x4*>(lds + n * T::kBm + ((c ^ (n & (kChunks - 1))) * 8));
     }
 }
-
-// Which tile a workgroup takes.  Workgroups go to the 8 dies in turn: each die
-// gets a contiguous run of tiles (its L2 is its own), and within a run 4 tiles
-// of m go with each tile of n, so that the tiles in work at one time share
-// operands both ways.
-constexpr uint32_t kDies = 8;
-__device__ __forceinline__ bool tile_of(uint32_t id, uint32_t ms, uint32_t ns, uint32_t& m, uint32_t& n) {
-    const uint32_t total = ms * ns, per = (total + 7) / 8, t = id % 8 * per + id / 8;
-    if (id / 8 >= per || t >= total) return false;
-    constexpr uint32_t kBand = 4;
-    const uint32_t band = t / (kBand * ns), left = ms - band * kBand, width = left < kBand ? left : kBand;
-    const uint32_t in = t - band * kBand * ns;
-    m = band * kBand + in % width;
-    n = in / width;
-    return true;
-}
-uint32_t tile_grid(uint32_t ms, uint32_t ns) { return (ms * ns + 7) / 8 * 8; }
 
 struct CeParams {
     const uint16_t* h;
@@ -746,8 +730,6 @@ using Thin = Tile<kAx, kBx, 256, 64, 4, 1, 3, 64>;     // few tokens: bound by r
 constexpr uint32_t kThinTokens = 64;
 constexpr uint32_t kCus = 256;
 constexpr uint32_t kRestTokens = 128;   // up to these, what d loses is kept (see above)
-
-uint32_t cdiv(uint64_t a, uint32_t b) { return (uint32_t)((a + b - 1) / b); }
 
 // z of few tokens takes thin tiles where the vocabulary has enough of them to
 // keep the memory busy (z, thin and mid, us: 16 x 131072 x 4096 190 and 204; 64

@@ -27,6 +27,7 @@
 #include "e4m3.h"
 #include "gemm_fp8_plan.h"
 #include "lds_copy.h"
+#include "tiles.h"
 
 namespace wc {
 namespace {
@@ -146,22 +147,6 @@ struct Tile {
     static constexpr uint32_t kLdsBytes = kScalesAt + kStages * kGroups * kScaleBytes;
     static_assert(kWaveN <= 64 && kBlockCols % kWaveM == 0 && kLdsBytes <= 160 * 1024, "shape");
 };
-
-constexpr uint32_t kDies = 8;
-// Which tile a workgroup takes.  Workgroups go to the 8 dies in turn: each die gets a contiguous run of tiles (its L2
-// is its own), and within a run 4 tiles of rows go with each tile of tokens, so that the tiles in work at one time
-// share operands both ways.
-__device__ __forceinline__ bool tile_of(uint32_t id, uint32_t ms, uint32_t ns, uint32_t& m, uint32_t& n) {
-    const uint32_t total = ms * ns, per = (total + kDies - 1) / kDies, t = id % kDies * per + id / kDies;
-    if (id / kDies >= per || t >= total) return false;
-    constexpr uint32_t kBand = 4;
-    const uint32_t band = t / (kBand * ns), left = ms - band * kBand, width = left < kBand ? left : kBand;
-    const uint32_t in = t - band * kBand * ns;
-    m = band * kBand + in % width;
-    n = in / width;
-    return true;
-}
-uint32_t tile_grid(uint32_t ms, uint32_t ns) { return (ms * ns + kDies - 1) / kDies * kDies; }
 
 // Four neighbouring results of a token, those past the last row left out.
 __device__ __forceinline__ void store4(void* y, uint32_t kind, uint64_t at, uint32_t left, const f32x4& v) {

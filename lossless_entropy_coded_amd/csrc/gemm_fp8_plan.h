@@ -6,10 +6,9 @@
 #include <cstdint>
 
 #include "../../include/wc.h"
+#include "tiles.h"
 
 namespace wc {
-
-constexpr uint32_t cdiv(uint64_t a, uint32_t b) { return (uint32_t)((a + b - 1) / b); }
 
 // Elements of one split's sums: they begin on 16 bytes.
 constexpr uint64_t split_elems(uint64_t tokens, uint32_t rows) { return (tokens * rows + 3) / 4 * 4; }
