@@ -171,7 +171,9 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(Params p) {
     const float norm = (float)total;
     if (p.norm && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = norm;
     const bool clips = norm > p.max_norm && norm < INFINITY;
-    const float factor = clips ? (float)((double)p.max_norm / total) : 1.0f;
+    // a quotient below fp32's normal range, of which few bits would be left, is multiplied by in two steps
+    const double quotient = (double)p.max_norm / total;
+    const float last = quotient < 0x1p-100 ? 0x1p-126f : 1.0f, factor = (float)(quotient / last);
     if (!any || (!clips && t.g == t.out)) return;
     if (kStream) load_chunk<true>(t, c, w);
     u32x4* const out = static_cast<u32x4*>(t.out) + c.wide;
@@ -182,19 +184,20 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(Params p) {
         if (clips) {
 #pragma unroll
             for (uint32_t e = 0; e < 4; ++e)
-                w[k][e] = t.kind == WC_OUT_F32 ? __float_as_uint(__uint_as_float(w[k][e]) * factor)
-                                               : pack_bf16(bf16_lo(w[k][e]) * factor, bf16_hi(w[k][e]) * factor);
+                w[k][e] = t.kind == WC_OUT_F32
+                              ? __float_as_uint(__uint_as_float(w[k][e]) * factor * last)
+                              : pack_bf16(bf16_lo(w[k][e]) * factor * last, bf16_hi(w[k][e]) * factor * last);
         }
         store16<kStream>(out + i, w[k]);
     }
     for (uint32_t i = c.lanes * c.per_lane + threadIdx.x; i < c.count; i += kThreads) {
         if (t.kind == WC_OUT_F32) {
             const float v = static_cast<const float*>(t.g)[c.begin + i];
-            static_cast<float*>(t.out)[c.begin + i] = clips ? v * factor : v;
+            static_cast<float*>(t.out)[c.begin + i] = clips ? v * factor * last : v;
         } else {
             const uint16_t v = static_cast<const uint16_t*>(t.g)[c.begin + i];
             static_cast<uint16_t*>(t.out)[c.begin + i] =
-                clips ? (uint16_t)pack_bf16(__uint_as_float((uint32_t)v << 16) * factor, 0.0f) : v;
+                clips ? (uint16_t)pack_bf16(__uint_as_float((uint32_t)v << 16) * factor * last, 0.0f) : v;
         }
     }
 }
