@@ -466,9 +466,10 @@ int wc_quant_fp8_async(const uint16_t* x, uint64_t n, uint32_t dim, int gated, u
  *             (y or codes must be given);
  *   rstd      device, n float32 (written): r, for the gradient; or NULL.
  * bf16 tensors and codes are 16-byte aligned.  sum may be x or residual itself,
- * y may be x itself; no other output may overlap an input or another output.
- * eps is at least 0.  n == 0 is a no-op.  Squares are summed in fp32: a row whose
- * sum of squares leaves its range has r = 0.
+ * and y may be x itself where sum is not; no other output may overlap an input or
+ * another output.  eps is at least 0.  n == 0 is a no-op.  Squares are summed in
+ * fp32: a row whose sum of squares leaves its range has r = 0, one whose squares
+ * are below it r = 1 / sqrt(eps).
  */
 int wc_rms_norm_async(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, uint64_t n, uint32_t dim,
                       float eps, uint16_t* sum, uint16_t* y, uint8_t* codes, float* scales, float* rstd, void* stream);

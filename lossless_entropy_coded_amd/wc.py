@@ -758,9 +758,12 @@ def rms_norm_async(x_dev, weight_dev, n: int, dim: int, eps: float, y_dev=None, 
     which goes to sum_dev; one launch.
 
     y goes to y_dev (bf16), to codes_dev and scales_dev (as quant_fp8_async writes them), or to both; rstd_dev (n
-    float32), if given, keeps rstd for the gradient."""
+    float32), if given, keeps rstd for the gradient.  sum_dev may be x_dev or residual_dev, and y_dev may be x_dev, but
+    not both the same tensor."""
     call = "wc_rms_norm_async"
     dev = _current_device()
+    if y_dev is not None and y_dev is sum_dev:
+        raise WCError(WC_ERR_INVALID_ARG, call, "y and sum are the same tensor")
     if (n | dim) >> 32:
         _sizes(call, n=n, dim=dim)
     wide = 2 * n * dim
