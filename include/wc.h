@@ -434,6 +434,8 @@ int wc_ce_grad_async(const uint16_t* h, const uint16_t* W, const void* targets, 
  * Codes in 8-bit floating point: e4m3 bytes (OCP: no infinities, 0x7F and 0xFF
  * NaN, largest value 448), one fp32 scale per block of WC_FP8_BLOCK columns
  * (the last block of a row may be shorter); a code stands for scale * code.
+ * In this call and those below, what is written (workspaces too) overlaps
+ * neither what is read nor what else is written, but where it is said to.
  *
  * wc_quant_fp8_async -- rows of activations to such codes.  With a the largest
  * magnitude of a row's block,
@@ -522,7 +524,9 @@ int wc_fp8_check(const wc_fp8_matrix* W);
  * sums are fp32 in a fixed order that depends on the sizes alone, so y is the
  * same bits on every run.  bf16 results of more than 32 tokens come of the 8-bit
  * matrix instructions, which sum eight neighbouring products at a time and drop
- * what lies below 2^-14 of the largest of them; fp32 results, and those of up to
+ * what lies below 2^-14 of the largest of them: where large products cancel, what
+ * remains may be off by more than its rounding to bf16, and a token's result may
+ * differ between calls of 32 and of 33 tokens.  fp32 results, and those of up to
  * 32 tokens, keep every product.  At most two launches.
  *   x_codes   device, tokens x cols e4m3, 16-byte aligned;
  *   x_scales  device, tokens x ceil(cols / 128) float32 (both as

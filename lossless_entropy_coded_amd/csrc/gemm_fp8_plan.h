@@ -17,17 +17,19 @@ constexpr uint32_t kCus = 256;
 constexpr uint32_t kFewTokens = 32;
 
 // Tiles and splits of more tokens are those that a model of the time likes best.  It knows what a tile takes per block of
-// columns: a CU takes in about 40 bytes per ns, whatever the tile (measured: 36 to 41 with operands past the L2 cache, from
-// 32 x 32 to 256 x 256), or, where codes are made bf16, up to half of that, as the products then bound it; a workgroup's
-// start and end, 3 us; and for joining splits a launch of 2.5 us and their sums, written and read at 4 TB/s.  Few and small
-// tiles leave CUs idle, large ones re-read the least.  Measured (us, tile:splits; * what the model takes):
+// columns, which is fitted to the times below: 36 to 41 bytes per ns and CU from 32 x 32 to 256 x 256, or, where codes are
+// made bf16, down to half of that.  (No unit is at its limit there: of 256 tokens x 28672 x 8192 the matrix cores are busy
+// 26% of the time and memory gives 3.0 TB/s.  A tile's copies, reads from LDS and products wait for one another: 94 us, of
+// columns that stay in L2 74, without copies 62.)  It adds a workgroup's start and end, 3 us, and for joining splits a launch
+// of 2.5 us and their sums, written and read at 4 TB/s.  Few and small tiles leave CUs idle, large ones re-read the least.
+// Measured (us, tile:splits; * what the model takes):
 //                                32x32   32x64   64x64     128x64    128x128   256x128   256x256
 //    64 tokens x 4096 x 4096       7.6*   12.7    12.8       -         -         -         -
 //   128 x 4096 x 4096             13.1     9.3*   10.8      14.2:2     -         -         -
 //   256 x 4096 x 4096              -      16.4    11.3*     15.2      17.7:4     -         -
 //    64 x 28672 x 8192             -       -      61.2      49.1*     49.7      63.5:2     -
 //   128 x 4096 x 14336             -       -       -        28.3:4    28.7:8*   29.0:16    -
-//   128 x 8192 x 28672             -       -       -        86.3:2    69.4:4*   61.9:8     -
+//   128 x 8192 x 28672             -       -       -        86.3:2    69.4:4*   61.9:8     -     (the model is wrong here)
 //   128 x 28672 x 8192             -       -       -        82.2      62.3*     69.1:2     -
 //   512 x 4096 x 4096              -       -      20.0      16.4*     22.0       -         -
 //   512 x 14336 x 4096             -       -      94.2      62.6      57.5      45.9*     58.9

@@ -870,7 +870,10 @@ def gemm_fp8_async(W: Fp8Matrix, x_codes_dev, x_scales_dev, tokens: int, y_dev, 
 class GradList:
     """A list of gradients for clip_grads_async (kept alive by this handle): float32 or bf16 device tensors, and where the
     clipped ones go (outs: tensors of the same sizes and types, any of them the gradient itself; None: all in place).
-    No output may overlap another tensor of the list."""
+    No output may overlap another tensor of the list.
+
+    Each tensor's type, device, size and place is looked at here and no more in the calls: about 2 us per tensor (291 of
+    them 0.54 ms).  Keep the handle while the tensors stay where they are."""
 
     def __init__(self, grads, outs=None):
         call = "wc_clip_grads_async"
